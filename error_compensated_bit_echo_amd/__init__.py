@@ -12,7 +12,7 @@ _BINDING_NAMES = {
     "echo_owner", "echo_decode", "echo_gemm_stage1", "echo_gemm_bf16", "echo_reset", "echo_destroy_state",
     "echo_reduce_noalloc", "ECHO_STATIC_SCRATCH_BYTES",
     "echo_wire_bytes", "echo_debug_views", "echo_status_str", "library_path",
-    "load_library",
+    "load_library", "EchoFp8", "echo_quantize_fp8", "echo_gemm_fp8", "echo_dropout_add",
 }
 
 

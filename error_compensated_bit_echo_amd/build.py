@@ -17,8 +17,10 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libecho.so")
 SOURCES = ["echo_kernels.hip"] + [f"echo_owner_p{lo}_{lo + 1}.hip" for lo in range(1, 17, 2)] + \
-    ["echo_gemm.hip", "echo_scratch.hip", "echo_api.hip"]
-HEADERS = ["echo_internal.h", "echo_div7.h", "echo_quant.h", "echo_device.h", "echo_owner.h"]
+    ["echo_gemm.hip", "echo_scratch.hip", "echo_api.hip",
+     "echo_fp8_quant.hip", "echo_fp8_gemm.hip", "echo_dropout.hip", "echo_layer_api.hip"]
+HEADERS = ["echo_internal.h", "echo_div7.h", "echo_quant.h", "echo_device.h", "echo_owner.h",
+           "echo_layer_internal.h", "echo_elem.h", "echo_slab.h"]
 ARCH = "gfx950"
 
 # -ffp-contract=off: every multiply and add is its own IEEE operation (the

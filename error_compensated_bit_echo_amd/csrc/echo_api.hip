@@ -511,7 +511,8 @@ const char* echo_status_str(echo_status s) {
     case ECHO_OK: return "ok";
     case ECHO_ERR_ARG: return "invalid argument (null, misaligned or overlapping pointer, bad enum)";
     case ECHO_ERR_SHAPE:
-      return "invalid shape (P outside [1,16], group not 32/64/128, numel not a multiple of the group or too large)";
+      return "invalid shape (P outside [1,16], group not 32/64/128, numel not a multiple of the group or too large; "
+             "a size, pitch or stride outside the operator's limits)";
     case ECHO_ERR_DTYPE: return "invalid dtype";
     case ECHO_ERR_WORKSPACE:
       return "workspace missing or too small (echo_reduce_noalloc: the payloads exceed the static scratch)";

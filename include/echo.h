@@ -75,14 +75,16 @@ extern "C" {
 typedef enum {
   ECHO_OK = 0,
   ECHO_ERR_ARG = 1,       /* null / misaligned / overlapping pointer, bad enum   */
-  ECHO_ERR_SHAPE = 2,     /* P outside [1,16], group not 32/64/128, numel % group != 0 or too large */
+  ECHO_ERR_SHAPE = 2,     /* P outside [1,16], group not 32/64/128, numel % group != 0 or too large; */
+                          /* a size, row pitch or stride outside an operator's limits     */
   ECHO_ERR_DTYPE = 3,     /* unknown dtype                                        */
   ECHO_ERR_WORKSPACE = 4, /* workspace missing or smaller than echo_workspace_bytes */
   ECHO_ERR_STATE = 5,     /* null state, or called with another device current   */
   ECHO_ERR_HIP = 6        /* a HIP runtime call or a kernel launch failed         */
 } echo_status;
 
-typedef enum { ECHO_F32 = 0, ECHO_BF16 = 1 } echo_dtype;
+/* ECHO_F16 is taken by the operators of the layer around the all-reduce only */
+typedef enum { ECHO_F32 = 0, ECHO_BF16 = 1, ECHO_F16 = 2 } echo_dtype;
 typedef enum { ECHO_FWD = 0, ECHO_BWD = 1 } echo_dir;
 
 #define ECHO_MAX_RANKS 16
@@ -295,6 +297,113 @@ typedef struct {
 } echo_views;
 
 echo_status echo_debug_views(const echo_state* st, echo_dir dir, echo_views* out);
+
+/* ---- operators of the layer around the all-reduce -------------------------
+ * The products whose partial results the all-reduce adds, in 8-bit floating
+ * point, with their quantizer, and the dropout between the reduced result and
+ * the residual stream.  They use no state: every device pointer is on the
+ * device that is current at the call, all ranks' matrices have the same sizes
+ * and strides, sizes of zero make a call a no-op (a product over k = 0 gives
+ * zeros), and the conventions above hold otherwise (stream order, validation
+ * before any launch, one kernel launch per call, no allocation, no workspace,
+ * so calls may be captured and may run on several streams at once).
+ * Non-finite values are specified for these operators.  */
+
+/* 8-bit formats: e4m3 (bias 7, largest 448, no infinity, NaN 0x7F/0xFF) and
+ * e5m2 (bias 15, largest 57344), both with subnormals. */
+typedef enum { ECHO_E4M3 = 0, ECHO_E5M2 = 1 } echo_fp8_format;
+/* types of the scales: fp32, or a power of two 2^(b - 127) held in its exponent
+ * byte b (255 = NaN). */
+typedef enum { ECHO_SCALE_F32 = 0, ECHO_SCALE_E8M0 = 1 } echo_scale_type;
+
+#define ECHO_FP8_BLOCK 128
+
+/* P matrices [rows, k] in 8-bit floating point with a scale for each block of
+ * 128 elements along k (the last block of a row may be shorter): of each row
+ * (block_rows 1) or of each block of 128 rows (block_rows 128).  Element (i, j)
+ * stands for codes[i * ld + j] * scales[(i / block_rows) * scale_row_stride +
+ * (j / 128) * scale_k_stride].  codes: 16-byte aligned, ld a multiple of 16 and
+ * at most 2^22; bytes k .. ld - 1 of a row are never used or written (up to the
+ * next multiple of 16 they may be read).  Scales next to each other for
+ * consecutive rows (scale_row_stride 1) are read and written fastest. */
+typedef struct {
+  void* const* codes;       /* host array of P device pointers                   */
+  void* const* scales;      /* host array of P device pointers                   */
+  int64_t ld;               /* bytes between rows of codes                       */
+  int64_t scale_row_stride; /* elements between the scales of (blocks of) rows   */
+  int64_t scale_k_stride;   /* elements between the scales of blocks along k     */
+  int32_t format;           /* echo_fp8_format                                   */
+  int32_t scale_type;       /* echo_scale_type                                   */
+  int32_t block_rows;       /* 1 or 128                                          */
+} echo_fp8;
+
+/* Source: none on the pages (they leave the products' own precision open).
+ * Quantize P matrices X_r [rows, cols] (dtype fp32, bfloat16 or fp16; ldx
+ * elements between rows, any alignment of the element type) to 8-bit floating
+ * point, in one pass over X_r: along_rows (or NULL) receives X_r with blocks
+ * along its rows (codes [rows, cols]), along_cols (or NULL) its transpose with
+ * blocks along its columns (codes [cols, rows]); with both, format, scale type
+ * and block_rows are the same.
+ * Of each block with the largest finite magnitude a, the scale is the smallest
+ * power of two s, at least 2^-126, with a / s within the format (1 where a is
+ * 0); the codes are x / s (exact) rounded to nearest, ties to even: one rounding
+ * per element, the same whatever kernel or split computes it.  Infinities and NaN become
+ * NaN codes and do not count in a.  Scales are positive and distinct elements
+ * of the outputs do not share memory (strides of at least 1).
+ * rows, cols: at most 2^22 each, P * ceil(rows / 128) * ceil(cols / 128) below
+ * 2^21.  Errors: ECHO_ERR_ARG (null or misaligned pointer, both outputs NULL or not alike, bad enum, an output overlapping
+ * another output or an input), ECHO_ERR_SHAPE, ECHO_ERR_DTYPE, ECHO_ERR_HIP. */
+echo_status echo_quantize_fp8(const void* const* X, int32_t P, int64_t rows, int64_t cols, int64_t ldx,
+                              int32_t dtype, const echo_fp8* along_rows, const echo_fp8* along_cols,
+                              echo_stream_t stream);
+
+/* Source: Page R «Почему обычное 4-битное суммирование портит модель» (each
+ * GPU computes its own part of the layer's result); the 8-bit operands are this
+ * library's.
+ * out_r = A_r W_r^T for every rank: A_r [M, K] and W_r [N, K] as echo_fp8 (each
+ * of either format and either block_rows, both of the same scale type), out_r
+ * [M, N] of out_dtype (fp32, bfloat16 or fp16) with ldo elements between rows,
+ * any alignment of the element type.  Products of a block of 128 are added in
+ * fp32 on the matrix cores, the blocks' sums, scaled, in fp32; the result is
+ * rounded once, to out_dtype.  Scales of any strides of 0 or more.  With the
+ * three operands of a linear layer quantized both ways this covers the forward
+ * product, the input gradient and the weight gradient.  Deterministic; a row's
+ * result does not depend on what other rows hold, NaN and infinities included.
+ * M, N, K: at most 2^22 each, P * ceil(M / 128) * ceil(N / 128) below 2^21.
+ * Errors: ECHO_ERR_ARG (null or misaligned pointer, scale types that differ, bad enum, an output overlapping another
+ * output or an input), ECHO_ERR_SHAPE, ECHO_ERR_DTYPE, ECHO_ERR_HIP. */
+echo_status echo_gemm_fp8(const echo_fp8* A, const echo_fp8* W, void* const* out, int32_t P, int64_t M,
+                          int64_t N, int64_t K, int64_t ldo, int32_t out_dtype, echo_stream_t stream);
+
+/* Source: none on the pages (dropout before the residual add of the blocks that
+ * «Почему обычное 4-битное суммирование портит модель» reduces).
+ * out = residual + dropout(x), or dropout(x) where residual is NULL, which with
+ * x the gradient of the output is the backward pass.  x, residual, out: [rows,
+ * cols] with ldx, ldr, ldo elements between rows, x of x_dtype, residual and
+ * out of out_dtype (each fp32, bfloat16 or fp16), any alignment of the element
+ * type.  Element (i, j) has the index e = first + i * cols + j and is kept iff
+ * u(e) >= t, t = p * 65536 rounded to nearest (ties to even): u(e) is 16-bit
+ * lane e % 8 (low half first) of the four words of Philox4x32-10 (Salmon,
+ * Moraes, Dror, Shaw, "Parallel random numbers: as easy as 1, 2, 3", SC 2011)
+ * with the 64-bit counter halves (e / 8, rng[1] + offset, wrapping) and the key
+ * rng[0].  A kept x is multiplied by fp32(65536 / (65536 - t)), so the mean is
+ * exact for the p in force; a dropped one counts as 0 even where it is NaN or
+ * infinite.  Product and sum are fp32 operations, rounded once to out_dtype.
+ * The mask is a function of rng, offset and e alone: it is never stored, the
+ * backward pass draws it again, and ranks that hold different rows (`first`)
+ * or copies of the same ones agree on it.
+ * rng: device pointer to two int64 (key, step), 8-byte aligned, read by the
+ * kernel, so a captured call follows what the caller puts there between
+ * replays.  out may be x or residual itself (same pointer and pitch; of x only
+ * where their types have the same size), and overlap neither otherwise.
+ * 0 <= p <= 1 - 2^-16; first >= 0, first + rows * cols <= 2^62; rows, cols at
+ * most 2^31 - 1, rows * cols at most 2^40.  Errors: ECHO_ERR_ARG (null or
+ * misaligned pointer, p or first out of range, an overlap), ECHO_ERR_SHAPE,
+ * ECHO_ERR_DTYPE, ECHO_ERR_HIP. */
+echo_status echo_dropout_add(const void* x, const void* residual, void* out, int64_t rows, int64_t cols,
+                             int64_t ldx, int64_t ldr, int64_t ldo, int32_t x_dtype, int32_t out_dtype,
+                             double p, const int64_t* rng, int64_t offset, int64_t first,
+                             echo_stream_t stream);
 
 /* Source: none on the pages (error reporting of this library).
  * Static description of a status code. */

@@ -1,0 +1,78 @@
+"""Plain references of the layer operators in 64 bits (numpy), and their inputs."""
+import numpy as np
+
+FORMATS = {"e4m3": (3, -6, 448.0), "e5m2": (2, -14, 57344.0)}  # mantissa bits, lowest exponent, largest
+
+
+def round_to_format(v, fmt):
+    """v (float64) to the nearest value of the format, ties to even; v within range."""
+    bits, low, _ = FORMATS[fmt]
+    _, e = np.frexp(v)
+    step = np.ldexp(1.0, np.maximum(e - 1, low) - bits)
+    return np.rint(v / step) * step
+
+
+def quantize_ref(x, fmt, block_rows):
+    """(codes as values, scales) of x [rows, k] float64, blocks along k; what is not
+    finite becomes NaN and does not count."""
+    rows, k = x.shape
+    limit = FORMATS[fmt][2]
+    nb, kb = -(-rows // block_rows), -(-k // 128)
+    codes, scales = np.zeros_like(x), np.ones((nb, kb))
+    for i in range(nb):
+        for j in range(kb):
+            at = (slice(i * block_rows, (i + 1) * block_rows), slice(j * 128, (j + 1) * 128))
+            b = x[at]
+            fin = np.isfinite(b)
+            a = np.abs(b[fin]).max() if fin.any() else 0.0
+            if a > 0:
+                s = 2.0 ** -126
+                while a / s > limit:
+                    s *= 2.0
+                scales[i, j] = s
+            codes[at] = np.where(fin, round_to_format(np.where(fin, b, 0.0) / scales[i, j], fmt), np.nan)
+    return codes, scales
+
+
+def dequantize(codes, scales, block_rows):
+    rows, k = codes.shape
+    i, j = np.arange(rows) // block_rows, np.arange(k) // 128
+    return codes * scales[np.ix_(i, j)]
+
+
+def philox10(chunk, step, key):
+    """The four 32-bit words of Philox4x32-10 for arrays of 64-bit chunk numbers."""
+    m = np.uint64(0xFFFFFFFF)
+    s32 = np.uint64(32)
+    chunk = np.asarray(chunk, dtype=np.uint64)
+    c = [chunk & m, chunk >> s32, np.full_like(chunk, step & 0xFFFFFFFF), np.full_like(chunk, (step >> 32) & 0xFFFFFFFF)]
+    k = [key & 0xFFFFFFFF, (key >> 32) & 0xFFFFFFFF]
+    for _ in range(10):
+        p0, p1 = c[0] * np.uint64(0xD2511F53), c[2] * np.uint64(0xCD9E8D57)
+        c = [(p1 >> s32) ^ c[1] ^ np.uint64(k[0]), p1 & m, (p0 >> s32) ^ c[3] ^ np.uint64(k[1]), p0 & m]
+        k = [(k[0] + 0x9E3779B9) & 0xFFFFFFFF, (k[1] + 0xBB67AE85) & 0xFFFFFFFF]
+    return c
+
+
+def keep_mask(first, n, step, key, p):
+    """Which of the elements first .. first + n - 1 stay."""
+    t = int(np.rint(p * 65536))
+    e = np.arange(n, dtype=np.uint64) + np.uint64(first)
+    w = philox10(e >> np.uint64(3), step, key)
+    lane = (e & np.uint64(7)).astype(np.int64)
+    word = np.choose(lane // 2, w)
+    return ((word >> (np.uint64(16) * (lane % 2).astype(np.uint64))) & np.uint64(0xFFFF)) >= t
+
+
+def dropout_ref(x, r, p, first, step, key):
+    """residual + dropout(x) as the fp32 operations the definition names (x, r
+    float32 arrays), before the rounding to the output's type."""
+    t = int(np.rint(p * 65536))
+    keep = keep_mask(first, x.size, step, key, p).reshape(x.shape)
+    with np.errstate(all="ignore"):
+        y = np.where(keep, x * np.float32(65536.0 / (65536 - t)), np.float32(0))
+        return y if r is None else y + r
+
+
+def to_np64(t):
+    return t.detach().float().cpu().numpy().astype(np.float64)
