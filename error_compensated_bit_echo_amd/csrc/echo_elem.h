@@ -11,6 +11,20 @@
 namespace echo {
 namespace {
 
+// The launch arguments (the kernel's first parameter, at the start of the argument
+// segment) where they lie in constant memory, so that a pointer picked by the rank,
+// which is uniform, is one scalar load; indexing the parameter itself would make the
+// compiler copy it to scratch memory.
+#if defined(__HIP_DEVICE_COMPILE__)
+template <typename Args>
+__device__ __forceinline__ const __attribute__((address_space(4))) Args* kernel_args() {
+  return (const __attribute__((address_space(4))) Args*)__builtin_amdgcn_kernarg_segment_ptr();
+}
+#else
+template <typename Args>
+__device__ const Args* kernel_args();  // never run: the host pass only parses the kernels
+#endif
+
 template <int E>
 struct ElemOf;
 template <>

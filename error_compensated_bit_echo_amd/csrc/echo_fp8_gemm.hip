@@ -1,16 +1,23 @@
 // The product of matrices in 8-bit floating point with a scale per 128 elements of
 // k, on the matrix cores: out[m, n] = sum_b sA[m, b] sW[n, b] sum_{k in b} A[m, k] W[n, k].
 //
-// The codes are widened to bfloat16, which holds every value of both formats, and
-// multiplied with v_mfma_f32_16x16x32_bf16, whose fp32 sums are precise; a block's
-// sum is scaled and added in fp32.  (The 8-bit instructions align the products of
-// each run of 8 consecutive k to the largest of them and drop what lies below 2^-13
-// of it: measured 1.5e-5 of the result against 6e-9 for normal e4m3 data.)
+// Two ways to a block's sum.
+//   * The 8-bit instruction v_mfma_scale_f32_32x32x64_f8f6f4, with exponent-byte
+//     scales applied by the instruction itself.  It aligns the products of each run
+//     of 8 consecutive k to the largest of them and drops what lies below 2^-13 of it
+//     (measured: 1.5e-5 of the result for normal e4m3 data, whatever K), so it serves
+//     outputs of 16 bits, whose own rounding is 2^-9 or 2^-12.
+//   * Codes widened to bfloat16, which holds every value of both formats, and
+//     v_mfma_f32_32x32x16_bf16, whose fp32 sums are precise (measured 6e-9 per
+//     block), at half the rate: fp32 outputs.
 // The product is computed transposed (W supplies the instruction's first operand),
-// so a lane holds four consecutive columns n of one row m.
+// so a lane holds runs of four consecutive columns n of one row m.
 #pragma clang fp contract(off)
 
+#include <type_traits>
+
 #include "echo_elem.h"
+#include "echo_slab.h"
 
 namespace echo {
 namespace {
@@ -18,8 +25,74 @@ namespace {
 typedef int i32x4 __attribute__((ext_vector_type(4)));
 typedef int i32x8 __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 
-constexpr int kThreads = 256;
+// 8 codes (two dwords) as bfloat16, exactly.
+template <bool E5>
+__device__ __forceinline__ bf16x8 widen8(int lo, int hi) {
+  bf16x8 x{};
+#if defined(__HIP_DEVICE_COMPILE__)
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const uint32_t w = static_cast<uint32_t>(i ? hi : lo);
+    const bf16x2 p = E5 ? __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(w, 1.0f, false)
+                        : __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, 1.0f, false);
+    const bf16x2 q = E5 ? __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(w, 1.0f, true)
+                        : __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, 1.0f, true);
+    x[4 * i] = p[0];
+    x[4 * i + 1] = p[1];
+    x[4 * i + 2] = q[0];
+    x[4 * i + 3] = q[1];
+  }
+#endif
+  return x;
+}
+
+// A scale's bits: fp32 bits, or the exponent byte.
+template <bool E8>
+__device__ __forceinline__ uint32_t scale_bits(const void* s, int64_t at) {
+  if constexpr (E8) return static_cast<const uint8_t*>(s)[at];
+  else return static_cast<const uint32_t*>(s)[at];
+}
+// ... and its value in fp32 (exponent byte 0 is 2^-127, subnormal, and 255 NaN).
+template <bool E8>
+__device__ __forceinline__ float scale_value(uint32_t b) {
+  if constexpr (E8) return __uint_as_float(b == 255 ? 0x7FC00000u : b == 0 ? 0x00400000u : b << 23);
+  else return __uint_as_float(b);
+}
+
+struct RankPtrs {
+  const uint8_t *A, *W;
+  const void *sA, *sW;
+  void* out;
+};
+__device__ __forceinline__ RankPtrs rank_ptrs(int r) {
+  const auto* k = kernel_args<GemmFp8Args>();
+  return RankPtrs{k->A[r], k->W[r], k->sA[r], k->sW[r], k->out[r]};
+}
+
+// Stores n (at most 4) consecutive columns of a row one by one.
+__device__ __forceinline__ void store_each(void* out, int64_t at, int64_t left, const float* v, int n, int elem) {
+#pragma unroll
+  for (int e = 0; e < 4; ++e)
+    if (e < n && e < left) {
+      if (elem == kElemF32) store1<kElemF32>(out, at + e, v[e]);
+      else if (elem == kElemBf16) store1<kElemBf16>(out, at + e, v[e]);
+      else store1<kElemF16>(out, at + e, v[e]);
+    }
+}
+
+// ---- few rows of A -------------------------------------------------------------
+//
+// 16 CT columns of the output (rows of W) per workgroup of 8 wavefronts, which share
+// k: wavefront w takes the blocks w, w + 8, ... of 128 and reads its codes of W and
+// A straight from memory (W is read once in all, 2 KiB per instruction pair), and
+// the eight sums meet in LDS in a fixed order.  Bound by the bytes of W.
+
+constexpr int kThinWaves = 8;
 
 // 32 bytes of a row from byte k on, zeros from K on.  The 16-byte runs that hold a
 // valid byte lie within the row's pitch (a multiple of 16).
@@ -45,128 +118,453 @@ __device__ __forceinline__ i32x8 load_frag(const uint8_t* row, int64_t k, int64_
   return f;
 }
 
-typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
-typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
-
-// 8 codes (two dwords) as bfloat16, exactly.
-template <bool E5>
-__device__ __forceinline__ bf16x8 widen8(int lo, int hi) {
-  bf16x8 x{};
-#if defined(__HIP_DEVICE_COMPILE__)
+// MT tiles of 16 rows of A.
+template <int MT, int CT, bool A5, bool W5, bool E8>
+__global__ __launch_bounds__(64 * kThinWaves) void echo_gemm_fp8_thin_k(const GemmFp8Args a) {
+  __shared__ f32x4 part[kThinWaves][MT][CT][64];
+  const RankPtrs p = rank_ptrs(blockIdx.z);
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, sub = lane & 15, g = lane >> 4;
+  const int64_t m0 = static_cast<int64_t>(blockIdx.y) * (16 * MT), n0 = static_cast<int64_t>(blockIdx.x) * (16 * CT);
+  int64_t m[MT], n[CT];  // the rows this lane supplies, clamped: what lies past the edge is not stored
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const uint32_t w = static_cast<uint32_t>(i ? hi : lo);
-    const bf16x2 p = E5 ? __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(w, 1.0f, false)
-                        : __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, 1.0f, false);
-    const bf16x2 q = E5 ? __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(w, 1.0f, true)
-                        : __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, 1.0f, true);
-    x[4 * i] = p[0];
-    x[4 * i + 1] = p[1];
-    x[4 * i + 2] = q[0];
-    x[4 * i + 3] = q[1];
-  }
-#endif
-  return x;
-}
-
-// The sum over a block: lane l supplies 32 codes of row l % 16 of W and of A (any
-// assignment of k to lanes does, as both operands use the same).
-template <bool A5, bool W5>
-__device__ __forceinline__ f32x4 block_sum(i32x8 w, i32x8 a) {
-  f32x4 c{};
-#if defined(__HIP_DEVICE_COMPILE__)
+  for (int i = 0; i < MT; ++i) m[i] = m0 + 16 * i + sub < a.M ? m0 + 16 * i + sub : a.M - 1;
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-    c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(widen8<W5>(w[2 * i], w[2 * i + 1]), widen8<A5>(a[2 * i], a[2 * i + 1]),
-                                                c, 0, 0, 0);
-#endif
-  return c;
-}
-
-// A scale as fp32.
-template <bool E8>
-__device__ __forceinline__ float scale_at(const void* s, int64_t at) {
-  if constexpr (E8) {
-    const uint32_t b = static_cast<const uint8_t*>(s)[at];
-    return __uint_as_float(b == 255 ? 0x7FC00000u : b == 0 ? 0x00400000u : b << 23);  // 0: 2^-127, subnormal
-  } else {
-    return static_cast<const float*>(s)[at];
-  }
-}
-
-// 64 x 64 tiles, four wavefronts of 32 x 32, fragments straight from memory.
-template <bool A5, bool W5, bool E8>
-__global__ __launch_bounds__(kThreads) void echo_gemm_fp8_k(const GemmFp8Args a, int64_t tiles_n) {
-  const int r = blockIdx.y;
-  const uint8_t *A = a.A[0], *W = a.W[0];
-  const void *sA = a.sA[0], *sW = a.sW[0];
-  void* out = a.out[0];
-#pragma unroll
-  for (int i = 1; i < kMaxRanks; ++i)
-    if (r == i) {
-      A = a.A[i];
-      W = a.W[i];
-      sA = a.sA[i];
-      sW = a.sW[i];
-      out = a.out[i];
-    }
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int64_t tm = blockIdx.x / tiles_n, tn = blockIdx.x - tm * tiles_n;
-  const int64_t m0 = tm * 64 + 32 * (wave >> 1), n0 = tn * 64 + 32 * (wave & 1);
-  const int sub = lane & 15, g = lane >> 4;
-  int64_t m[2], n[2];  // the rows this lane supplies, clamped: what lies past the edge is not stored
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    m[i] = m0 + 16 * i + sub < a.M ? m0 + 16 * i + sub : a.M - 1;
-    n[i] = n0 + 16 * i + sub < a.N ? n0 + 16 * i + sub : a.N - 1;
-  }
-  f32x4 acc[2][2] = {};
+  for (int j = 0; j < CT; ++j) n[j] = n0 + 16 * j + sub < a.N ? n0 + 16 * j + sub : a.N - 1;
+  f32x4 acc[MT][CT] = {};
   const int64_t nb = (a.K + kFp8Block - 1) / kFp8Block;
-  for (int64_t b = 0; b < nb; ++b) {
-    i32x8 fa[2], fw[2];
+#pragma unroll 2
+  for (int64_t b = wave; b < nb; b += kThinWaves) {
+    i32x8 fa[MT], fw[CT];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      fa[i] = load_frag(A + m[i] * a.lda, b * kFp8Block + 32 * g, a.K);
-      fw[i] = load_frag(W + n[i] * a.ldw, b * kFp8Block + 32 * g, a.K);
-    }
+    for (int j = 0; j < CT; ++j) fw[j] = load_frag(p.W + n[j] * a.ldw, b * kFp8Block + 32 * g, a.K);
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const float ca = scale_at<E8>(sA, (m[i] >> a.sa_shift) * a.sa_row + b * a.sa_k);
+    for (int i = 0; i < MT; ++i) fa[i] = load_frag(p.A + m[i] * a.lda, b * kFp8Block + 32 * g, a.K);
+    float ca[MT], cw[CT][4];
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const f32x4 p = block_sum<A5, W5>(fw[j], fa[i]);
+    for (int i = 0; i < MT; ++i)
+      ca[i] = scale_value<E8>(scale_bits<E8>(p.sA, (m[i] >> a.sa_shift) * a.sa_row + b * a.sa_k));
 #pragma unroll
-        for (int v = 0; v < 4; ++v) {
-          int64_t nn = n0 + 16 * j + 4 * g + v;
-          nn = nn < a.N ? nn : a.N - 1;
-          const float cw = scale_at<E8>(sW, (nn >> a.sw_shift) * a.sw_row + b * a.sw_k);
-          acc[i][j][v] = __builtin_fmaf(p[v], ca * cw, acc[i][j][v]);
-        }
-      }
-    }
-  }
-#pragma unroll
-  for (int i = 0; i < 2; ++i)
-#pragma unroll
-    for (int j = 0; j < 2; ++j)
+    for (int j = 0; j < CT; ++j)
 #pragma unroll
       for (int v = 0; v < 4; ++v) {
-        const int64_t mm = m0 + 16 * i + sub, nn = n0 + 16 * j + 4 * g + v;
-        if (mm < a.M && nn < a.N) {
-          const int64_t at = mm * a.ldo + nn;
-          if (a.out_elem == kElemF32) store1<kElemF32>(out, at, acc[i][j][v]);
-          else if (a.out_elem == kElemBf16) store1<kElemBf16>(out, at, acc[i][j][v]);
-          else store1<kElemF16>(out, at, acc[i][j][v]);
+        int64_t nn = n0 + 16 * j + 4 * g + v;
+        nn = nn < a.N ? nn : a.N - 1;
+        cw[j][v] = scale_value<E8>(scale_bits<E8>(p.sW, (nn >> a.sw_shift) * a.sw_row + b * a.sw_k));
+      }
+    f32x4 t[MT][CT] = {};
+#pragma unroll
+    for (int s = 0; s < 4; ++s) {
+      bf16x8 wa[CT];
+#pragma unroll
+      for (int j = 0; j < CT; ++j) wa[j] = widen8<W5>(fw[j][2 * s], fw[j][2 * s + 1]);
+#pragma unroll
+      for (int i = 0; i < MT; ++i) {
+        const bf16x8 aa = widen8<A5>(fa[i][2 * s], fa[i][2 * s + 1]);
+#if defined(__HIP_DEVICE_COMPILE__)
+#pragma unroll
+        for (int j = 0; j < CT; ++j) t[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wa[j], aa, t[i][j], 0, 0, 0);
+#endif
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+      for (int j = 0; j < CT; ++j)
+#pragma unroll
+        for (int v = 0; v < 4; ++v) acc[i][j][v] = __builtin_fmaf(t[i][j][v], ca[i] * cw[j][v], acc[i][j][v]);
+  }
+#pragma unroll
+  for (int i = 0; i < MT; ++i)
+#pragma unroll
+    for (int j = 0; j < CT; ++j) part[wave][i][j][lane] = acc[i][j];
+  __syncthreads();
+  // wavefront w sums and writes the sub-tiles w, w + 8, ...
+  for (int u = wave; u < MT * CT; u += kThinWaves) {
+    const int i = u / CT, j = u - i * CT;
+    f32x4 s = part[0][i][j][lane];
+#pragma unroll
+    for (int w = 1; w < kThinWaves; ++w) {
+      const f32x4 x = part[w][i][j][lane];
+#pragma unroll
+      for (int v = 0; v < 4; ++v) s[v] = s[v] + x[v];
+    }
+    const int64_t mm = m0 + 16 * i + sub, nn = n0 + 16 * j + 4 * g;
+    if (mm < a.M) {
+      const float v[4] = {s[0], s[1], s[2], s[3]};
+      store_each(p.out, mm * a.ldo + nn, a.N - nn, v, 4, a.out_elem);
+    }
+  }
+}
+
+// ---- tiles through LDS -----------------------------------------------------------
+//
+// A workgroup of WM x WN wavefronts computes a BM x BN tile, each wavefront BM / WM
+// rows and BN / WN columns in 32 x 32 sub-tiles.  k advances one block of 128 (128
+// bytes of each row) at a time through a ring of S LDS slabs, filled straight from
+// memory while earlier slabs are multiplied; each K step needs one barrier.  16-byte
+// chunk c of row r lies at slot c ^ ((r / 2) % 8) of its 128-byte row, so a fragment
+// read covers all LDS banks.  Lane l supplies row l % 32 of a sub-tile and the bytes
+// 64 (l / 32) .. + 63 of the K step: which k a lane and instruction covers does not
+// matter, as both operands use the same assignment and a scale covers all 128.
+// Accumulator v of lane l is row l % 32 of the tile's A rows and column
+// 8 (v / 4) + 4 (l / 32) + v % 4 of its W rows.
+// The scales of a K step's rows are staged in LDS by one load per thread, a step
+// ahead, in a ring of three (a wavefront may still read step it's while another
+// writes step it + 2's).
+// Rows past the edge read as zeros (the buffer resources end with the matrix), and
+// so does what lies past K in the last step: 16-byte chunks by an offset out of
+// range, the bytes behind K in the last chunk by one pass over the slab.
+
+enum TileMode {
+  kScaled8 = 0,  // the 8-bit instruction applies exponent-byte scales
+  kPlain8 = 1,   // the 8-bit instruction, a block's sum scaled in fp32
+  kWide = 2      // bfloat16, a block's sum scaled in fp32
+};
+
+// An offset past the end of every buffer resource here (they stay below 2^31 bytes).
+constexpr uint32_t kPastEnd = 0x80000000u;
+
+template <int BM, int BN, int WM, int WN, int S, int MODE, bool A5, bool W5, bool E8>
+__global__ __launch_bounds__(64 * WM * WN) void echo_gemm_fp8_tile_k(const GemmFp8Args a, uint32_t gm, uint32_t gn) {
+  static_assert(MODE != kScaled8 || E8, "the instruction takes exponent bytes");
+  constexpr int NW = WM * WN, kThreads = 64 * NW;
+  constexpr int RW = BM / WM, CW = BN / WN, MI = RW / 32, NJ = CW / 32;
+  constexpr int JA = BM / (8 * NW), JW = BN / (8 * NW), kLoads = JA + JW;  // 1 KiB slab blocks per wavefront
+  static_assert(MI * 32 * WM == BM && NJ * 32 * WN == BN && JA * 8 * NW == BM && JW * 8 * NW == BN, "even splits");
+  constexpr int kSlabA = BM * 128, kSlab = (BM + BN) * 128;
+  constexpr int kRows = BM + BN;                              // rows with a scale
+  constexpr int kPer = (kRows + kThreads - 1) / kThreads;     // scales per thread
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[S * kSlab];
+  __shared__ __attribute__((aligned(16))) uint32_t sc[3][kRows];
+
+  // The hardware hands the workgroups of a launch to the eight XCDs in turn, and each
+  // XCD has its own L2: workgroup i takes a tile of the (i % 8)-th contiguous run, and
+  // tiles are ordered in bands of 8 row tiles, so the tiles an XCD works on at a time
+  // share their panels of A and of W.
+  const uint32_t T = gridDim.x, x = blockIdx.x % 8, q = T / 8, rem = T % 8;
+  uint32_t id = x * q + (x < rem ? x : rem) + blockIdx.x / 8;
+  const int r = static_cast<int>(id / (gm * gn));
+  id -= r * gm * gn;
+  const uint32_t band = id / (8 * gn), in_band = id - band * 8 * gn;
+  const uint32_t high = gm - 8 * band < 8 ? gm - 8 * band : 8;  // row tiles of this band
+  const int64_t m0 = static_cast<int64_t>(8 * band + in_band % high) * BM;
+  const int64_t n0 = static_cast<int64_t>(in_band / high) * BN;
+  const RankPtrs p = rank_ptrs(r);
+
+  const int t = threadIdx.x, lane = t & 63, wave = t >> 6, wm = wave / WN, wn = wave % WN, half = lane >> 5;
+  const int64_t steps = (a.K + 127) / 128;
+  const int64_t K16 = (a.K + 15) / 16 * 16;
+  const int64_t rows_a = a.M - m0 < BM ? a.M - m0 : BM, rows_w = a.N - n0 < BN ? a.N - n0 : BN;
+  const BufRsrc rA = buffer_rsrc(p.A + m0 * a.lda, static_cast<int32_t>((rows_a - 1) * a.lda + K16));
+  const BufRsrc rW = buffer_rsrc(p.W + n0 * a.ldw, static_cast<int32_t>((rows_w - 1) * a.ldw + K16));
+  // Lane l fills slot l of each 1 KiB block: row 8 i + l / 8, slot l % 8.
+  uint32_t offA[JA], offW[JW];
+#pragma unroll
+  for (int j = 0; j < JA; ++j) {
+    const int row = 8 * (JA * wave + j) + (lane >> 3);
+    offA[j] = static_cast<uint32_t>(row * a.lda + 16 * ((lane & 7) ^ ((row >> 1) & 7)));
+  }
+#pragma unroll
+  for (int j = 0; j < JW; ++j) {
+    const int row = 8 * (JW * wave + j) + (lane >> 3);
+    offW[j] = static_cast<uint32_t>(row * a.ldw + 16 * ((lane & 7) ^ ((row >> 1) & 7)));
+  }
+  auto issue = [&](int buf, int64_t it) {
+    uint8_t* As = lds + buf * kSlab;
+    uint8_t* Ws = As + kSlabA;
+    const uint32_t kb = static_cast<uint32_t>(it * 128);
+    if (it + 1 < steps || K16 % 128 == 0) {
+#pragma unroll
+      for (int j = 0; j < JA; ++j) buffer_load_lds16<0>(rA, As + 1024 * (JA * wave + j), offA[j], kb);
+#pragma unroll
+      for (int j = 0; j < JW; ++j) buffer_load_lds16<0>(rW, Ws + 1024 * (JW * wave + j), offW[j], kb);
+    } else {  // the last step of a K that is no multiple of 128
+      const int chunks = static_cast<int>((K16 - it * 128) / 16);
+#pragma unroll
+      for (int j = 0; j < JA; ++j) {
+        const int row = 8 * (JA * wave + j) + (lane >> 3);
+        const bool in = ((lane & 7) ^ ((row >> 1) & 7)) < chunks;
+        buffer_load_lds16<0>(rA, As + 1024 * (JA * wave + j), in ? offA[j] : kPastEnd, kb);
+      }
+#pragma unroll
+      for (int j = 0; j < JW; ++j) {
+        const int row = 8 * (JW * wave + j) + (lane >> 3);
+        const bool in = ((lane & 7) ^ ((row >> 1) & 7)) < chunks;
+        buffer_load_lds16<0>(rW, Ws + 1024 * (JW * wave + j), in ? offW[j] : kPastEnd, kb);
+      }
+    }
+  };
+  // The scales: thread t stages rows t, t + kThreads, ... of A's then W's.
+  const void* sp[kPer];
+  int64_t sat[kPer], sk[kPer];
+#pragma unroll
+  for (int u = 0; u < kPer; ++u) {
+    int row = t + u * kThreads;
+    row = row < kRows ? row : kRows - 1;
+    const bool of_a = row < BM;
+    int64_t i = of_a ? m0 + row : n0 + row - BM;
+    const int64_t end = of_a ? a.M : a.N;
+    i = i < end ? i : end - 1;  // past the edge: any scale does
+    sp[u] = of_a ? p.sA : p.sW;
+    sat[u] = of_a ? (i >> a.sa_shift) * a.sa_row : (i >> a.sw_shift) * a.sw_row;
+    sk[u] = of_a ? a.sa_k : a.sw_k;
+  }
+  uint32_t sreg[kPer];
+  auto load_scales = [&](int64_t it) {
+#pragma unroll
+    for (int u = 0; u < kPer; ++u) sreg[u] = scale_bits<E8>(sp[u], sat[u] + it * sk[u]);
+  };
+  auto stage_scales = [&](int ring) {
+#pragma unroll
+    for (int u = 0; u < kPer; ++u)
+      if (t + u * kThreads < kRows)
+        sc[ring][t + u * kThreads] =
+            MODE == kScaled8 ? sreg[u] : __float_as_uint(scale_value<E8>(sreg[u]));
+  };
+  // Bytes behind K in the last chunk of the last slab, on both sides (a NaN there
+  // would survive a product with zero).
+  auto clear_tail = [&](uint8_t* slab) {
+    const int c = static_cast<int>(a.K % 128) / 16, n = static_cast<int>(a.K % 16);
+    for (int row = t; row < kRows; row += kThreads) {
+      const int in = row < BM ? row : row - BM;
+      uint8_t* b = slab + row * 128 + 16 * (c ^ ((in >> 1) & 7));
+      for (int i = n; i < 16; ++i) b[i] = 0;
+    }
+    __syncthreads();
+  };
+
+  f32x16 acc[MI][NJ];
+#pragma unroll
+  for (int i = 0; i < MI; ++i)
+#pragma unroll
+    for (int j = 0; j < NJ; ++j)
+#pragma unroll
+      for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.0f;
+  [[maybe_unused]] f32x16 blk[MI][NJ];
+
+  // Fragments of a half step: 32 bytes per lane of each sub-tile, as two 16-byte
+  // chunks.  They roll: as soon as the instructions that use a fragment are issued,
+  // the next half step's is read in its place (A's, used until the end, alternate
+  // between two sets with the 8-bit instruction).
+  constexpr int kSetsA = MODE == kWide ? 1 : 2;
+  i32x4 fa[kSetsA][MI][2], fw[NJ][2];
+  auto read_a = [&](int set, const uint8_t* slab, int hs, int c) {
+#pragma unroll
+    for (int i = 0; i < MI; ++i) {
+      const int row = RW * wm + 32 * i + (lane & 31), ch = 4 * half + 2 * hs + c;
+      fa[set][i][c] = *reinterpret_cast<const i32x4*>(slab + row * 128 + 16 * (ch ^ ((row >> 1) & 7)));
+    }
+  };
+  auto read_w = [&](int j, const uint8_t* slab, int hs, int c) {
+    const int row = CW * wn + 32 * j + (lane & 31), ch = 4 * half + 2 * hs + c;
+    fw[j][c] = *reinterpret_cast<const i32x4*>(slab + kSlabA + row * 128 + 16 * (ch ^ ((row >> 1) & 7)));
+  };
+  uint32_t ea[MI], ew[NJ];  // kScaled8: the step's scale bytes of the rows this lane supplies
+  // The instructions of half step HS, reading the next one's fragments (READ) from
+  // `slab`.
+  auto half_step = [&](auto hs, auto read, const uint8_t* slab) {
+    constexpr int HS = decltype(hs)::value;
+    constexpr bool READ = decltype(read)::value;
+    [[maybe_unused]] const f32x16 zero{};
+#if defined(__HIP_DEVICE_COMPILE__)
+    if constexpr (MODE != kWide) {
+      if constexpr (READ) {
+        read_a(HS ^ 1, slab, HS ^ 1, 0);
+        read_a(HS ^ 1, slab, HS ^ 1, 1);
+      }
+#pragma unroll
+      for (int j = 0; j < NJ; ++j) {
+        const i32x8 w = __builtin_shufflevector(fw[j][0], fw[j][1], 0, 1, 2, 3, 4, 5, 6, 7);
+#pragma unroll
+        for (int i = 0; i < MI; ++i) {
+          const i32x8 x8 = __builtin_shufflevector(fa[HS][i][0], fa[HS][i][1], 0, 1, 2, 3, 4, 5, 6, 7);
+          if constexpr (MODE == kScaled8)
+            acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
+                w, x8, acc[i][j], W5 ? 1 : 0, A5 ? 1 : 0, 0, static_cast<int>(ew[j]), 0, static_cast<int>(ea[i]));
+          else
+            blk[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(w, x8, HS == 0 ? zero : blk[i][j], W5 ? 1 : 0,
+                                                                       A5 ? 1 : 0, 0, 127, 0, 127);
+        }
+        if constexpr (READ) {
+          read_w(j, slab, HS ^ 1, 0);
+          read_w(j, slab, HS ^ 1, 1);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    } else {
+#pragma unroll
+      for (int s = 0; s < 4; ++s) {  // 16 k each
+        const int c = s >> 1, d = 2 * (s & 1);
+        bf16x8 wb[NJ];
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) wb[j] = widen8<W5>(fw[j][c][d], fw[j][c][d + 1]);
+#pragma unroll
+        for (int i = 0; i < MI; ++i) {
+          const bf16x8 ab = widen8<A5>(fa[0][i][c][d], fa[0][i][c][d + 1]);
+#pragma unroll
+          for (int j = 0; j < NJ; ++j)
+            blk[i][j] =
+                __builtin_amdgcn_mfma_f32_32x32x16_bf16(wb[j], ab, HS == 0 && s == 0 ? zero : blk[i][j], 0, 0, 0);
+        }
+        if constexpr (READ) {
+          if (s & 1) {
+            read_a(0, slab, HS ^ 1, c);
+#pragma unroll
+            for (int j = 0; j < NJ; ++j) read_w(j, slab, HS ^ 1, c);
+          }
         }
       }
+    }
+#endif
+  };
+  constexpr std::integral_constant<int, 0> H0{};
+  constexpr std::integral_constant<int, 1> H1{};
+
+  load_scales(0);
+#pragma unroll
+  for (int s = 0; s < S - 1; ++s)
+    if (s < steps) issue(s, s);
+  stage_scales(0);
+  if (steps >= S - 1)
+    __builtin_amdgcn_s_waitcnt(vmcnt_at_most_lds_drained((S - 2) * kLoads));
+  else
+    __builtin_amdgcn_s_waitcnt(vmcnt_at_most_lds_drained(0));
+  slab_barrier();
+  if (steps == 1 && a.K % 16 != 0) clear_tail(lds);
+  for (int c = 0; c < 2; ++c) {
+    read_a(0, lds, 0, c);
+    for (int j = 0; j < NJ; ++j) read_w(j, lds, 0, c);
+  }
+  int cur = 0, ring = 0;  // slab and scales of the step
+  auto step = [&](int64_t it, auto last) {
+    constexpr bool LAST = decltype(last)::value;
+    const bool more = it + S - 1 < steps;
+    const int next = cur + 1 == S ? 0 : cur + 1, ring1 = ring == 2 ? 0 : ring + 1;
+    if constexpr (!LAST) {
+      load_scales(it + 1);
+      if (more) issue(cur == 0 ? S - 1 : cur - 1, it + S - 1);  // into the slab step it - 1 used
+    }
+    if constexpr (MODE == kScaled8) {
+#pragma unroll
+      for (int i = 0; i < MI; ++i) ea[i] = sc[ring][RW * wm + 32 * i + (lane & 31)];
+#pragma unroll
+      for (int j = 0; j < NJ; ++j) ew[j] = sc[ring][BM + CW * wn + 32 * j + (lane & 31)];
+    }
+    half_step(H0, std::true_type{}, lds + cur * kSlab);
+    if constexpr (!LAST) {
+      stage_scales(ring1);
+      // this wavefront's reads of the slab are done and the next slab has landed
+      if (more)
+        __builtin_amdgcn_s_waitcnt(vmcnt_at_most_lds_drained((S - 2) * kLoads));
+      else
+        __builtin_amdgcn_s_waitcnt(vmcnt_at_most_lds_drained(0));
+      slab_barrier();
+      uint8_t* An = lds + next * kSlab;
+      if (it + 2 == steps && a.K % 16 != 0) clear_tail(An);
+      half_step(H1, std::true_type{}, An);
+    } else {
+      half_step(H1, std::false_type{}, nullptr);
+    }
+    if constexpr (MODE != kScaled8) {
+#pragma unroll
+      for (int j = 0; j < NJ; ++j) {
+        f32x4 cw[4];
+#pragma unroll
+        for (int v4 = 0; v4 < 4; ++v4)
+          cw[v4] = *reinterpret_cast<const f32x4*>(&sc[ring][BM + CW * wn + 32 * j + 8 * v4 + 4 * half]);
+#pragma unroll
+        for (int i = 0; i < MI; ++i) {
+          const float ca = __uint_as_float(sc[ring][RW * wm + 32 * i + (lane & 31)]);
+#pragma unroll
+          for (int v = 0; v < 16; ++v)
+            acc[i][j][v] = __builtin_fmaf(blk[i][j][v], ca * cw[v >> 2][v & 3], acc[i][j][v]);
+        }
+      }
+    }
+    cur = next;
+    ring = ring1;
+  };
+  for (int64_t it = 0; it + 1 < steps; ++it) step(it, std::false_type{});
+  step(steps - 1, std::true_type{});
+
+  // Out from the accumulators.  fp32: runs of 4 columns, 16 bytes.  16 bits: the two
+  // halves of the wavefront exchange runs (v_permlane32_swap), so a lane holds 8
+  // consecutive columns, 16 bytes.
+#pragma unroll
+  for (int i = 0; i < MI; ++i) {
+    const int64_t m = m0 + RW * wm + 32 * i + (lane & 31);
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) {
+      const int64_t nb = n0 + CW * wn + 32 * j;
+      const bool whole = nb + 32 <= a.N;
+      if (a.out_elem == kElemF32 || !whole) {
+#pragma unroll
+        for (int v4 = 0; v4 < 4; ++v4) {
+          const int64_t n = nb + 8 * v4 + 4 * half;
+          const float v[4] = {acc[i][j][4 * v4], acc[i][j][4 * v4 + 1], acc[i][j][4 * v4 + 2], acc[i][j][4 * v4 + 3]};
+          if (m < a.M) {
+            if (whole)
+              __builtin_memcpy(static_cast<float*>(p.out) + m * a.ldo + n, v, 16);
+            else
+              store_each(p.out, m * a.ldo + n, a.N - n, v, 4, a.out_elem);
+          }
+        }
+      } else {
+#pragma unroll
+        for (int v8 = 0; v8 < 2; ++v8) {
+          uint32_t w[4];  // two dwords of run 2 v8, two of run 2 v8 + 1
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float lo = acc[i][j][8 * v8 + 2 * e], hi = acc[i][j][8 * v8 + 2 * e + 1];
+            if (a.out_elem == kElemBf16)
+              w[e] = __builtin_bit_cast(uint32_t, bf16x2{narrow<kElemBf16>(lo), narrow<kElemBf16>(hi)});
+            else
+              w[e] = __builtin_bit_cast(uint32_t, f16x2{narrow<kElemF16>(lo), narrow<kElemF16>(hi)});
+          }
+          const auto s0 = __builtin_amdgcn_permlane32_swap(w[0], w[2], false, false);
+          const auto s1 = __builtin_amdgcn_permlane32_swap(w[1], w[3], false, false);
+          const uint32_t o[4] = {s0[0], s1[0], s0[1], s1[1]};
+          if (m < a.M)
+            __builtin_memcpy(static_cast<uint16_t*>(p.out) + m * a.ldo + nb + 16 * v8 + 8 * half, o, 16);
+        }
+      }
+    }
+  }
+}
+
+template <int BM, int BN, int WM, int WN, int S, int MODE, bool A5, bool W5, bool E8>
+hipError_t tile(const GemmFp8Args& a, int P, hipStream_t s) {
+  const uint32_t gm = static_cast<uint32_t>((a.M + BM - 1) / BM), gn = static_cast<uint32_t>((a.N + BN - 1) / BN);
+  hipLaunchKernelGGL((echo_gemm_fp8_tile_k<BM, BN, WM, WN, S, MODE, A5, W5, E8>), dim3(gm * gn * P),
+                     dim3(64 * WM * WN), 0, s, a, gm, gn);
+  return hipGetLastError();
+}
+
+template <int MT, int CT, bool A5, bool W5, bool E8>
+hipError_t thin(const GemmFp8Args& a, int P, hipStream_t s) {
+  const dim3 grid(static_cast<unsigned>((a.N + 16 * CT - 1) / (16 * CT)),
+                  static_cast<unsigned>((a.M + 16 * MT - 1) / (16 * MT)), static_cast<unsigned>(P));
+  hipLaunchKernelGGL((echo_gemm_fp8_thin_k<MT, CT, A5, W5, E8>), grid, dim3(64 * kThinWaves), 0, s, a);
+  return hipGetLastError();
 }
 
 template <bool A5, bool W5, bool E8>
 hipError_t launch(const GemmFp8Args& a, int P, hipStream_t s) {
-  const int64_t tm = (a.M + 63) / 64, tn = (a.N + 63) / 64;
-  const dim3 grid(static_cast<unsigned>(tm * tn), static_cast<unsigned>(P));
-  hipLaunchKernelGGL((echo_gemm_fp8_k<A5, W5, E8>), grid, dim3(kThreads), 0, s, a, tn);
-  return hipGetLastError();
+  if (a.M <= 16 || a.K == 0) return thin<1, 1, A5, W5, E8>(a, P, s);
+  if (a.M <= 32) return thin<2, 1, A5, W5, E8>(a, P, s);
+  const int64_t big = (a.M + 255) / 256 * ((a.N + 255) / 256) * P;
+  if (a.out_elem == kElemF32) {
+    if ((a.M + 255) / 256 * ((a.N + 127) / 128) * P >= 256) return tile<256, 128, 4, 2, 3, kWide, A5, W5, E8>(a, P, s);
+    return tile<64, 64, 2, 2, 4, kWide, A5, W5, E8>(a, P, s);
+  }
+  if constexpr (E8) {
+    if (big >= 256) return tile<256, 256, 4, 2, 2, kScaled8, A5, W5, E8>(a, P, s);
+    if (4 * big >= 256) return tile<128, 128, 4, 2, 4, kScaled8, A5, W5, E8>(a, P, s);
+    return tile<64, 64, 2, 2, 4, kScaled8, A5, W5, E8>(a, P, s);
+  } else {
+    if (2 * big >= 256) return tile<256, 128, 4, 2, 3, kPlain8, A5, W5, E8>(a, P, s);
+    return tile<64, 64, 2, 2, 4, kPlain8, A5, W5, E8>(a, P, s);
+  }
 }
 
 }  // namespace

@@ -109,16 +109,10 @@ __device__ __forceinline__ void store_codes8(uint8_t* p, uint2 w, int n) {
 template <int X>
 __global__ __launch_bounds__(kThreads) void echo_quant_rows_k(const QuantFp8Args a) {
   const int r = blockIdx.y;
-  const void* x = a.X[0];
-  uint8_t* q = a.rows.codes[0];
-  void* sc = a.rows.scales[0];
-#pragma unroll
-  for (int i = 1; i < kMaxRanks; ++i)
-    if (r == i) {
-      x = a.X[i];
-      q = a.rows.codes[i];
-      sc = a.rows.scales[i];
-    }
+  const auto* k = kernel_args<QuantFp8Args>();
+  const void* x = k->X[r];
+  uint8_t* q = k->rows.codes[r];
+  void* sc = k->rows.scales[r];
   const bool e5m2 = a.e5m2 != 0;
   const int64_t nb = (a.C + kFp8Block - 1) / kFp8Block, units = a.R * nb;
   const int l = threadIdx.x & 15;
@@ -162,18 +156,10 @@ __global__ __launch_bounds__(kThreads) void echo_quant_tile_k(const QuantFp8Args
   const int r = static_cast<int>(blockIdx.x / per);
   const int64_t at = blockIdx.x - r * per;
   const int64_t br = at / nbc, bc = at - br * nbc;
-  const void* x = a.X[0];
-  uint8_t *qr = a.rows.codes[0], *qc = a.cols.codes[0];
-  void *sr = a.rows.scales[0], *sc = a.cols.scales[0];
-#pragma unroll
-  for (int i = 1; i < kMaxRanks; ++i)
-    if (r == i) {
-      x = a.X[i];
-      qr = a.rows.codes[i];
-      sr = a.rows.scales[i];
-      qc = a.cols.codes[i];
-      sc = a.cols.scales[i];
-    }
+  const auto* k = kernel_args<QuantFp8Args>();
+  const void* x = k->X[r];
+  uint8_t *qr = k->rows.codes[r], *qc = k->cols.codes[r];
+  void *sr = k->rows.scales[r], *sc = k->cols.scales[r];
   const bool e5m2 = a.e5m2 != 0, e8m0 = a.e8m0 != 0;
   const int t = threadIdx.x, cg = t & 15, rg = t >> 4, wave = t >> 6;
   const int64_t row0 = br * kFp8Block + 8 * rg, col0 = bc * kFp8Block + 8 * cg;

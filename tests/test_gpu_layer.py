@@ -6,7 +6,16 @@ a power of two is exact and the generator is integer arithmetic.  A product's
 element is a sum of K exact products (8-bit mantissas), scaled: added in fp32 in any
 order, with at most one unit in the last place (2^-23) lost per addition and two per
 scaling and block, it is off by at most (K + 4 blocks) 2^-23 sum |a w|, and the
-rounding to the output type adds half a step of the value (finfo.eps / 2)."""
+rounding to the output type adds half a step of the value (finfo.eps / 2).
+
+Outputs of 16 bits come from the 8-bit matrix instruction where A has more than a few
+rows, and that instruction adds each run of 8 consecutive products in fixed point.  The
+run's unit is 2^-13 of the largest 2^(ea + ew) in it (ea, ew: the exponents of the two
+codes, at least the format's lowest), and every product is cut to a multiple of it,
+toward zero.  A product whose own 2^(ea + ew) is the largest has at most 6 fraction
+bits below it (3 + 3 for e4m3) and loses nothing; each of the other 7 loses less than
+one unit.  So a run is off by less than 7 * 2^-13 * max 2^(ea + ew), times the scales,
+and an element by the sum of that over its runs."""
 import numpy as np
 import pytest
 
@@ -156,11 +165,29 @@ def values(m, block):
     return dequantize(to_np64(m[0]), to_np64(m[1]), block)
 
 
-def assert_product(out, a, w):
+def exponents(m, block):
+    """2^e of every code (the lowest normal exponent for subnormals and zero), scaled."""
     torch = torch_()
+    low = -6 if m[0].dtype == torch.float8_e4m3fn else -14
+    c = np.abs(to_np64(m[0]))
+    e = np.maximum(np.frexp(c)[1] - 1, low)
+    return dequantize(np.where(c > 0, np.ldexp(1.0, e), 2.0 ** low), to_np64(m[1]), block)
+
+
+def assert_product(out, A, W, block_a=1, block_w=1, m=slice(None), n=slice(None)):
+    """out (rows m, columns n of the result) against A W^T in 64 bits."""
+    torch = torch_()
+    a, w = values(A, block_a)[m], values(W, block_w)[n]
     K = a.shape[1]
     want = a @ w.T
     tol = (K + 4 * (K // 128 + 1)) * 2.0 ** -23 * (np.abs(a) @ np.abs(w).T)
+    if out.dtype != torch.float32:
+        ea, ew = exponents(A, block_a)[m], exponents(W, block_w)[n]
+        for k in range(0, K, 8):
+            run = np.zeros_like(want)
+            for i in range(k, min(k + 8, K)):
+                np.maximum(run, np.outer(ea[:, i], ew[:, i]), out=run)
+            tol += 7 * 2.0 ** -13 * run
     tol += torch.finfo(out.dtype).eps / 2 * (np.abs(want) + tol) + (6e-8 if out.dtype == torch.float16 else 0.0)
     err = np.abs(to_np64(out) - want)
     assert (err <= tol).all(), f"off by up to {np.max(err / np.maximum(tol, 1e-300)):.3g} of the tolerance"
@@ -188,7 +215,7 @@ def test_product(E, cuda, M, N, K, scale, block):
             a.codes.copy_((a.codes.float() / 64).to(a.codes.dtype))
     E.echo_gemm_fp8(A, W, out)
     for r in range(P):
-        assert_product(out[r], values(A[r], 1), values(W[r], block))
+        assert_product(out[r], A[r], W[r], 1, block)
         assert (out[r].as_strided((M, 3), (N + 3, 1), N) == 7.0).all(), "columns behind the output were written"
 
 
@@ -200,12 +227,13 @@ SWEEP = [(m, n, k, p) for m, n, k, p in (
 
 @pytest.mark.parametrize("M,N,K,P", SWEEP)
 @pytest.mark.parametrize("scale,block", [("e8m0", 128), ("f32", 1), ("f32", 128)])
-def test_product_sizes(E, cuda, M, N, K, P, scale, block):
+@pytest.mark.parametrize("out_dtype", ["f32", "bf16"])
+def test_product_sizes(E, cuda, M, N, K, P, scale, block, out_dtype):
     """Sizes over the whole range of tilings, sampled rows and columns."""
     torch = torch_()
     A = [operand(E, cuda, 10 + r, M, K, "e4m3", scale, 1) for r in range(P)]
     W = [operand(E, cuda, 50 + r, N, K, "e4m3", scale, block) for r in range(P)]
-    out = [torch.full((M, N), float("nan"), dtype=torch.float32, device=cuda) for _ in range(P)]
+    out = [torch.full((M, N), float("nan"), dtype=dt(out_dtype), device=cuda) for _ in range(P)]
     E.echo_gemm_fp8(A, W, out)
     g = np.random.default_rng(1)
     for r in range(P):
@@ -213,7 +241,7 @@ def test_product_sizes(E, cuda, M, N, K, P, scale, block):
         m = np.unique(np.r_[0, M - 1, g.integers(0, M, 40)])
         n = np.unique(np.r_[0, N - 1, g.integers(0, N, 40)])
         sub = out[r][torch.from_numpy(m).to(cuda)][:, torch.from_numpy(n).to(cuda)]
-        assert_product(sub, values(A[r], 1)[m], values(W[r], block)[n])
+        assert_product(sub, A[r], W[r], 1, block, m, n)
 
 
 def test_product_block_rows_on_both_sides_and_broadcast_scales(E, cuda):
@@ -223,10 +251,10 @@ def test_product_block_rows_on_both_sides_and_broadcast_scales(E, cuda):
     W = operand(E, cuda, 2, N, K, "e4m3", "f32", 128)
     out = torch.empty(M, N, dtype=torch.float32, device=cuda)
     E.echo_gemm_fp8([A], [W], [out])
-    assert_product(out, values(A, 128), values(W, 128))
+    assert_product(out, A, W, 128, 128)
     one = torch.tensor([[0.375]], device=cuda)
     E.echo_gemm_fp8([(A.codes, one.expand(M, 3))], [(W.codes, one.expand(2, 3))], [out])
-    assert_product(out, to_np64(A.codes) * 0.375, to_np64(W.codes) * 0.375)
+    assert_product(out, (A.codes, one.expand(M, 3)), (W.codes, one.expand(2, 3)), 1, 128)
 
 
 def test_product_over_nothing_gives_zeros(E, cuda):
@@ -267,7 +295,7 @@ def test_product_into_columns_of_one_buffer(E, cuda):
     whole = torch.zeros(M, P * N, dtype=torch.bfloat16, device=cuda)
     E.echo_gemm_fp8(A, W, [whole[:, r * N:(r + 1) * N] for r in range(P)])
     for r in range(P):
-        assert_product(whole[:, r * N:(r + 1) * N], values(A[r], 1), values(W[r], 128))
+        assert_product(whole[:, r * N:(r + 1) * N], A[r], W[r], 1, 128)
     with pytest.raises(E.EchoError):
         E.echo_gemm_fp8(A[:2], W[:2], [whole[:, 0:N], whole[:, 1:N + 1]])
 
