@@ -418,14 +418,6 @@ def echo_debug_views(state: EchoState, direction: int = ECHO_FWD) -> dict:
 # ---- operators of the layer around the all-reduce ---------------------------
 
 
-def _elem_type(dtype, what: str) -> int:
-    import torch
-    d = {torch.float32: ECHO_F32, torch.bfloat16: ECHO_BF16, torch.float16: ECHO_F16}
-    if dtype not in d:
-        raise EchoError(ECHO_ERR_DTYPE, f"{what}: {dtype}, expected float32, bfloat16 or float16")
-    return d[dtype]
-
-
 def _fp8_blocks(n: int) -> int:
     return (n + ECHO_FP8_BLOCK - 1) // ECHO_FP8_BLOCK
 
@@ -456,137 +448,46 @@ class EchoFp8(NamedTuple):
         return cls(codes, torch.empty(_fp8_blocks(k), n, dtype=types[scale], device=device).t())
 
 
-def _same_device(tensors, what: str):
-    """The one GPU the tensors are on."""
-    dev = tensors[0].device
-    if dev.type != "cuda" or any(t.device != dev for t in tensors):
-        raise EchoError(ECHO_ERR_ARG, f"{what}: every tensor must be on one GPU")
-    return dev
+_marshal = None  # the extension module that reads the tensors (built with libecho)
+_raw_current = None  # device index -> handle of torch's current stream
 
 
-class _OnDevice:
-    """The device made current for a call, where it is not already."""
-
-    def __init__(self, device):
-        import torch
-        self.guard = None if torch.cuda.current_device() == device.index else torch.cuda.device(device)
-
-    def __enter__(self):
-        if self.guard is not None:
-            self.guard.__enter__()
-
-    def __exit__(self, *exc):
-        if self.guard is not None:
-            self.guard.__exit__(*exc)
-
-
-def _pointers(tensors):
-    return (ctypes.c_void_p * len(tensors))(*[t.data_ptr() for t in tensors])
+def _native():
+    global _marshal, _raw_current
+    if _marshal is None:
+        import torch  # its libraries must be loaded before the module's
+        load_library()
+        path = os.path.join(_PKG, "_echo_marshal.so")
+        if not os.path.exists(path):
+            from . import build
+            build.build_marshal()
+        from . import _echo_marshal
+        _raw_current = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+            (lambda index: torch.cuda.current_stream(index).cuda_stream)
+        _marshal = _echo_marshal
+    return _marshal
 
 
-def _fp8_struct(mats, rows: int, k: int, what: str) -> _Fp8Struct:
-    """Marshal P matrices [rows, k] of one layout."""
-    import torch
-    formats = {torch.float8_e4m3fn: ECHO_E4M3, torch.float8_e5m2: ECHO_E5M2}
-    types = {torch.float32: ECHO_SCALE_F32, torch.float8_e8m0fnu: ECHO_SCALE_E8M0}
-    codes, scales = [m[0] for m in mats], [m[1] for m in mats]
-    c, s = codes[0], scales[0]
-    if c.dtype not in formats or s.dtype not in types:
-        raise EchoError(ECHO_ERR_DTYPE, f"{what}: codes {c.dtype}, scales {s.dtype}")
-    kb = _fp8_blocks(k)
-    if tuple(s.shape) == (rows, kb):
-        block_rows = 1
-    elif tuple(s.shape) == (_fp8_blocks(rows), kb):
-        block_rows = ECHO_FP8_BLOCK
-    else:
-        raise EchoError(ECHO_ERR_ARG, f"{what}: scales {tuple(s.shape)} of codes [{rows}, {k}]")
-    for x, y in zip(codes, scales):
-        if tuple(x.shape) != (rows, k) or x.dtype != c.dtype or x.stride() != c.stride() or (k > 1 and x.stride(1) != 1):
-            raise EchoError(ECHO_ERR_ARG, f"{what}: codes must be [{rows}, {k}] {c.dtype}, k contiguous, of one pitch")
-        if y.shape != s.shape or y.dtype != s.dtype or y.stride() != s.stride():
-            raise EchoError(ECHO_ERR_ARG, f"{what}: scales must be of one shape, type and layout")
-    f = _Fp8Struct()
-    f.codes, f.scales = _pointers(codes), _pointers(scales)
-    f.ld = c.stride(0) if rows > 1 else (k + 15) // 16 * 16  # the pitch of a single row says nothing
-    f.scale_row_stride, f.scale_k_stride = s.stride()
-    f.format, f.scale_type, f.block_rows = formats[c.dtype], types[s.dtype], block_rows
-    return f
-
-
-def _matrices(mats, what: str):
-    """Shape, pitch and type of P matrices with contiguous rows."""
-    x = mats[0]
-    if x.dim() != 2:
-        raise EchoError(ECHO_ERR_ARG, f"{what} must be matrices")
-    rows, cols = x.shape
-    for t in mats:
-        if t.shape != x.shape or t.dtype != x.dtype or t.stride() != x.stride() or (cols > 1 and t.stride(1) != 1):
-            raise EchoError(ECHO_ERR_ARG, f"{what} must be of one shape, type and pitch, with contiguous rows")
-    return rows, cols, (x.stride(0) if rows > 1 else cols)
+def _raise_if(refused):
+    if refused is not None:
+        raise EchoError(*refused)
 
 
 def echo_quantize_fp8(X: Sequence, rows: Sequence = None, cols: Sequence = None, stream=None):
     """Quantize P matrices X_r [R, C] (float32, bfloat16 or float16) to 8-bit floating
     point in one pass: ``rows`` (P EchoFp8 of [R, C], or None) receives blocks along
     the rows, ``cols`` (P EchoFp8 of [C, R], or None) the transposes."""
-    X = list(X)
-    if not X or (rows is None and cols is None):
-        raise EchoError(ECHO_ERR_ARG, "echo_quantize_fp8: at least one matrix and one of rows and cols")
-    if any(o is not None and len(o) != len(X) for o in (rows, cols)):
-        raise EchoError(ECHO_ERR_ARG, "echo_quantize_fp8: as many outputs as matrices")
-    R, C, ldx = _matrices(X, "X")
-    dtype = _elem_type(X[0].dtype, "X")
-    dev = _same_device(X + [t for o in (rows, cols) if o is not None for m in o for t in m], "echo_quantize_fp8")
-    fr = None if rows is None else _fp8_struct(rows, R, C, "rows")
-    fc = None if cols is None else _fp8_struct(cols, C, R, "cols")
-    if fr is not None and fc is not None:  # one row is a row and a block of rows: it goes by the other orientation
-        if R == 1:
-            fr.block_rows = fc.block_rows
-        elif C == 1:
-            fc.block_rows = fr.block_rows
-    with _OnDevice(dev):
-        _check(load_library().echo_quantize_fp8(_pointers(X), len(X), R, C, ldx, dtype,
-                                                None if fr is None else ctypes.byref(fr),
-                                                None if fc is None else ctypes.byref(fc),
-                                                _stream_handle(stream, dev)), "echo_quantize_fp8")
+    _raise_if((_marshal or _native()).quantize_fp8(X, rows, cols, None if stream is None else stream.cuda_stream,
+                                                   _raw_current))
 
 
 def echo_gemm_fp8(A: Sequence, W: Sequence, out: Sequence, stream=None):
     """out[r] = A_r @ W_r.T for matrices in 8-bit floating point (A_r [M, K], W_r
     [N, K] as EchoFp8 of either format and block height and one scale type; out[r]
     [M, N] float32, bfloat16 or float16)."""
-    A, W, out = list(A), list(W), list(out)
-    P = len(A)
-    if P < 1 or len(W) != P or len(out) != P:
-        raise EchoError(ECHO_ERR_ARG, "A, W and out must hold the same number (>= 1) of matrices")
-    if A[0][0].dim() != 2 or W[0][0].dim() != 2:
-        raise EchoError(ECHO_ERR_ARG, "A and W must be matrices")
-    M, K = A[0][0].shape
-    N = W[0][0].shape[0]
-    fa, fw = _fp8_struct(A, M, K, "A"), _fp8_struct(W, N, K, "W")
-    om, on, ldo = _matrices(out, "out")
-    if (om, on) != (M, N):
-        raise EchoError(ECHO_ERR_ARG, f"out must be [{M}, {N}]")
-    dtype = _elem_type(out[0].dtype, "out")
-    dev = _same_device(out + [t for m in A + W for t in m], "echo_gemm_fp8")
-    with _OnDevice(dev):
-        _check(load_library().echo_gemm_fp8(ctypes.byref(fa), ctypes.byref(fw), _pointers(out), P, M, N, K, ldo,
-                                            dtype, _stream_handle(stream, dev)), "echo_gemm_fp8")
+    _raise_if((_marshal or _native()).gemm_fp8(A, W, out, None if stream is None else stream.cuda_stream,
+                                               _raw_current))
     return out
-
-
-def _row_layout(t, shape, what: str):
-    """(rows, cols, pitch) of a tensor of ``shape``: any contiguous one, or a matrix
-    with contiguous rows."""
-    if tuple(t.shape) != tuple(shape):
-        raise EchoError(ECHO_ERR_ARG, f"{what} must be {tuple(shape)}")
-    cols = t.shape[-1] if t.dim() else 1
-    rows = t.numel() // cols if cols else 0
-    if t.is_contiguous():
-        return rows, cols, cols
-    if t.dim() != 2 or (cols > 1 and t.stride(1) != 1):
-        raise EchoError(ECHO_ERR_ARG, f"{what} must be contiguous, or a matrix with contiguous rows")
-    return rows, cols, t.stride(0)
 
 
 def echo_dropout_add(x, out, p: float, rng, residual=None, offset: int = 0, first: int = 0, stream=None):
@@ -595,24 +496,9 @@ def echo_dropout_add(x, out, p: float, rng, residual=None, offset: int = 0, firs
     step); ``offset`` is added to the step (which of a step's dropouts this is);
     ``first``: index of the first element in the whole message, for a rank that
     holds a part of it.  out may be x or the residual itself."""
-    import torch
-    tensors = [x, out, rng] + ([] if residual is None else [residual])
-    dev = _same_device(tensors, "echo_dropout_add")
-    rows, cols, ldx = _row_layout(x, x.shape, "x")
-    _, _, ldo = _row_layout(out, x.shape, "out")
-    ldr = cols
-    if residual is not None:
-        if residual.dtype != out.dtype:
-            raise EchoError(ECHO_ERR_DTYPE, f"residual {residual.dtype}, out {out.dtype}")
-        _, _, ldr = _row_layout(residual, x.shape, "residual")
-    if rng.dtype != torch.int64 or rng.numel() != 2 or not rng.is_contiguous():
-        raise EchoError(ECHO_ERR_ARG, "rng must be a contiguous int64 tensor of 2 elements")
-    offset = (int(offset) + (1 << 63)) % (1 << 64) - (1 << 63)  # the step wraps at 64 bits
-    if not 0 <= int(first) < 1 << 63:
+    if not 0 <= first < 1 << 63:
         raise EchoError(ECHO_ERR_ARG, f"first {first}")
-    with _OnDevice(dev):
-        _check(load_library().echo_dropout_add(
-            x.data_ptr(), None if residual is None else residual.data_ptr(), out.data_ptr(), rows, cols, ldx, ldr,
-            ldo, _elem_type(x.dtype, "x"), _elem_type(out.dtype, "out"), float(p), rng.data_ptr(), offset,
-            int(first), _stream_handle(stream, dev)), "echo_dropout_add")
+    offset = (offset + (1 << 63)) % (1 << 64) - (1 << 63)  # the step wraps at 64 bits
+    _raise_if((_marshal or _native()).dropout_add(x, residual, out, p, rng, offset, first,
+                                                  None if stream is None else stream.cuda_stream, _raw_current))
     return out

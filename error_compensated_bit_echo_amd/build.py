@@ -1,4 +1,5 @@
-"""Build libecho.so (HIP kernels + C ABI) in-tree for gfx950 with hipcc.
+"""Build libecho.so (HIP kernels + C ABI) in-tree for gfx950 with hipcc, and the
+extension module that marshals torch tensors into its layer operators with g++.
 
 Usage: ``python -m error_compensated_bit_echo_amd.build`` (or call
 :func:`build_library`).  The library lands next to this file.
@@ -47,7 +48,7 @@ def _run(cmd, verbose):
         print(" ".join(cmd), flush=True)
     res = subprocess.run(cmd, capture_output=True, text=True)
     if res.returncode != 0:
-        raise RuntimeError(f"hipcc failed ({res.returncode}):\n{res.stdout}\n{res.stderr}")
+        raise RuntimeError(f"{os.path.basename(cmd[0])} failed ({res.returncode}):\n{res.stdout}\n{res.stderr}")
 
 
 def build_library(verbose: bool = False, jobs: int = 0) -> str:
@@ -69,11 +70,39 @@ def build_library(verbose: bool = False, jobs: int = 0) -> str:
         # the host pass does not know the gfx feature flag; that warning is expected
         _run([cc, f"--offload-arch={ARCH}", "-shared", "-fPIC", *objs, "-o", tmp], verbose)
         os.replace(tmp, LIB)
+        build_marshal(verbose)
     finally:
         if os.path.exists(tmp):
             os.unlink(tmp)
         shutil.rmtree(tmpdir, ignore_errors=True)
     return LIB
+
+
+MARSHAL_SRC = os.path.join(CSRC, "echo_marshal.cpp")
+MARSHAL = os.path.join(PKG, "_echo_marshal.so")
+
+
+def build_marshal(verbose: bool = False) -> str:
+    """Compile the extension module (CPython, torch's C++ tensors) against the built
+    libecho.so; returns its path."""
+    import sysconfig
+
+    from torch.utils import cpp_extension
+    rocm = os.path.dirname(os.path.dirname(os.path.realpath(hipcc())))
+    tmp = MARSHAL + f".tmp{os.getpid()}"
+    includes = [*cpp_extension.include_paths(), sysconfig.get_paths()["include"], os.path.join(rocm, "include")]
+    cmd = [shutil.which("g++") or "g++", "-std=c++17", "-O2", "-fPIC", "-shared", "-Wall", "-Wextra", "-Wno-unused-parameter",
+           "-D__HIP_PLATFORM_AMD__", "-DUSE_ROCM", f"-I{INCLUDE}", *[a for i in includes for a in ("-isystem", i)],
+           MARSHAL_SRC, "-o", tmp, f"-L{PKG}", "-lecho", "-Wl,-rpath,$ORIGIN",
+           *[f"-L{d}" for d in cpp_extension.library_paths()], "-lc10", "-ltorch_cpu", "-ltorch_python",
+           f"-L{os.path.join(rocm, 'lib')}", "-lamdhip64"]
+    try:
+        _run(cmd, verbose)
+        os.replace(tmp, MARSHAL)
+    finally:
+        if os.path.exists(tmp):
+            os.unlink(tmp)
+    return MARSHAL
 
 
 C_CLIENT_SRC = os.path.join(ROOT, "tests", "c_client", "echo_c_client.c")
