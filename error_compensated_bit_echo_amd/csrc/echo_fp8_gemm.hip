@@ -27,7 +27,6 @@ typedef int i32x8 __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
-typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 
 // 8 codes (two dwords) as bfloat16, exactly.
@@ -231,11 +230,14 @@ __global__ __launch_bounds__(64 * WM * WN) void echo_gemm_fp8_tile_k(const GemmF
   constexpr int RW = BM / WM, CW = BN / WN, MI = RW / 32, NJ = CW / 32;
   constexpr int JA = BM / (8 * NW), JW = BN / (8 * NW), kLoads = JA + JW;  // 1 KiB slab blocks per wavefront
   static_assert(MI * 32 * WM == BM && NJ * 32 * WN == BN && JA * 8 * NW == BM && JW * 8 * NW == BN, "even splits");
+  static_assert(BM % 64 == 0 && BN % 64 == 0, "a wavefront stages scales of one operand");
   constexpr int kSlabA = BM * 128, kSlab = (BM + BN) * 128;
-  constexpr int kRows = BM + BN;                              // rows with a scale
-  constexpr int kPer = (kRows + kThreads - 1) / kThreads;     // scales per thread
-  __shared__ __attribute__((aligned(1024))) uint8_t lds[S * kSlab];
-  __shared__ __attribute__((aligned(16))) uint32_t sc[3][kRows];
+  constexpr int kPer = (BM + BN + kThreads - 1) / kThreads;  // scales per thread
+  constexpr int kRows = kPer * kThreads;                     // rows with a scale, rounded up to whole threads
+  // one array for slabs and scales: with two, the compiler tells the accesses of each
+  // apart and then waits for every load into LDS before the next fragment read
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[S * kSlab + 3 * 4 * kRows];
+  const auto sc = reinterpret_cast<uint32_t(*)[kRows]>(lds + S * kSlab);
 
   // The hardware hands the workgroups of a launch to the eight XCDs in turn, and each
   // XCD has its own L2: workgroup i takes a tile of the (i % 8)-th contiguous run, and
@@ -247,85 +249,80 @@ __global__ __launch_bounds__(64 * WM * WN) void echo_gemm_fp8_tile_k(const GemmF
   id -= r * gm * gn;
   const uint32_t band = id / (8 * gn), in_band = id - band * 8 * gn;
   const uint32_t high = gm - 8 * band < 8 ? gm - 8 * band : 8;  // row tiles of this band
-  const int64_t m0 = static_cast<int64_t>(8 * band + in_band % high) * BM;
-  const int64_t n0 = static_cast<int64_t>(in_band / high) * BN;
+  const int m0 = static_cast<int>(8 * band + in_band % high) * BM, n0 = static_cast<int>(in_band / high) * BN;
   const RankPtrs p = rank_ptrs(r);
+  const int M = static_cast<int>(a.M), N = static_cast<int>(a.N), K = static_cast<int>(a.K);
 
-  const int t = threadIdx.x, lane = t & 63, wave = t >> 6, wm = wave / WN, wn = wave % WN, half = lane >> 5;
-  const int64_t steps = (a.K + 127) / 128;
-  const int64_t K16 = (a.K + 15) / 16 * 16;
-  const int64_t rows_a = a.M - m0 < BM ? a.M - m0 : BM, rows_w = a.N - n0 < BN ? a.N - n0 : BN;
+  const int t = threadIdx.x, lane = t & 63, half = lane >> 5;
+  const int wave = __builtin_amdgcn_readfirstlane(t >> 6), wm = wave / WN, wn = wave % WN;
+  const int steps = (K + 127) / 128, K16 = (K + 15) / 16 * 16;
+  const int rows_a = M - m0 < BM ? M - m0 : BM, rows_w = N - n0 < BN ? N - n0 : BN;
   const BufRsrc rA = buffer_rsrc(p.A + m0 * a.lda, static_cast<int32_t>((rows_a - 1) * a.lda + K16));
   const BufRsrc rW = buffer_rsrc(p.W + n0 * a.ldw, static_cast<int32_t>((rows_w - 1) * a.ldw + K16));
   // Lane l fills slot l of each 1 KiB block: row 8 i + l / 8, slot l % 8.
   uint32_t offA[JA], offW[JW];
+  const auto chunk_of = [&](int row) { return (lane & 7) ^ ((row >> 1) & 7); };
 #pragma unroll
   for (int j = 0; j < JA; ++j) {
     const int row = 8 * (JA * wave + j) + (lane >> 3);
-    offA[j] = static_cast<uint32_t>(row * a.lda + 16 * ((lane & 7) ^ ((row >> 1) & 7)));
+    offA[j] = static_cast<uint32_t>(row * static_cast<int>(a.lda) + 16 * chunk_of(row));
   }
 #pragma unroll
   for (int j = 0; j < JW; ++j) {
     const int row = 8 * (JW * wave + j) + (lane >> 3);
-    offW[j] = static_cast<uint32_t>(row * a.ldw + 16 * ((lane & 7) ^ ((row >> 1) & 7)));
+    offW[j] = static_cast<uint32_t>(row * static_cast<int>(a.ldw) + 16 * chunk_of(row));
   }
-  auto issue = [&](int buf, int64_t it) {
-    uint8_t* As = lds + buf * kSlab;
-    uint8_t* Ws = As + kSlabA;
-    const uint32_t kb = static_cast<uint32_t>(it * 128);
-    if (it + 1 < steps || K16 % 128 == 0) {
+  // The loads of K step `it` into slab `buf`; `last`: of the last step, whose chunks
+  // past K16 read as zeros.
+  auto issue = [&](int buf, int it, auto last) {
+    uint8_t* As = lds + buf * kSlab + 1024 * JA * wave;
+    uint8_t* Ws = lds + buf * kSlab + kSlabA + 1024 * JW * wave;
+    const int chunks = (K16 - it * 128) / 16;
 #pragma unroll
-      for (int j = 0; j < JA; ++j) buffer_load_lds16<0>(rA, As + 1024 * (JA * wave + j), offA[j], kb);
+    for (int j = 0; j < JA; ++j) {
+      uint32_t off = offA[j];
+      if constexpr (decltype(last)::value) off = chunk_of(8 * (JA * wave + j) + (lane >> 3)) < chunks ? off : kPastEnd;
+      buffer_load_lds16<0>(rA, As + 1024 * j, off, static_cast<uint32_t>(it * 128));
+    }
 #pragma unroll
-      for (int j = 0; j < JW; ++j) buffer_load_lds16<0>(rW, Ws + 1024 * (JW * wave + j), offW[j], kb);
-    } else {  // the last step of a K that is no multiple of 128
-      const int chunks = static_cast<int>((K16 - it * 128) / 16);
-#pragma unroll
-      for (int j = 0; j < JA; ++j) {
-        const int row = 8 * (JA * wave + j) + (lane >> 3);
-        const bool in = ((lane & 7) ^ ((row >> 1) & 7)) < chunks;
-        buffer_load_lds16<0>(rA, As + 1024 * (JA * wave + j), in ? offA[j] : kPastEnd, kb);
-      }
-#pragma unroll
-      for (int j = 0; j < JW; ++j) {
-        const int row = 8 * (JW * wave + j) + (lane >> 3);
-        const bool in = ((lane & 7) ^ ((row >> 1) & 7)) < chunks;
-        buffer_load_lds16<0>(rW, Ws + 1024 * (JW * wave + j), in ? offW[j] : kPastEnd, kb);
-      }
+    for (int j = 0; j < JW; ++j) {
+      uint32_t off = offW[j];
+      if constexpr (decltype(last)::value) off = chunk_of(8 * (JW * wave + j) + (lane >> 3)) < chunks ? off : kPastEnd;
+      buffer_load_lds16<0>(rW, Ws + 1024 * j, off, static_cast<uint32_t>(it * 128));
     }
   };
   // The scales: thread t stages rows t, t + kThreads, ... of A's then W's.
-  const void* sp[kPer];
-  int64_t sat[kPer], sk[kPer];
+  constexpr int kScaleBytes = E8 ? 1 : 4;
+  const uint8_t* sp[kPer];
+  int64_t sk[kPer];
 #pragma unroll
   for (int u = 0; u < kPer; ++u) {
-    int row = t + u * kThreads;
-    row = row < kRows ? row : kRows - 1;
-    const bool of_a = row < BM;
-    int64_t i = of_a ? m0 + row : n0 + row - BM;
-    const int64_t end = of_a ? a.M : a.N;
+    const bool of_a = 64 * (wave + u * NW) < BM;
+    int i = t + u * kThreads + (of_a ? m0 : n0 - BM);
+    const int end = of_a ? M : N;
     i = i < end ? i : end - 1;  // past the edge: any scale does
-    sp[u] = of_a ? p.sA : p.sW;
-    sat[u] = of_a ? (i >> a.sa_shift) * a.sa_row : (i >> a.sw_shift) * a.sw_row;
-    sk[u] = of_a ? a.sa_k : a.sw_k;
+    sp[u] = static_cast<const uint8_t*>(of_a ? p.sA : p.sW) +
+            (of_a ? (i >> a.sa_shift) * a.sa_row : (i >> a.sw_shift) * a.sw_row) * kScaleBytes;
+    sk[u] = (of_a ? a.sa_k : a.sw_k) * kScaleBytes;
   }
   uint32_t sreg[kPer];
-  auto load_scales = [&](int64_t it) {
+  auto load_scales = [&]() {  // the next K step's
 #pragma unroll
-    for (int u = 0; u < kPer; ++u) sreg[u] = scale_bits<E8>(sp[u], sat[u] + it * sk[u]);
+    for (int u = 0; u < kPer; ++u) {
+      sreg[u] = scale_bits<E8>(sp[u], 0);
+      sp[u] += sk[u];
+    }
   };
   auto stage_scales = [&](int ring) {
 #pragma unroll
     for (int u = 0; u < kPer; ++u)
-      if (t + u * kThreads < kRows)
-        sc[ring][t + u * kThreads] =
-            MODE == kScaled8 ? sreg[u] : __float_as_uint(scale_value<E8>(sreg[u]));
+      sc[ring][t + u * kThreads] = MODE == kScaled8 ? sreg[u] : __float_as_uint(scale_value<E8>(sreg[u]));
   };
   // Bytes behind K in the last chunk of the last slab, on both sides (a NaN there
   // would survive a product with zero).
   auto clear_tail = [&](uint8_t* slab) {
-    const int c = static_cast<int>(a.K % 128) / 16, n = static_cast<int>(a.K % 16);
-    for (int row = t; row < kRows; row += kThreads) {
+    const int c = K % 128 / 16, n = K % 16;
+    for (int row = t; row < BM + BN; row += kThreads) {
       const int in = row < BM ? row : row - BM;
       uint8_t* b = slab + row * 128 + 16 * (c ^ ((in >> 1) & 7));
       for (int i = n; i < 16; ++i) b[i] = 0;
@@ -348,21 +345,31 @@ __global__ __launch_bounds__(64 * WM * WN) void echo_gemm_fp8_tile_k(const GemmF
   // between two sets with the 8-bit instruction).
   constexpr int kSetsA = MODE == kWide ? 1 : 2;
   i32x4 fa[kSetsA][MI][2], fw[NJ][2];
-  auto read_a = [&](int set, const uint8_t* slab, int hs, int c) {
+  int at[2][2];  // byte offset of this lane's chunk c of half step hs in a 32-row sub-tile
 #pragma unroll
-    for (int i = 0; i < MI; ++i) {
-      const int row = RW * wm + 32 * i + (lane & 31), ch = 4 * half + 2 * hs + c;
-      fa[set][i][c] = *reinterpret_cast<const i32x4*>(slab + row * 128 + 16 * (ch ^ ((row >> 1) & 7)));
-    }
+  for (int hs = 0; hs < 2; ++hs)
+#pragma unroll
+    for (int c = 0; c < 2; ++c) at[hs][c] = (lane & 31) * 128 + 16 * ((4 * half + 2 * hs + c) ^ ((lane >> 1) & 7));
+  auto read_a = [&](int set, int slab, int hs, int c) {
+    const uint8_t* b = lds + slab * kSlab + RW * wm * 128 + at[hs][c];
+#pragma unroll
+    for (int i = 0; i < MI; ++i) fa[set][i][c] = *reinterpret_cast<const i32x4*>(b + 4096 * i);
   };
-  auto read_w = [&](int j, const uint8_t* slab, int hs, int c) {
-    const int row = CW * wn + 32 * j + (lane & 31), ch = 4 * half + 2 * hs + c;
-    fw[j][c] = *reinterpret_cast<const i32x4*>(slab + kSlabA + row * 128 + 16 * (ch ^ ((row >> 1) & 7)));
+  auto read_w = [&](int j, int slab, int hs, int c) {
+    const uint8_t* b = lds + slab * kSlab + kSlabA + CW * wn * 128 + at[hs][c];
+    fw[j][c] = *reinterpret_cast<const i32x4*>(b + 4096 * j);
   };
-  uint32_t ea[MI], ew[NJ];  // kScaled8: the step's scale bytes of the rows this lane supplies
+  // kScaled8: the scale bytes of the rows this lane supplies, this step's and the next's
+  uint32_t ea[MI], ew[NJ], ea1[MI], ew1[NJ];
+  auto read_scales = [&](int ring, uint32_t* sa, uint32_t* sw) {
+#pragma unroll
+    for (int i = 0; i < MI; ++i) sa[i] = sc[ring][RW * wm + 32 * i + (lane & 31)];
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) sw[j] = sc[ring][BM + CW * wn + 32 * j + (lane & 31)];
+  };
   // The instructions of half step HS, reading the next one's fragments (READ) from
-  // `slab`.
-  auto half_step = [&](auto hs, auto read, const uint8_t* slab) {
+  // slab `slab`.
+  auto half_step = [&](auto hs, auto read, int slab) {
     constexpr int HS = decltype(hs)::value;
     constexpr bool READ = decltype(read)::value;
     [[maybe_unused]] const f32x16 zero{};
@@ -419,51 +426,56 @@ __global__ __launch_bounds__(64 * WM * WN) void echo_gemm_fp8_tile_k(const GemmF
   };
   constexpr std::integral_constant<int, 0> H0{};
   constexpr std::integral_constant<int, 1> H1{};
+  constexpr std::true_type kYes{};
+  constexpr std::false_type kNo{};
 
-  load_scales(0);
-#pragma unroll
-  for (int s = 0; s < S - 1; ++s)
-    if (s < steps) issue(s, s);
+  load_scales();
+  for (int s = 0; s < S - 1 && s < steps; ++s) {
+    if (s + 1 < steps) issue(s, s, kNo);
+    else issue(s, s, kYes);
+  }
   stage_scales(0);
   if (steps >= S - 1)
     __builtin_amdgcn_s_waitcnt(vmcnt_at_most_lds_drained((S - 2) * kLoads));
   else
     __builtin_amdgcn_s_waitcnt(vmcnt_at_most_lds_drained(0));
   slab_barrier();
-  if (steps == 1 && a.K % 16 != 0) clear_tail(lds);
+  if (steps == 1 && K % 16 != 0) clear_tail(lds);
+  if constexpr (MODE == kScaled8) read_scales(0, ea, ew);
+#pragma unroll
   for (int c = 0; c < 2; ++c) {
-    read_a(0, lds, 0, c);
-    for (int j = 0; j < NJ; ++j) read_w(j, lds, 0, c);
+    read_a(0, 0, 0, c);
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) read_w(j, 0, 0, c);
   }
   int cur = 0, ring = 0;  // slab and scales of the step
-  auto step = [&](int64_t it, auto last) {
+  // One K step.  ISSUE: the loads of step it + S - 1 go out at its start, into the slab
+  // step it - 1 used (2: they are the last step's).  Between its halves: the scales of
+  // the next step are staged, this wavefront's reads of the slab are done, the next
+  // slab has landed, and the barrier; LAST: none of that.  The steps of the main loop
+  // have no branch between the halves: the compiler would move the first half's
+  // instructions past it, behind the barrier.
+  auto step = [&](int it, auto issues, auto last) {
+    constexpr int ISSUE = decltype(issues)::value;
     constexpr bool LAST = decltype(last)::value;
-    const bool more = it + S - 1 < steps;
     const int next = cur + 1 == S ? 0 : cur + 1, ring1 = ring == 2 ? 0 : ring + 1;
     if constexpr (!LAST) {
-      load_scales(it + 1);
-      if (more) issue(cur == 0 ? S - 1 : cur - 1, it + S - 1);  // into the slab step it - 1 used
+      load_scales();
+      if constexpr (ISSUE == 1) issue(cur == 0 ? S - 1 : cur - 1, it + S - 1, kNo);
+      if constexpr (ISSUE == 2) issue(cur == 0 ? S - 1 : cur - 1, it + S - 1, kYes);
     }
-    if constexpr (MODE == kScaled8) {
-#pragma unroll
-      for (int i = 0; i < MI; ++i) ea[i] = sc[ring][RW * wm + 32 * i + (lane & 31)];
-#pragma unroll
-      for (int j = 0; j < NJ; ++j) ew[j] = sc[ring][BM + CW * wn + 32 * j + (lane & 31)];
-    }
-    half_step(H0, std::true_type{}, lds + cur * kSlab);
+    half_step(H0, kYes, cur);
     if constexpr (!LAST) {
       stage_scales(ring1);
-      // this wavefront's reads of the slab are done and the next slab has landed
-      if (more)
-        __builtin_amdgcn_s_waitcnt(vmcnt_at_most_lds_drained((S - 2) * kLoads));
-      else
-        __builtin_amdgcn_s_waitcnt(vmcnt_at_most_lds_drained(0));
+      __builtin_amdgcn_s_waitcnt(vmcnt_at_most_lds_drained(ISSUE != 0 ? (S - 2) * kLoads : 0));
+      __builtin_amdgcn_sched_barrier(0);
       slab_barrier();
-      uint8_t* An = lds + next * kSlab;
-      if (it + 2 == steps && a.K % 16 != 0) clear_tail(An);
-      half_step(H1, std::true_type{}, An);
+      if constexpr (ISSUE != 1)
+        if (it + 2 == steps && K % 16 != 0) clear_tail(lds + next * kSlab);
+      if constexpr (MODE == kScaled8) read_scales(ring1, ea1, ew1);
+      half_step(H1, kYes, next);
     } else {
-      half_step(H1, std::false_type{}, nullptr);
+      half_step(H1, kNo, 0);
     }
     if constexpr (MODE != kScaled8) {
 #pragma unroll
@@ -480,55 +492,69 @@ __global__ __launch_bounds__(64 * WM * WN) void echo_gemm_fp8_tile_k(const GemmF
             acc[i][j][v] = __builtin_fmaf(blk[i][j][v], ca * cw[v >> 2][v & 3], acc[i][j][v]);
         }
       }
+    } else if constexpr (!LAST) {
+#pragma unroll
+      for (int i = 0; i < MI; ++i) ea[i] = ea1[i];
+#pragma unroll
+      for (int j = 0; j < NJ; ++j) ew[j] = ew1[j];
     }
     cur = next;
     ring = ring1;
   };
-  for (int64_t it = 0; it + 1 < steps; ++it) step(it, std::false_type{});
-  step(steps - 1, std::true_type{});
+  int it = 0;
+  for (; it < steps - S; ++it) step(it, std::integral_constant<int, 1>{}, kNo);
+  if (it == steps - S) step(it++, std::integral_constant<int, 2>{}, kNo);
+  for (; it < steps - 1; ++it) step(it, std::integral_constant<int, 0>{}, kNo);
+  step(it, std::integral_constant<int, 0>{}, kYes);
 
   // Out from the accumulators.  fp32: runs of 4 columns, 16 bytes.  16 bits: the two
   // halves of the wavefront exchange runs (v_permlane32_swap), so a lane holds 8
-  // consecutive columns, 16 bytes.
+  // consecutive columns, 16 bytes.  Sub-tiles over the right edge go one by one.
+  const auto store = [&](auto elem) {
+    constexpr int E = decltype(elem)::value;
 #pragma unroll
-  for (int i = 0; i < MI; ++i) {
-    const int64_t m = m0 + RW * wm + 32 * i + (lane & 31);
+    for (int i = 0; i < MI; ++i) {
+      const int m = m0 + RW * wm + 32 * i + (lane & 31);
+      const bool in = m < M;
+      typename ElemOf<E>::T* row = static_cast<typename ElemOf<E>::T*>(p.out) + m * a.ldo;
 #pragma unroll
-    for (int j = 0; j < NJ; ++j) {
-      const int64_t nb = n0 + CW * wn + 32 * j;
-      const bool whole = nb + 32 <= a.N;
-      if (a.out_elem == kElemF32 || !whole) {
+      for (int j = 0; j < NJ; ++j) {
+        const int nb = n0 + CW * wn + 32 * j;
+        if (nb + 32 > N) {
 #pragma unroll
-        for (int v4 = 0; v4 < 4; ++v4) {
-          const int64_t n = nb + 8 * v4 + 4 * half;
-          const float v[4] = {acc[i][j][4 * v4], acc[i][j][4 * v4 + 1], acc[i][j][4 * v4 + 2], acc[i][j][4 * v4 + 3]};
-          if (m < a.M) {
-            if (whole)
-              __builtin_memcpy(static_cast<float*>(p.out) + m * a.ldo + n, v, 16);
-            else
-              store_each(p.out, m * a.ldo + n, a.N - n, v, 4, a.out_elem);
+          for (int v = 0; v < 16; ++v) {
+            const int n = nb + 8 * (v >> 2) + 4 * half + (v & 3);
+            if (in && n < N) row[n] = narrow<E>(acc[i][j][v]);
           }
-        }
-      } else {
+        } else if constexpr (E == kElemF32) {
 #pragma unroll
-        for (int v8 = 0; v8 < 2; ++v8) {
-          uint32_t w[4];  // two dwords of run 2 v8, two of run 2 v8 + 1
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float lo = acc[i][j][8 * v8 + 2 * e], hi = acc[i][j][8 * v8 + 2 * e + 1];
-            if (a.out_elem == kElemBf16)
-              w[e] = __builtin_bit_cast(uint32_t, bf16x2{narrow<kElemBf16>(lo), narrow<kElemBf16>(hi)});
-            else
-              w[e] = __builtin_bit_cast(uint32_t, f16x2{narrow<kElemF16>(lo), narrow<kElemF16>(hi)});
+          for (int v4 = 0; v4 < 4; ++v4) {
+            const f32x4 o{acc[i][j][4 * v4], acc[i][j][4 * v4 + 1], acc[i][j][4 * v4 + 2], acc[i][j][4 * v4 + 3]};
+            if (in) __builtin_memcpy(row + nb + 8 * v4 + 4 * half, &o, 16);
           }
-          const auto s0 = __builtin_amdgcn_permlane32_swap(w[0], w[2], false, false);
-          const auto s1 = __builtin_amdgcn_permlane32_swap(w[1], w[3], false, false);
-          const uint32_t o[4] = {s0[0], s1[0], s0[1], s1[1]};
-          if (m < a.M)
-            __builtin_memcpy(static_cast<uint16_t*>(p.out) + m * a.ldo + nb + 16 * v8 + 8 * half, o, 16);
+        } else {
+#pragma unroll
+          for (int v8 = 0; v8 < 2; ++v8) {
+            typedef typename ElemOf<E>::T T2 __attribute__((ext_vector_type(2)));
+            uint32_t w[4];  // two dwords of run 2 v8, two of run 2 v8 + 1
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              w[e] = __builtin_bit_cast(
+                  uint32_t, T2{narrow<E>(acc[i][j][8 * v8 + 2 * e]), narrow<E>(acc[i][j][8 * v8 + 2 * e + 1])});
+            const auto s0 = __builtin_amdgcn_permlane32_swap(w[0], w[2], false, false);
+            const auto s1 = __builtin_amdgcn_permlane32_swap(w[1], w[3], false, false);
+            const uint32_t o[4] = {s0[0], s1[0], s0[1], s1[1]};
+            if (in) __builtin_memcpy(row + nb + 16 * v8 + 8 * half, o, 16);
+          }
         }
       }
     }
+  };
+  if constexpr (MODE == kWide) {
+    store(std::integral_constant<int, kElemF32>{});
+  } else {
+    if (a.out_elem == kElemBf16) store(std::integral_constant<int, kElemBf16>{});
+    else store(std::integral_constant<int, kElemF16>{});
   }
 }
 
