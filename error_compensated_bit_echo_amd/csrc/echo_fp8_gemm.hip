@@ -29,18 +29,19 @@ typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 
-// 8 codes (two dwords) as bfloat16, exactly.
+// 8 codes (two dwords), times a power of two, as bfloat16: exact where the product is
+// a normal bfloat16.
 template <bool E5>
-__device__ __forceinline__ bf16x8 widen8(int lo, int hi) {
+__device__ __forceinline__ bf16x8 widen8(int lo, int hi, float scale = 1.0f) {
   bf16x8 x{};
 #if defined(__HIP_DEVICE_COMPILE__)
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     const uint32_t w = static_cast<uint32_t>(i ? hi : lo);
-    const bf16x2 p = E5 ? __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(w, 1.0f, false)
-                        : __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, 1.0f, false);
-    const bf16x2 q = E5 ? __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(w, 1.0f, true)
-                        : __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, 1.0f, true);
+    const bf16x2 p = E5 ? __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(w, scale, false)
+                        : __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, scale, false);
+    const bf16x2 q = E5 ? __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(w, scale, true)
+                        : __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, scale, true);
     x[4 * i] = p[0];
     x[4 * i + 1] = p[1];
     x[4 * i + 2] = q[0];
@@ -217,7 +218,8 @@ __global__ __launch_bounds__(64 * kThinWaves) void echo_gemm_fp8_thin_k(const Ge
 enum TileMode {
   kScaled8 = 0,  // the 8-bit instruction applies exponent-byte scales
   kPlain8 = 1,   // the 8-bit instruction, a block's sum scaled in fp32
-  kWide = 2      // bfloat16, a block's sum scaled in fp32
+  kWide = 2,     // bfloat16, a block's sum scaled in fp32
+  kWideScaled = 3  // bfloat16, exponent-byte scales applied as the codes are widened
 };
 
 // An offset past the end of every buffer resource here (they stay below 2^31 bytes).
@@ -225,7 +227,9 @@ constexpr uint32_t kPastEnd = 0x80000000u;
 
 template <int BM, int BN, int WM, int WN, int S, int MODE, bool A5, bool W5, bool E8>
 __global__ __launch_bounds__(64 * WM * WN) void echo_gemm_fp8_tile_k(const GemmFp8Args a, uint32_t gm, uint32_t gn) {
-  static_assert(MODE != kScaled8 || E8, "the instruction takes exponent bytes");
+  constexpr bool kBf16 = MODE == kWide || MODE == kWideScaled;  // else the 8-bit instruction
+  constexpr bool kFolded = MODE == kScaled8 || MODE == kWideScaled;  // scales applied with the products
+  static_assert(!kFolded || E8, "only exponent bytes fold into the products");
   constexpr int NW = WM * WN, kThreads = 64 * NW;
   constexpr int RW = BM / WM, CW = BN / WN, MI = RW / 32, NJ = CW / 32;
   constexpr int JA = BM / (8 * NW), JW = BN / (8 * NW), kLoads = JA + JW;  // 1 KiB slab blocks per wavefront
@@ -343,7 +347,7 @@ __global__ __launch_bounds__(64 * WM * WN) void echo_gemm_fp8_tile_k(const GemmF
   // chunks.  They roll: as soon as the instructions that use a fragment are issued,
   // the next half step's is read in its place (A's, used until the end, alternate
   // between two sets with the 8-bit instruction).
-  constexpr int kSetsA = MODE == kWide ? 1 : 2;
+  constexpr int kSetsA = kBf16 ? 1 : 2;
   i32x4 fa[kSetsA][MI][2], fw[NJ][2];
   int at[2][2];  // byte offset of this lane's chunk c of half step hs in a 32-row sub-tile
 #pragma unroll
@@ -359,7 +363,7 @@ __global__ __launch_bounds__(64 * WM * WN) void echo_gemm_fp8_tile_k(const GemmF
     const uint8_t* b = lds + slab * kSlab + kSlabA + CW * wn * 128 + at[hs][c];
     fw[j][c] = *reinterpret_cast<const i32x4*>(b + 4096 * j);
   };
-  // kScaled8: the scale bytes of the rows this lane supplies, this step's and the next's
+  // kFolded: the scales of the rows this lane supplies, this step's and the next's
   uint32_t ea[MI], ew[NJ], ea1[MI], ew1[NJ];
   auto read_scales = [&](int ring, uint32_t* sa, uint32_t* sw) {
 #pragma unroll
@@ -374,7 +378,7 @@ __global__ __launch_bounds__(64 * WM * WN) void echo_gemm_fp8_tile_k(const GemmF
     constexpr bool READ = decltype(read)::value;
     [[maybe_unused]] const f32x16 zero{};
 #if defined(__HIP_DEVICE_COMPILE__)
-    if constexpr (MODE != kWide) {
+    if constexpr (!kBf16) {
       if constexpr (READ) {
         read_a(HS ^ 1, slab, HS ^ 1, 0);
         read_a(HS ^ 1, slab, HS ^ 1, 1);
@@ -402,16 +406,21 @@ __global__ __launch_bounds__(64 * WM * WN) void echo_gemm_fp8_tile_k(const GemmF
 #pragma unroll
       for (int s = 0; s < 4; ++s) {  // 16 k each
         const int c = s >> 1, d = 2 * (s & 1);
+        const auto scale = [](uint32_t e) { return MODE == kWideScaled ? __uint_as_float(e) : 1.0f; };
         bf16x8 wb[NJ];
 #pragma unroll
-        for (int j = 0; j < NJ; ++j) wb[j] = widen8<W5>(fw[j][c][d], fw[j][c][d + 1]);
+        for (int j = 0; j < NJ; ++j) wb[j] = widen8<W5>(fw[j][c][d], fw[j][c][d + 1], scale(ew[j]));
 #pragma unroll
         for (int i = 0; i < MI; ++i) {
-          const bf16x8 ab = widen8<A5>(fa[0][i][c][d], fa[0][i][c][d + 1]);
+          const bf16x8 ab = widen8<A5>(fa[0][i][c][d], fa[0][i][c][d + 1], scale(ea[i]));
 #pragma unroll
-          for (int j = 0; j < NJ; ++j)
-            blk[i][j] =
-                __builtin_amdgcn_mfma_f32_32x32x16_bf16(wb[j], ab, HS == 0 && s == 0 ? zero : blk[i][j], 0, 0, 0);
+          for (int j = 0; j < NJ; ++j) {
+            if constexpr (MODE == kWideScaled)
+              acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(wb[j], ab, acc[i][j], 0, 0, 0);
+            else
+              blk[i][j] =
+                  __builtin_amdgcn_mfma_f32_32x32x16_bf16(wb[j], ab, HS == 0 && s == 0 ? zero : blk[i][j], 0, 0, 0);
+          }
         }
         if constexpr (READ) {
           if (s & 1) {
@@ -441,7 +450,7 @@ __global__ __launch_bounds__(64 * WM * WN) void echo_gemm_fp8_tile_k(const GemmF
     __builtin_amdgcn_s_waitcnt(vmcnt_at_most_lds_drained(0));
   slab_barrier();
   if (steps == 1 && K % 16 != 0) clear_tail(lds);
-  if constexpr (MODE == kScaled8) read_scales(0, ea, ew);
+  if constexpr (kFolded) read_scales(0, ea, ew);
 #pragma unroll
   for (int c = 0; c < 2; ++c) {
     read_a(0, 0, 0, c);
@@ -472,24 +481,38 @@ __global__ __launch_bounds__(64 * WM * WN) void echo_gemm_fp8_tile_k(const GemmF
       slab_barrier();
       if constexpr (ISSUE != 1)
         if (it + 2 == steps && K % 16 != 0) clear_tail(lds + next * kSlab);
-      if constexpr (MODE == kScaled8) read_scales(ring1, ea1, ew1);
+      if constexpr (kFolded) read_scales(ring1, ea1, ew1);
       half_step(H1, kYes, next);
     } else {
       half_step(H1, kNo, 0);
     }
-    if constexpr (MODE != kScaled8) {
+    if constexpr (!kFolded) {
+      float ca[MI];
 #pragma unroll
-      for (int j = 0; j < NJ; ++j) {
-        f32x4 cw[4];
+      for (int i = 0; i < MI; ++i) ca[i] = __uint_as_float(sc[ring][RW * wm + 32 * i + (lane & 31)]);
+      if (a.sw_shift != 0) {  // one scale for a sub-tile's 32 columns
 #pragma unroll
-        for (int v4 = 0; v4 < 4; ++v4)
-          cw[v4] = *reinterpret_cast<const f32x4*>(&sc[ring][BM + CW * wn + 32 * j + 8 * v4 + 4 * half]);
+        for (int j = 0; j < NJ; ++j) {
+          const float cw = __uint_as_float(sc[ring][BM + CW * wn + 32 * j]);
 #pragma unroll
-        for (int i = 0; i < MI; ++i) {
-          const float ca = __uint_as_float(sc[ring][RW * wm + 32 * i + (lane & 31)]);
+          for (int i = 0; i < MI; ++i) {
+            const float c = ca[i] * cw;
 #pragma unroll
-          for (int v = 0; v < 16; ++v)
-            acc[i][j][v] = __builtin_fmaf(blk[i][j][v], ca * cw[v >> 2][v & 3], acc[i][j][v]);
+            for (int v = 0; v < 16; ++v) acc[i][j][v] = __builtin_fmaf(blk[i][j][v], c, acc[i][j][v]);
+          }
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) {
+          f32x4 cw[4];
+#pragma unroll
+          for (int v4 = 0; v4 < 4; ++v4)
+            cw[v4] = *reinterpret_cast<const f32x4*>(&sc[ring][BM + CW * wn + 32 * j + 8 * v4 + 4 * half]);
+#pragma unroll
+          for (int i = 0; i < MI; ++i)
+#pragma unroll
+            for (int v = 0; v < 16; ++v)
+              acc[i][j][v] = __builtin_fmaf(blk[i][j][v], ca[i] * cw[v >> 2][v & 3], acc[i][j][v]);
         }
       }
     } else if constexpr (!LAST) {
@@ -550,7 +573,7 @@ __global__ __launch_bounds__(64 * WM * WN) void echo_gemm_fp8_tile_k(const GemmF
       }
     }
   };
-  if constexpr (MODE == kWide) {
+  if constexpr (kBf16) {
     store(std::integral_constant<int, kElemF32>{});
   } else {
     if (a.out_elem == kElemBf16) store(std::integral_constant<int, kElemBf16>{});
@@ -580,8 +603,13 @@ hipError_t launch(const GemmFp8Args& a, int P, hipStream_t s) {
   if (a.M <= 32) return thin<2, 1, A5, W5, E8>(a, P, s);
   const int64_t big = (a.M + 255) / 256 * ((a.N + 255) / 256) * P;
   if (a.out_elem == kElemF32) {
-    if ((a.M + 255) / 256 * ((a.N + 127) / 128) * P >= 256) return tile<256, 128, 4, 2, 3, kWide, A5, W5, E8>(a, P, s);
-    return tile<64, 64, 2, 2, 4, kWide, A5, W5, E8>(a, P, s);
+    if constexpr (E8) {
+      if (big >= 256) return tile<256, 256, 4, 2, 2, kWideScaled, A5, W5, E8>(a, P, s);
+      return tile<64, 64, 2, 2, 4, kWideScaled, A5, W5, E8>(a, P, s);
+    } else {
+      if (2 * big >= 256) return tile<256, 128, 4, 2, 3, kWide, A5, W5, E8>(a, P, s);
+      return tile<64, 64, 2, 2, 4, kWide, A5, W5, E8>(a, P, s);
+    }
   }
   if constexpr (E8) {
     if (big >= 256) return tile<256, 256, 4, 2, 2, kScaled8, A5, W5, E8>(a, P, s);
