@@ -439,13 +439,14 @@ __global__ __launch_bounds__(64 * WM * WN) void echo_gemm_fp8_tile_k(const GemmF
   constexpr std::false_type kNo{};
 
   load_scales();
-  for (int s = 0; s < S - 1 && s < steps; ++s) {
+  stage_scales(0);
+  if (steps > 1) load_scales();
+  for (int s = 0; s < S && s < steps; ++s) {
     if (s + 1 < steps) issue(s, s, kNo);
     else issue(s, s, kYes);
   }
-  stage_scales(0);
-  if (steps >= S - 1)
-    __builtin_amdgcn_s_waitcnt(vmcnt_at_most_lds_drained((S - 2) * kLoads));
+  if (steps >= S)
+    __builtin_amdgcn_s_waitcnt(vmcnt_at_most_lds_drained((S - 1) * kLoads));
   else
     __builtin_amdgcn_s_waitcnt(vmcnt_at_most_lds_drained(0));
   slab_barrier();
@@ -458,30 +459,33 @@ __global__ __launch_bounds__(64 * WM * WN) void echo_gemm_fp8_tile_k(const GemmF
     for (int j = 0; j < NJ; ++j) read_w(j, 0, 0, c);
   }
   int cur = 0, ring = 0;  // slab and scales of the step
-  // One K step.  ISSUE: the loads of step it + S - 1 go out at its start, into the slab
-  // step it - 1 used (2: they are the last step's).  Between its halves: the scales of
-  // the next step are staged, this wavefront's reads of the slab are done, the next
-  // slab has landed, and the barrier; LAST: none of that.  The steps of the main loop
-  // have no branch between the halves: the compiler would move the first half's
-  // instructions past it, behind the barrier.
+  // One K step.  Between its halves, unless it is the last: the scales of the next step
+  // are staged, this wavefront's reads of the slab are done, the next slab has landed,
+  // and the barrier; then the slab is free, and the loads of step it + S go out into it
+  // (ISSUE 1; 2: they are the last step's), so a slab has S - 1 whole steps to arrive.
+  // The scales of step it + 2 are loaded before them: waiting for those waits for
+  // everything issued earlier.  The steps of the main loop have no branch between
+  // the halves: the compiler would move the first half's instructions past it,
+  // behind the barrier.
   auto step = [&](int it, auto issues, auto last) {
     constexpr int ISSUE = decltype(issues)::value;
     constexpr bool LAST = decltype(last)::value;
     const int next = cur + 1 == S ? 0 : cur + 1, ring1 = ring == 2 ? 0 : ring + 1;
-    if constexpr (!LAST) {
-      load_scales();
-      if constexpr (ISSUE == 1) issue(cur == 0 ? S - 1 : cur - 1, it + S - 1, kNo);
-      if constexpr (ISSUE == 2) issue(cur == 0 ? S - 1 : cur - 1, it + S - 1, kYes);
-    }
     half_step(H0, kYes, cur);
     if constexpr (!LAST) {
       stage_scales(ring1);
       __builtin_amdgcn_s_waitcnt(vmcnt_at_most_lds_drained(ISSUE != 0 ? (S - 2) * kLoads : 0));
       __builtin_amdgcn_sched_barrier(0);
       slab_barrier();
-      if constexpr (ISSUE != 1)
+      if constexpr (ISSUE == 0) {
         if (it + 2 == steps && K % 16 != 0) clear_tail(lds + next * kSlab);
+        if (it + 2 < steps) load_scales();
+      } else {
+        load_scales();
+      }
       if constexpr (kFolded) read_scales(ring1, ea1, ew1);
+      if constexpr (ISSUE == 1) issue(cur, it + S, kNo);
+      if constexpr (ISSUE == 2) issue(cur, it + S, kYes);
       half_step(H1, kYes, next);
     } else {
       half_step(H1, kNo, 0);
@@ -525,8 +529,8 @@ __global__ __launch_bounds__(64 * WM * WN) void echo_gemm_fp8_tile_k(const GemmF
     ring = ring1;
   };
   int it = 0;
-  for (; it < steps - S; ++it) step(it, std::integral_constant<int, 1>{}, kNo);
-  if (it == steps - S) step(it++, std::integral_constant<int, 2>{}, kNo);
+  for (; it < steps - S - 1; ++it) step(it, std::integral_constant<int, 1>{}, kNo);
+  if (it == steps - S - 1) step(it++, std::integral_constant<int, 2>{}, kNo);
   for (; it < steps - 1; ++it) step(it, std::integral_constant<int, 0>{}, kNo);
   step(it, std::integral_constant<int, 0>{}, kYes);
 
