@@ -23,6 +23,7 @@ namespace echo {
 namespace {
 
 typedef int i32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef int i32x8 __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
@@ -534,46 +535,48 @@ __global__ __launch_bounds__(64 * WM * WN) void echo_gemm_fp8_tile_k(const GemmF
   for (; it < steps - 1; ++it) step(it, std::integral_constant<int, 0>{}, kNo);
   step(it, std::integral_constant<int, 0>{}, kYes);
 
-  // Out from the accumulators.  fp32: runs of 4 columns, 16 bytes.  16 bits: the two
-  // halves of the wavefront exchange runs (v_permlane32_swap), so a lane holds 8
-  // consecutive columns, 16 bytes.  Sub-tiles over the right edge go one by one.
+  // Out through LDS, each wavefront on its own in 32 rows at a time (the slabs are
+  // free once every wavefront is here): a lane's runs of 4 columns go in row-major and
+  // come back as 16 bytes of a row, so the stores cover whole lines.  (Straight from
+  // the accumulators, in 32-byte pieces, the stores of a 256 x 256 tile on every CU
+  // took 10 us.)
+  __syncthreads();
   const auto store = [&](auto elem) {
     constexpr int E = decltype(elem)::value;
+    typedef typename ElemOf<E>::T T;
+    typedef T T4 __attribute__((ext_vector_type(4)));
+    constexpr int kPitch = CW * sizeof(T) + 16, kRegion = 32 * kPitch, kPerLane = 16 / sizeof(T);
+    static_assert(NW * kRegion <= S * kSlab + 12 * kRows, "a region of LDS per wavefront");
+    constexpr int kLanes = CW / kPerLane, kStep = 64 / kLanes;  // lanes per row, rows per instruction
+    uint8_t* region = lds + wave * kRegion;
+    const int sr = lane / kLanes, scol = lane % kLanes * kPerLane;
+    const int n = n0 + CW * wn + scol;
 #pragma unroll
     for (int i = 0; i < MI; ++i) {
-      const int m = m0 + RW * wm + 32 * i + (lane & 31);
-      const bool in = m < M;
-      typename ElemOf<E>::T* row = static_cast<typename ElemOf<E>::T*>(p.out) + m * a.ldo;
 #pragma unroll
-      for (int j = 0; j < NJ; ++j) {
-        const int nb = n0 + CW * wn + 32 * j;
-        if (nb + 32 > N) {
+      for (int j = 0; j < NJ; ++j)
 #pragma unroll
-          for (int v = 0; v < 16; ++v) {
-            const int n = nb + 8 * (v >> 2) + 4 * half + (v & 3);
-            if (in && n < N) row[n] = narrow<E>(acc[i][j][v]);
-          }
-        } else if constexpr (E == kElemF32) {
+        for (int v4 = 0; v4 < 4; ++v4) {
+          const T4 o{narrow<E>(acc[i][j][4 * v4]), narrow<E>(acc[i][j][4 * v4 + 1]), narrow<E>(acc[i][j][4 * v4 + 2]),
+                     narrow<E>(acc[i][j][4 * v4 + 3])};
+          *reinterpret_cast<T4*>(region + (lane & 31) * kPitch + (32 * j + 8 * v4 + 4 * half) * sizeof(T)) = o;
+        }
+      T* row = static_cast<T*>(p.out) + (m0 + RW * wm + 32 * i + sr) * a.ldo + n;
 #pragma unroll
-          for (int v4 = 0; v4 < 4; ++v4) {
-            const f32x4 o{acc[i][j][4 * v4], acc[i][j][4 * v4 + 1], acc[i][j][4 * v4 + 2], acc[i][j][4 * v4 + 3]};
-            if (in) __builtin_memcpy(row + nb + 8 * v4 + 4 * half, &o, 16);
-          }
-        } else {
+      for (int u = 0; u < 32 / kStep; ++u) {
+        const u32x4 o = *reinterpret_cast<const u32x4*>(region + (sr + u * kStep) * kPitch + scol * sizeof(T));
+        if (m0 + RW * wm + 32 * i + sr + u * kStep < M) {
+          if (n + kPerLane <= N) {
+            __builtin_memcpy(row, &o, 16);
+          } else {
+            T each[kPerLane];
+            __builtin_memcpy(each, &o, 16);
 #pragma unroll
-          for (int v8 = 0; v8 < 2; ++v8) {
-            typedef typename ElemOf<E>::T T2 __attribute__((ext_vector_type(2)));
-            uint32_t w[4];  // two dwords of run 2 v8, two of run 2 v8 + 1
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              w[e] = __builtin_bit_cast(
-                  uint32_t, T2{narrow<E>(acc[i][j][8 * v8 + 2 * e]), narrow<E>(acc[i][j][8 * v8 + 2 * e + 1])});
-            const auto s0 = __builtin_amdgcn_permlane32_swap(w[0], w[2], false, false);
-            const auto s1 = __builtin_amdgcn_permlane32_swap(w[1], w[3], false, false);
-            const uint32_t o[4] = {s0[0], s1[0], s0[1], s1[1]};
-            if (in) __builtin_memcpy(row + nb + 16 * v8 + 8 * half, o, 16);
+            for (int e = 0; e < kPerLane; ++e)
+              if (n + e < N) row[e] = each[e];
           }
         }
+        row += kStep * a.ldo;
       }
     }
   };
