@@ -216,124 +216,263 @@ __global__ __launch_bounds__(64 * kThinWaves) void echo_gemm_fp8_thin_k(const Ge
 // so does what lies past K in the last step: 16-byte chunks by an offset out of
 // range, the bytes behind K in the last chunk by one pass over the slab.
 
-enum TileMode {
-  kScaled8 = 0,  // the 8-bit instruction applies exponent-byte scales
-  kPlain8 = 1,   // the 8-bit instruction, a block's sum scaled in fp32
-  kWide = 2,     // bfloat16, a block's sum scaled in fp32
-  kWideScaled = 3  // bfloat16, exponent-byte scales applied as the codes are widened
-};
-
 // An offset past the end of every buffer resource here (they stay below 2^31 bytes).
 constexpr uint32_t kPastEnd = 0x80000000u;
 
-template <int BM, int BN, int WM, int WN, int S, int MODE, bool A5, bool W5, bool E8>
-__global__ __launch_bounds__(64 * WM * WN) void echo_gemm_fp8_tile_k(const GemmFp8Args a, uint32_t gm, uint32_t gn) {
-  constexpr bool kBf16 = MODE == kWide || MODE == kWideScaled;  // else the 8-bit instruction
-  constexpr bool kFolded = MODE == kScaled8 || MODE == kWideScaled;  // scales applied with the products
-  static_assert(!kFolded || E8, "only exponent bytes fold into the products");
-  constexpr int NW = WM * WN, kThreads = 64 * NW;
-  constexpr int RW = BM / WM, CW = BN / WN, MI = RW / 32, NJ = CW / 32;
-  constexpr int JA = BM / (8 * NW), JW = BN / (8 * NW), kLoads = JA + JW;  // 1 KiB slab blocks per wavefront
-  static_assert(MI * 32 * WM == BM && NJ * 32 * WN == BN && JA * 8 * NW == BM && JW * 8 * NW == BN, "even splits");
-  static_assert(BM % 64 == 0 && BN % 64 == 0, "a wavefront stages scales of one operand");
-  constexpr int kSlabA = BM * 128, kSlab = (BM + BN) * 128;
-  constexpr int kPer = (BM + BN + kThreads - 1) / kThreads;  // scales per thread
-  constexpr int kRows = kPer * kThreads;                     // rows with a scale, rounded up to whole threads
-  // one array for slabs and scales: with two, the compiler tells the accesses of each
-  // apart and then waits for every load into LDS before the next fragment read
-  __shared__ __attribute__((aligned(1024))) uint8_t lds[S * kSlab + 3 * 4 * kRows];
-  const auto sc = reinterpret_cast<uint32_t(*)[kRows]>(lds + S * kSlab);
-
-  // The hardware hands the workgroups of a launch to the eight XCDs in turn, and each
-  // XCD has its own L2: workgroup i takes a tile of the (i % 8)-th contiguous run, and
-  // tiles are ordered in bands of 8 row tiles, so the tiles an XCD works on at a time
-  // share their panels of A and of W.
+// Which tile a workgroup takes.  The hardware hands the workgroups of a launch to the
+// eight XCDs in turn, and each XCD has its own L2: workgroup i takes a tile of the
+// (i % 8)-th contiguous run, and tiles are ordered in bands of 8 row tiles, so the
+// tiles an XCD works on at a time share their panels of A and of W.
+struct TileAt {
+  int rank, m0, n0;
+};
+template <int BM, int BN>
+__device__ __forceinline__ TileAt tile_at(uint32_t gm, uint32_t gn) {
   const uint32_t T = gridDim.x, x = blockIdx.x % 8, q = T / 8, rem = T % 8;
   uint32_t id = x * q + (x < rem ? x : rem) + blockIdx.x / 8;
-  const int r = static_cast<int>(id / (gm * gn));
-  id -= r * gm * gn;
+  const uint32_t rank = id / (gm * gn);
+  id -= rank * gm * gn;
   const uint32_t band = id / (8 * gn), in_band = id - band * 8 * gn;
   const uint32_t high = gm - 8 * band < 8 ? gm - 8 * band : 8;  // row tiles of this band
-  const int m0 = static_cast<int>(8 * band + in_band % high) * BM, n0 = static_cast<int>(in_band / high) * BN;
-  const RankPtrs p = rank_ptrs(r);
-  const int M = static_cast<int>(a.M), N = static_cast<int>(a.N), K = static_cast<int>(a.K);
+  return TileAt{static_cast<int>(rank), static_cast<int>(8 * band + in_band % high) * BM,
+                static_cast<int>(in_band / high) * BN};
+}
 
-  const int t = threadIdx.x, lane = t & 63, half = lane >> 5;
-  const int wave = __builtin_amdgcn_readfirstlane(t >> 6), wm = wave / WN, wn = wave % WN;
-  const int steps = (K + 127) / 128, K16 = (K + 15) / 16 * 16;
-  const int rows_a = M - m0 < BM ? M - m0 : BM, rows_w = N - n0 < BN ? N - n0 : BN;
-  const BufRsrc rA = buffer_rsrc(p.A + m0 * a.lda, static_cast<int32_t>((rows_a - 1) * a.lda + K16));
-  const BufRsrc rW = buffer_rsrc(p.W + n0 * a.ldw, static_cast<int32_t>((rows_w - 1) * a.ldw + K16));
-  // Lane l fills slot l of each 1 KiB block: row 8 i + l / 8, slot l % 8.
+// The slabs and scales of a tile's K steps.  BYTES: scales are staged as exponent
+// bytes, else as fp32.
+template <int BM, int BN, int NW, int S, bool BYTES, bool E8>
+struct Slabs {
+  static constexpr int kThreads = 64 * NW;
+  static constexpr int JA = BM / (8 * NW), JW = BN / (8 * NW), kLoads = JA + JW;  // 1 KiB slab blocks per wavefront
+  static constexpr int kSlabA = BM * 128, kSlab = (BM + BN) * 128;
+  static constexpr int kPer = (BM + BN + kThreads - 1) / kThreads;  // scales per thread
+  static constexpr int kRows = kPer * kThreads;                     // rows with a scale, rounded up to whole threads
+  static constexpr int kBytes = S * kSlab + 3 * 4 * kRows;
+  static_assert(JA * 8 * NW == BM && JW * 8 * NW == BN, "slab blocks split evenly");
+  static_assert(BM % 64 == 0 && BN % 64 == 0, "a wavefront stages scales of one operand");
+
+  // One array for slabs and scales: with two, the compiler tells the accesses of each
+  // apart and then waits for every load into LDS before the next fragment read.
+  uint8_t* lds;
+  BufRsrc rA, rW;
   uint32_t offA[JA], offW[JW];
-  const auto chunk_of = [&](int row) { return (lane & 7) ^ ((row >> 1) & 7); };
-#pragma unroll
-  for (int j = 0; j < JA; ++j) {
-    const int row = 8 * (JA * wave + j) + (lane >> 3);
-    offA[j] = static_cast<uint32_t>(row * static_cast<int>(a.lda) + 16 * chunk_of(row));
+  const uint8_t* sp[kPer];
+  int64_t sk[kPer];
+  uint32_t sreg[kPer];
+  int K, K16, steps, t, lane, wave;
+
+  __device__ __forceinline__ int chunk_of(int row) const { return (lane & 7) ^ ((row >> 1) & 7); }
+  __device__ __forceinline__ uint32_t* scales(int ring) const {
+    return reinterpret_cast<uint32_t*>(lds + S * kSlab) + ring * kRows;
   }
+
+  __device__ __forceinline__ void init(uint8_t* l, const GemmFp8Args& a, const RankPtrs& p, const TileAt& at) {
+    lds = l;
+    t = threadIdx.x;
+    lane = t & 63;
+    wave = __builtin_amdgcn_readfirstlane(t >> 6);
+    K = static_cast<int>(a.K);
+    K16 = (K + 15) / 16 * 16;
+    steps = (K + 127) / 128;
+    const int M = static_cast<int>(a.M), N = static_cast<int>(a.N);
+    const int rows_a = M - at.m0 < BM ? M - at.m0 : BM, rows_w = N - at.n0 < BN ? N - at.n0 : BN;
+    rA = buffer_rsrc(p.A + at.m0 * a.lda, static_cast<int32_t>((rows_a - 1) * a.lda + K16));
+    rW = buffer_rsrc(p.W + at.n0 * a.ldw, static_cast<int32_t>((rows_w - 1) * a.ldw + K16));
+    // Lane l fills slot l of each 1 KiB block: row 8 i + l / 8, slot l % 8.
 #pragma unroll
-  for (int j = 0; j < JW; ++j) {
-    const int row = 8 * (JW * wave + j) + (lane >> 3);
-    offW[j] = static_cast<uint32_t>(row * static_cast<int>(a.ldw) + 16 * chunk_of(row));
+    for (int j = 0; j < JA; ++j) {
+      const int row = 8 * (JA * wave + j) + (lane >> 3);
+      offA[j] = static_cast<uint32_t>(row * static_cast<int>(a.lda) + 16 * chunk_of(row));
+    }
+#pragma unroll
+    for (int j = 0; j < JW; ++j) {
+      const int row = 8 * (JW * wave + j) + (lane >> 3);
+      offW[j] = static_cast<uint32_t>(row * static_cast<int>(a.ldw) + 16 * chunk_of(row));
+    }
+    // Thread t stages the scales of rows t, t + kThreads, ... of A's then W's.
+    constexpr int kScaleBytes = E8 ? 1 : 4;
+#pragma unroll
+    for (int u = 0; u < kPer; ++u) {
+      const bool of_a = 64 * (wave + u * NW) < BM;
+      int i = t + u * kThreads + (of_a ? at.m0 : at.n0 - BM);
+      const int end = of_a ? M : N;
+      i = i < end ? i : end - 1;  // past the edge: any scale does
+      sp[u] = static_cast<const uint8_t*>(of_a ? p.sA : p.sW) +
+              (of_a ? (i >> a.sa_shift) * a.sa_row : (i >> a.sw_shift) * a.sw_row) * kScaleBytes;
+      sk[u] = (of_a ? a.sa_k : a.sw_k) * kScaleBytes;
+    }
   }
-  // The loads of K step `it` into slab `buf`; `last`: of the last step, whose chunks
+
+  // The loads of K step `it` into slab `buf`.  LAST: of the last step, whose chunks
   // past K16 read as zeros.
-  auto issue = [&](int buf, int it, auto last) {
+  template <bool LAST>
+  __device__ __forceinline__ void issue(int buf, int it) {
     uint8_t* As = lds + buf * kSlab + 1024 * JA * wave;
     uint8_t* Ws = lds + buf * kSlab + kSlabA + 1024 * JW * wave;
     const int chunks = (K16 - it * 128) / 16;
 #pragma unroll
     for (int j = 0; j < JA; ++j) {
       uint32_t off = offA[j];
-      if constexpr (decltype(last)::value) off = chunk_of(8 * (JA * wave + j) + (lane >> 3)) < chunks ? off : kPastEnd;
+      if constexpr (LAST) off = chunk_of(8 * (JA * wave + j) + (lane >> 3)) < chunks ? off : kPastEnd;
       buffer_load_lds16<0>(rA, As + 1024 * j, off, static_cast<uint32_t>(it * 128));
     }
 #pragma unroll
     for (int j = 0; j < JW; ++j) {
       uint32_t off = offW[j];
-      if constexpr (decltype(last)::value) off = chunk_of(8 * (JW * wave + j) + (lane >> 3)) < chunks ? off : kPastEnd;
+      if constexpr (LAST) off = chunk_of(8 * (JW * wave + j) + (lane >> 3)) < chunks ? off : kPastEnd;
       buffer_load_lds16<0>(rW, Ws + 1024 * j, off, static_cast<uint32_t>(it * 128));
     }
-  };
-  // The scales: thread t stages rows t, t + kThreads, ... of A's then W's.
-  constexpr int kScaleBytes = E8 ? 1 : 4;
-  const uint8_t* sp[kPer];
-  int64_t sk[kPer];
-#pragma unroll
-  for (int u = 0; u < kPer; ++u) {
-    const bool of_a = 64 * (wave + u * NW) < BM;
-    int i = t + u * kThreads + (of_a ? m0 : n0 - BM);
-    const int end = of_a ? M : N;
-    i = i < end ? i : end - 1;  // past the edge: any scale does
-    sp[u] = static_cast<const uint8_t*>(of_a ? p.sA : p.sW) +
-            (of_a ? (i >> a.sa_shift) * a.sa_row : (i >> a.sw_shift) * a.sw_row) * kScaleBytes;
-    sk[u] = (of_a ? a.sa_k : a.sw_k) * kScaleBytes;
   }
-  uint32_t sreg[kPer];
-  auto load_scales = [&]() {  // the next K step's
+
+  __device__ __forceinline__ void load_scales() {  // the next K step's
 #pragma unroll
     for (int u = 0; u < kPer; ++u) {
       sreg[u] = scale_bits<E8>(sp[u], 0);
       sp[u] += sk[u];
     }
-  };
-  auto stage_scales = [&](int ring) {
+  }
+  __device__ __forceinline__ void stage_scales(int ring) {
 #pragma unroll
     for (int u = 0; u < kPer; ++u)
-      sc[ring][t + u * kThreads] = MODE == kScaled8 ? sreg[u] : __float_as_uint(scale_value<E8>(sreg[u]));
-  };
-  // Bytes behind K in the last chunk of the last slab, on both sides (a NaN there
+      scales(ring)[t + u * kThreads] = BYTES ? sreg[u] : __float_as_uint(scale_value<E8>(sreg[u]));
+  }
+
+  // Zeros behind K in the last chunk of the last slab, on both sides (a NaN there
   // would survive a product with zero).
-  auto clear_tail = [&](uint8_t* slab) {
+  __device__ __forceinline__ void clear_tail(int buf) {
     const int c = K % 128 / 16, n = K % 16;
     for (int row = t; row < BM + BN; row += kThreads) {
       const int in = row < BM ? row : row - BM;
-      uint8_t* b = slab + row * 128 + 16 * (c ^ ((in >> 1) & 7));
+      uint8_t* b = lds + buf * kSlab + row * 128 + 16 * (c ^ ((in >> 1) & 7));
       for (int i = n; i < 16; ++i) b[i] = 0;
     }
     __syncthreads();
-  };
+  }
+
+  // Step 0's scales staged, step 1's on their way, the loads of the first S steps out and
+  // the first slab landed.
+  __device__ __forceinline__ void start() {
+    load_scales();
+    stage_scales(0);
+    if (steps > 1) load_scales();
+    for (int s = 0; s < S && s < steps; ++s) {
+      if (s + 1 < steps) issue<false>(s, s);
+      else issue<true>(s, s);
+    }
+    if (steps >= S)
+      __builtin_amdgcn_s_waitcnt(vmcnt_at_most_lds_drained((S - 1) * kLoads));
+    else
+      __builtin_amdgcn_s_waitcnt(vmcnt_at_most_lds_drained(0));
+    slab_barrier();
+    if (steps == 1 && K % 16 != 0) clear_tail(0);
+  }
+
+  // Between the reads of step it's slab `cur` and those of the next one `next`: the next
+  // step's scales are staged, this wavefront's reads are done, the next slab has landed,
+  // and the barrier; then slab `cur` is free and the loads of step it + S go out into
+  // it (ISSUE 1; 2: they are the last step's; 0: none are left), so a slab has S - 1
+  // whole steps to arrive.  The scales of step it + 2 are loaded before them: waiting
+  // for those waits for everything issued earlier.
+  template <int ISSUE>
+  __device__ __forceinline__ void wait_next(int it, int next, int ring1) {
+    stage_scales(ring1);
+    __builtin_amdgcn_s_waitcnt(vmcnt_at_most_lds_drained(ISSUE != 0 ? (S - 2) * kLoads : 0));
+    __builtin_amdgcn_sched_barrier(0);
+    slab_barrier();
+    if constexpr (ISSUE == 0) {
+      if (it + 2 == steps && K % 16 != 0) clear_tail(next);
+      if (it + 2 < steps) load_scales();
+    } else {
+      load_scales();
+    }
+  }
+  template <int ISSUE>
+  __device__ __forceinline__ void refill(int it, int cur) {
+    if constexpr (ISSUE == 1) issue<false>(cur, it + S);
+    if constexpr (ISSUE == 2) issue<true>(cur, it + S);
+  }
+
+  // Runs step(it, ISSUE, LAST) for every K step.  The steps of the main loop contain no
+  // branch: the compiler would move a step's instructions past it, behind the barrier.
+  template <typename Step>
+  __device__ __forceinline__ void run(Step step) {
+    int it = 0;
+    for (; it < steps - S - 1; ++it) step(it, std::integral_constant<int, 1>{}, std::false_type{});
+    if (it == steps - S - 1) step(it++, std::integral_constant<int, 2>{}, std::false_type{});
+    for (; it < steps - 1; ++it) step(it, std::integral_constant<int, 0>{}, std::false_type{});
+    step(it, std::integral_constant<int, 0>{}, std::true_type{});
+  }
+};
+
+// Writes RW x CW of the tile out of a wavefront's registers, 32 rows at a time, through
+// its own region of LDS (the slabs are free once every wavefront is here): `put(region,
+// pitch, i)` lays rows 32 i .. 32 i + 31 out row-major, and they come back as 16 bytes
+// of a row per lane, so the stores cover whole lines.  (Straight from the
+// accumulators, in 32-byte pieces, the stores of a 256 x 256 tile on every CU took
+// 10 us.)
+template <int E, int RW, int CW, int REGION, typename Put>
+__device__ __forceinline__ void store_tile(uint8_t* region, const GemmFp8Args& a, void* out, int row0, int col0, Put put) {
+  typedef typename ElemOf<E>::T T;
+  constexpr int kPitch = CW * sizeof(T) + 16, kPerLane = 16 / sizeof(T);
+  static_assert(32 * kPitch <= REGION, "a region of LDS per wavefront");
+  constexpr int kLanes = CW / kPerLane, kStep = 64 / kLanes;  // lanes per row, rows per instruction
+  const int lane = threadIdx.x & 63, sr = lane / kLanes, scol = lane % kLanes * kPerLane;
+  const int n = col0 + scol, M = static_cast<int>(a.M), N = static_cast<int>(a.N);
+#pragma unroll
+  for (int i = 0; i < RW / 32; ++i) {
+    put(region, kPitch, i);
+    T* row = static_cast<T*>(out) + (row0 + 32 * i + sr) * a.ldo + n;
+#pragma unroll
+    for (int u = 0; u < 32 / kStep; ++u) {
+      const u32x4 o = *reinterpret_cast<const u32x4*>(region + (sr + u * kStep) * kPitch + scol * sizeof(T));
+      if (row0 + 32 * i + sr + u * kStep < M) {
+        if (n + kPerLane <= N) {
+          __builtin_memcpy(row, &o, 16);
+        } else {
+          T each[kPerLane];
+          __builtin_memcpy(each, &o, 16);
+#pragma unroll
+          for (int e = 0; e < kPerLane; ++e)
+            if (n + e < N) row[e] = each[e];
+        }
+      }
+      row += kStep * a.ldo;
+    }
+  }
+}
+
+// Four values to consecutive elements of a row in LDS.
+template <int E>
+__device__ __forceinline__ void put4(uint8_t* at, float a, float b, float c, float d) {
+  typedef typename ElemOf<E>::T T4 __attribute__((ext_vector_type(4)));
+  *reinterpret_cast<T4*>(at) = T4{narrow<E>(a), narrow<E>(b), narrow<E>(c), narrow<E>(d)};
+}
+
+enum TileMode {
+  kScaled8 = 0,     // the 8-bit instruction applies exponent-byte scales
+  kWide = 1,        // bfloat16, a block's sum scaled in fp32
+  kWideScaled = 2,  // bfloat16, exponent-byte scales applied as the codes are widened
+};
+
+// 32 x 32 sub-tiles.  Lane l supplies row l % 32 of a sub-tile and the bytes
+// 64 (l / 32) .. + 63 of the K step, in two half steps.  Accumulator v of lane l is
+// row l % 32 of the tile's A rows and column 8 (v / 4) + 4 (l / 32) + v % 4 of its W
+// rows.
+template <int BM, int BN, int WM, int WN, int S, int MODE, bool A5, bool W5, bool E8>
+__global__ __launch_bounds__(64 * WM * WN) void echo_gemm_fp8_tile_k(const GemmFp8Args a, uint32_t gm, uint32_t gn) {
+  constexpr bool kBf16 = MODE == kWide || MODE == kWideScaled;       // else the 8-bit instruction
+  constexpr bool kFolded = MODE == kScaled8 || MODE == kWideScaled;  // scales applied with the products
+  static_assert(!kFolded || E8, "only exponent bytes fold into the products");
+  constexpr int NW = WM * WN, RW = BM / WM, CW = BN / WN, MI = RW / 32, NJ = CW / 32;
+  static_assert(MI * 32 * WM == BM && NJ * 32 * WN == BN, "even splits");
+  typedef Slabs<BM, BN, NW, S, MODE == kScaled8, E8> SL;
+  constexpr int kSlab = SL::kSlab, kSlabA = SL::kSlabA;
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[SL::kBytes];
+  const TileAt tile = tile_at<BM, BN>(gm, gn);
+  const RankPtrs p = rank_ptrs(tile.rank);
+  SL sl;
+  sl.init(lds, a, p, tile);
+  const int lane = sl.lane, half = lane >> 5, wm = sl.wave / WN, wn = sl.wave % WN;
 
   f32x16 acc[MI][NJ];
 #pragma unroll
@@ -368,9 +507,9 @@ __global__ __launch_bounds__(64 * WM * WN) void echo_gemm_fp8_tile_k(const GemmF
   uint32_t ea[MI], ew[NJ], ea1[MI], ew1[NJ];
   auto read_scales = [&](int ring, uint32_t* sa, uint32_t* sw) {
 #pragma unroll
-    for (int i = 0; i < MI; ++i) sa[i] = sc[ring][RW * wm + 32 * i + (lane & 31)];
+    for (int i = 0; i < MI; ++i) sa[i] = sl.scales(ring)[RW * wm + 32 * i + (lane & 31)];
 #pragma unroll
-    for (int j = 0; j < NJ; ++j) sw[j] = sc[ring][BM + CW * wn + 32 * j + (lane & 31)];
+    for (int j = 0; j < NJ; ++j) sw[j] = sl.scales(ring)[BM + CW * wn + 32 * j + (lane & 31)];
   };
   // The instructions of half step HS, reading the next one's fragments (READ) from
   // slab `slab`.
@@ -390,12 +529,8 @@ __global__ __launch_bounds__(64 * WM * WN) void echo_gemm_fp8_tile_k(const GemmF
 #pragma unroll
         for (int i = 0; i < MI; ++i) {
           const i32x8 x8 = __builtin_shufflevector(fa[HS][i][0], fa[HS][i][1], 0, 1, 2, 3, 4, 5, 6, 7);
-          if constexpr (MODE == kScaled8)
-            acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
-                w, x8, acc[i][j], W5 ? 1 : 0, A5 ? 1 : 0, 0, static_cast<int>(ew[j]), 0, static_cast<int>(ea[i]));
-          else
-            blk[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(w, x8, HS == 0 ? zero : blk[i][j], W5 ? 1 : 0,
-                                                                       A5 ? 1 : 0, 0, 127, 0, 127);
+          acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
+              w, x8, acc[i][j], W5 ? 1 : 0, A5 ? 1 : 0, 0, static_cast<int>(ew[j]), 0, static_cast<int>(ea[i]));
         }
         if constexpr (READ) {
           read_w(j, slab, HS ^ 1, 0);
@@ -439,19 +574,7 @@ __global__ __launch_bounds__(64 * WM * WN) void echo_gemm_fp8_tile_k(const GemmF
   constexpr std::true_type kYes{};
   constexpr std::false_type kNo{};
 
-  load_scales();
-  stage_scales(0);
-  if (steps > 1) load_scales();
-  for (int s = 0; s < S && s < steps; ++s) {
-    if (s + 1 < steps) issue(s, s, kNo);
-    else issue(s, s, kYes);
-  }
-  if (steps >= S)
-    __builtin_amdgcn_s_waitcnt(vmcnt_at_most_lds_drained((S - 1) * kLoads));
-  else
-    __builtin_amdgcn_s_waitcnt(vmcnt_at_most_lds_drained(0));
-  slab_barrier();
-  if (steps == 1 && K % 16 != 0) clear_tail(lds);
+  sl.start();
   if constexpr (kFolded) read_scales(0, ea, ew);
 #pragma unroll
   for (int c = 0; c < 2; ++c) {
@@ -460,33 +583,14 @@ __global__ __launch_bounds__(64 * WM * WN) void echo_gemm_fp8_tile_k(const GemmF
     for (int j = 0; j < NJ; ++j) read_w(j, 0, 0, c);
   }
   int cur = 0, ring = 0;  // slab and scales of the step
-  // One K step.  Between its halves, unless it is the last: the scales of the next step
-  // are staged, this wavefront's reads of the slab are done, the next slab has landed,
-  // and the barrier; then the slab is free, and the loads of step it + S go out into it
-  // (ISSUE 1; 2: they are the last step's), so a slab has S - 1 whole steps to arrive.
-  // The scales of step it + 2 are loaded before them: waiting for those waits for
-  // everything issued earlier.  The steps of the main loop have no branch between
-  // the halves: the compiler would move the first half's instructions past it,
-  // behind the barrier.
   auto step = [&](int it, auto issues, auto last) {
     constexpr int ISSUE = decltype(issues)::value;
-    constexpr bool LAST = decltype(last)::value;
     const int next = cur + 1 == S ? 0 : cur + 1, ring1 = ring == 2 ? 0 : ring + 1;
     half_step(H0, kYes, cur);
-    if constexpr (!LAST) {
-      stage_scales(ring1);
-      __builtin_amdgcn_s_waitcnt(vmcnt_at_most_lds_drained(ISSUE != 0 ? (S - 2) * kLoads : 0));
-      __builtin_amdgcn_sched_barrier(0);
-      slab_barrier();
-      if constexpr (ISSUE == 0) {
-        if (it + 2 == steps && K % 16 != 0) clear_tail(lds + next * kSlab);
-        if (it + 2 < steps) load_scales();
-      } else {
-        load_scales();
-      }
+    if constexpr (!decltype(last)::value) {
+      sl.template wait_next<ISSUE>(it, next, ring1);
       if constexpr (kFolded) read_scales(ring1, ea1, ew1);
-      if constexpr (ISSUE == 1) issue(cur, it + S, kNo);
-      if constexpr (ISSUE == 2) issue(cur, it + S, kYes);
+      sl.template refill<ISSUE>(it, cur);
       half_step(H1, kYes, next);
     } else {
       half_step(H1, kNo, 0);
@@ -494,11 +598,11 @@ __global__ __launch_bounds__(64 * WM * WN) void echo_gemm_fp8_tile_k(const GemmF
     if constexpr (!kFolded) {
       float ca[MI];
 #pragma unroll
-      for (int i = 0; i < MI; ++i) ca[i] = __uint_as_float(sc[ring][RW * wm + 32 * i + (lane & 31)]);
+      for (int i = 0; i < MI; ++i) ca[i] = __uint_as_float(sl.scales(ring)[RW * wm + 32 * i + (lane & 31)]);
       if (a.sw_shift != 0) {  // one scale for a sub-tile's 32 columns
 #pragma unroll
         for (int j = 0; j < NJ; ++j) {
-          const float cw = __uint_as_float(sc[ring][BM + CW * wn + 32 * j]);
+          const float cw = __uint_as_float(sl.scales(ring)[BM + CW * wn + 32 * j]);
 #pragma unroll
           for (int i = 0; i < MI; ++i) {
             const float c = ca[i] * cw;
@@ -512,7 +616,7 @@ __global__ __launch_bounds__(64 * WM * WN) void echo_gemm_fp8_tile_k(const GemmF
           f32x4 cw[4];
 #pragma unroll
           for (int v4 = 0; v4 < 4; ++v4)
-            cw[v4] = *reinterpret_cast<const f32x4*>(&sc[ring][BM + CW * wn + 32 * j + 8 * v4 + 4 * half]);
+            cw[v4] = *reinterpret_cast<const f32x4*>(&sl.scales(ring)[BM + CW * wn + 32 * j + 8 * v4 + 4 * half]);
 #pragma unroll
           for (int i = 0; i < MI; ++i)
 #pragma unroll
@@ -520,7 +624,7 @@ __global__ __launch_bounds__(64 * WM * WN) void echo_gemm_fp8_tile_k(const GemmF
               acc[i][j][v] = __builtin_fmaf(blk[i][j][v], ca[i] * cw[v >> 2][v & 3], acc[i][j][v]);
         }
       }
-    } else if constexpr (!LAST) {
+    } else if constexpr (!decltype(last)::value) {
 #pragma unroll
       for (int i = 0; i < MI; ++i) ea[i] = ea1[i];
 #pragma unroll
@@ -529,56 +633,21 @@ __global__ __launch_bounds__(64 * WM * WN) void echo_gemm_fp8_tile_k(const GemmF
     cur = next;
     ring = ring1;
   };
-  int it = 0;
-  for (; it < steps - S - 1; ++it) step(it, std::integral_constant<int, 1>{}, kNo);
-  if (it == steps - S - 1) step(it++, std::integral_constant<int, 2>{}, kNo);
-  for (; it < steps - 1; ++it) step(it, std::integral_constant<int, 0>{}, kNo);
-  step(it, std::integral_constant<int, 0>{}, kYes);
+  sl.run(step);
 
-  // Out through LDS, each wavefront on its own in 32 rows at a time (the slabs are
-  // free once every wavefront is here): a lane's runs of 4 columns go in row-major and
-  // come back as 16 bytes of a row, so the stores cover whole lines.  (Straight from
-  // the accumulators, in 32-byte pieces, the stores of a 256 x 256 tile on every CU
-  // took 10 us.)
   __syncthreads();
   const auto store = [&](auto elem) {
     constexpr int E = decltype(elem)::value;
-    typedef typename ElemOf<E>::T T;
-    typedef T T4 __attribute__((ext_vector_type(4)));
-    constexpr int kPitch = CW * sizeof(T) + 16, kRegion = 32 * kPitch, kPerLane = 16 / sizeof(T);
-    static_assert(NW * kRegion <= S * kSlab + 12 * kRows, "a region of LDS per wavefront");
-    constexpr int kLanes = CW / kPerLane, kStep = 64 / kLanes;  // lanes per row, rows per instruction
-    uint8_t* region = lds + wave * kRegion;
-    const int sr = lane / kLanes, scol = lane % kLanes * kPerLane;
-    const int n = n0 + CW * wn + scol;
+    constexpr int kRegion = SL::kBytes / NW / 16 * 16;
+    store_tile<E, RW, CW, kRegion>(
+        lds + sl.wave * kRegion, a, p.out, tile.m0 + RW * wm, tile.n0 + CW * wn, [&](uint8_t* region, int pitch, int i) {
 #pragma unroll
-    for (int i = 0; i < MI; ++i) {
+          for (int j = 0; j < NJ; ++j)
 #pragma unroll
-      for (int j = 0; j < NJ; ++j)
-#pragma unroll
-        for (int v4 = 0; v4 < 4; ++v4) {
-          const T4 o{narrow<E>(acc[i][j][4 * v4]), narrow<E>(acc[i][j][4 * v4 + 1]), narrow<E>(acc[i][j][4 * v4 + 2]),
-                     narrow<E>(acc[i][j][4 * v4 + 3])};
-          *reinterpret_cast<T4*>(region + (lane & 31) * kPitch + (32 * j + 8 * v4 + 4 * half) * sizeof(T)) = o;
-        }
-      T* row = static_cast<T*>(p.out) + (m0 + RW * wm + 32 * i + sr) * a.ldo + n;
-#pragma unroll
-      for (int u = 0; u < 32 / kStep; ++u) {
-        const u32x4 o = *reinterpret_cast<const u32x4*>(region + (sr + u * kStep) * kPitch + scol * sizeof(T));
-        if (m0 + RW * wm + 32 * i + sr + u * kStep < M) {
-          if (n + kPerLane <= N) {
-            __builtin_memcpy(row, &o, 16);
-          } else {
-            T each[kPerLane];
-            __builtin_memcpy(each, &o, 16);
-#pragma unroll
-            for (int e = 0; e < kPerLane; ++e)
-              if (n + e < N) row[e] = each[e];
-          }
-        }
-        row += kStep * a.ldo;
-      }
-    }
+            for (int v = 0; v < 16; v += 4)
+              put4<E>(region + (lane & 31) * pitch + (32 * j + 2 * v + 4 * half) * sizeof(typename ElemOf<E>::T),
+                      acc[i][j][v], acc[i][j][v + 1], acc[i][j][v + 2], acc[i][j][v + 3]);
+        });
   };
   if constexpr (kBf16) {
     store(std::integral_constant<int, kElemF32>{});
@@ -588,11 +657,153 @@ __global__ __launch_bounds__(64 * WM * WN) void echo_gemm_fp8_tile_k(const GemmF
   }
 }
 
+// fp32 scales on the 8-bit instruction: 16 x 16 sub-tiles, whose v_mfma_..._16x16x128
+// sums a whole block of 128 at once into four registers, so that the scaling (four
+// multiply-adds per instruction, half its time) follows two instructions behind and
+// runs beside the matrix cores, with no second set of accumulators.  Lane l supplies
+// row l % 16 of a sub-tile and the bytes 32 (l / 16) .. + 31 of the K step, and holds
+// row l % 16 of the A rows, columns 4 (l / 16) .. + 3 of the W rows.  A step's fragments
+// of A stay in registers; those of W come one sub-tile ahead.
+// WB: W's scales are of blocks of 128 rows, one for all of a wavefront's columns.
+template <int BM, int BN, int WM, int WN, int S, bool WB, bool A5, bool W5>
+__global__ __launch_bounds__(64 * WM * WN) void echo_gemm_fp8_fma_k(const GemmFp8Args a, uint32_t gm, uint32_t gn) {
+  constexpr int NW = WM * WN, RW = BM / WM, CW = BN / WN, MI = RW / 16, NJ = CW / 16;
+  static_assert(MI * 16 * WM == BM && NJ * 16 * WN == BN && CW <= 128 && 128 % CW == 0, "even splits");
+  static_assert(NJ % 2 == 0 && NJ >= 4, "fragments of W alternate between two sets");
+  typedef Slabs<BM, BN, NW, S, false, false> SL;
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[SL::kBytes];
+  const TileAt tile = tile_at<BM, BN>(gm, gn);
+  const RankPtrs p = rank_ptrs(tile.rank);
+  SL sl;
+  sl.init(lds, a, p, tile);
+  const int lane = sl.lane, sub = lane & 15, g = lane >> 4, wm = sl.wave / WN, wn = sl.wave % WN;
+
+  f32x4 acc[MI][NJ] = {};
+  i32x8 fa[MI], fw[2];
+  int at[2];  // byte offset of this lane's chunk c in a 16-row sub-tile
+#pragma unroll
+  for (int c = 0; c < 2; ++c) at[c] = sub * 128 + 16 * ((2 * g + c) ^ (sub >> 1));
+  auto frag = [&](const uint8_t* b) {
+    const i32x4 lo = *reinterpret_cast<const i32x4*>(b + at[0]), hi = *reinterpret_cast<const i32x4*>(b + at[1]);
+    return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+  };
+  auto read_a = [&](int slab, int i) { fa[i] = frag(lds + slab * SL::kSlab + (RW * wm + 16 * i) * 128); };
+  auto read_w = [&](int slab, int j) {
+    fw[j & 1] = frag(lds + slab * SL::kSlab + SL::kSlabA + (CW * wn + 16 * j) * 128);
+  };
+  // this step's scales: of the lane's rows of A (times W's where one covers all its
+  // columns), and of its columns of the sub-tiles at hand (the previous column's last sums are still to come)
+  float ca[MI];
+  f32x4 cw[3];
+  auto read_ca = [&](int ring) {
+#pragma unroll
+    for (int i = 0; i < MI; ++i) ca[i] = __uint_as_float(sl.scales(ring)[RW * wm + 16 * i + sub]);
+    if constexpr (WB) {
+      const float w = __uint_as_float(sl.scales(ring)[BM + CW * wn]);
+#pragma unroll
+      for (int i = 0; i < MI; ++i) ca[i] = ca[i] * w;
+    }
+  };
+  auto read_cw = [&](int ring, int j) {
+    if constexpr (!WB) cw[j % 3] = *reinterpret_cast<const f32x4*>(sl.scales(ring) + BM + CW * wn + 16 * j + 4 * g);
+  };
+  f32x4 sum[2];  // the last two block sums
+  auto add = [&](int k) {  // the k-th, of sub-tile (k % MI, k / MI)
+    const int i = k % MI, j = k / MI;
+#pragma unroll
+    for (int v = 0; v < 4; ++v)
+      acc[i][j][v] = __builtin_fmaf(sum[k & 1][v], WB ? ca[i] : ca[i] * cw[j % 3][v], acc[i][j][v]);
+  };
+  // the instructions of sub-tile column j
+  auto column = [&](int j) {
+#pragma unroll
+    for (int i = 0; i < MI; ++i) {
+      const int k = j * MI + i;
+      if (k >= 2) add(k - 2);
+#if defined(__HIP_DEVICE_COMPILE__)
+      sum[k & 1] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(fw[j & 1], fa[i], f32x4{}, W5 ? 1 : 0, A5 ? 1 : 0, 0,
+                                                                    127, 0, 127);
+#endif
+    }
+  };
+
+  sl.start();
+#pragma unroll
+  for (int i = 0; i < MI; ++i) read_a(0, i);
+  read_w(0, 0);
+  read_w(0, 1);
+  read_ca(0);
+  read_cw(0, 0);
+  int cur = 0, ring = 0;
+  auto step = [&](int it, auto issues, auto last) {
+    constexpr int ISSUE = decltype(issues)::value;
+    constexpr bool LAST = decltype(last)::value;
+    const int next = cur + 1 == S ? 0 : cur + 1, ring1 = ring == 2 ? 0 : ring + 1;
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) {
+      if (j + 1 < NJ) read_cw(ring, j + 1);
+      column(j);
+      if (j + 2 < NJ) read_w(cur, j + 2);
+      __builtin_amdgcn_sched_barrier(0);
+      if (j + 3 == NJ) {
+        // the slab's last fragments are on their way
+        if constexpr (!LAST) {
+          sl.template wait_next<ISSUE>(it, next, ring1);
+          sl.template refill<ISSUE>(it, cur);
+        }
+      }
+      if constexpr (!LAST) {
+        if (j + 2 >= NJ) read_w(next, j + 2 - NJ);
+      }
+    }
+    if constexpr (!LAST) {
+#pragma unroll
+      for (int i = 0; i < MI; ++i) read_a(next, i);
+    }
+    add(MI * NJ - 2);
+    add(MI * NJ - 1);
+    if constexpr (!LAST) {
+      read_ca(ring1);
+      read_cw(ring1, 0);
+    }
+    cur = next;
+    ring = ring1;
+  };
+  sl.run(step);
+
+  __syncthreads();
+  const auto store = [&](auto elem) {
+    constexpr int E = decltype(elem)::value;
+    constexpr int kRegion = SL::kBytes / NW / 16 * 16;
+    store_tile<E, RW, CW, kRegion>(
+        lds + sl.wave * kRegion, a, p.out, tile.m0 + RW * wm, tile.n0 + CW * wn, [&](uint8_t* region, int pitch, int i) {
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int j = 0; j < NJ; ++j) {
+              const f32x4 o = acc[2 * i + h][j];
+              put4<E>(region + (16 * h + sub) * pitch + (16 * j + 4 * g) * sizeof(typename ElemOf<E>::T), o[0], o[1], o[2],
+                      o[3]);
+            }
+        });
+  };
+  if (a.out_elem == kElemBf16) store(std::integral_constant<int, kElemBf16>{});
+  else store(std::integral_constant<int, kElemF16>{});
+}
+
 template <int BM, int BN, int WM, int WN, int S, int MODE, bool A5, bool W5, bool E8>
 hipError_t tile(const GemmFp8Args& a, int P, hipStream_t s) {
   const uint32_t gm = static_cast<uint32_t>((a.M + BM - 1) / BM), gn = static_cast<uint32_t>((a.N + BN - 1) / BN);
   hipLaunchKernelGGL((echo_gemm_fp8_tile_k<BM, BN, WM, WN, S, MODE, A5, W5, E8>), dim3(gm * gn * P),
                      dim3(64 * WM * WN), 0, s, a, gm, gn);
+  return hipGetLastError();
+}
+
+template <int BM, int BN, int WM, int WN, int S, bool WB, bool A5, bool W5>
+hipError_t fma_tile(const GemmFp8Args& a, int P, hipStream_t s) {
+  const uint32_t gm = static_cast<uint32_t>((a.M + BM - 1) / BM), gn = static_cast<uint32_t>((a.N + BN - 1) / BN);
+  hipLaunchKernelGGL((echo_gemm_fp8_fma_k<BM, BN, WM, WN, S, WB, A5, W5>), dim3(gm * gn * P), dim3(64 * WM * WN), 0, s,
+                     a, gm, gn);
   return hipGetLastError();
 }
 
@@ -623,8 +834,12 @@ hipError_t launch(const GemmFp8Args& a, int P, hipStream_t s) {
     if (4 * big >= 256) return tile<128, 128, 4, 2, 4, kScaled8, A5, W5, E8>(a, P, s);
     return tile<64, 64, 2, 2, 4, kScaled8, A5, W5, E8>(a, P, s);
   } else {
-    if (2 * big >= 256) return tile<256, 128, 4, 2, 3, kPlain8, A5, W5, E8>(a, P, s);
-    return tile<64, 64, 2, 2, 4, kPlain8, A5, W5, E8>(a, P, s);
+    if (a.sw_shift != 0) {
+      if (big >= 256) return fma_tile<256, 256, 4, 2, 2, true, A5, W5>(a, P, s);
+      return fma_tile<64, 128, 2, 2, 4, true, A5, W5>(a, P, s);
+    }
+    if (big >= 256) return fma_tile<256, 256, 4, 2, 2, false, A5, W5>(a, P, s);
+    return fma_tile<64, 128, 2, 2, 4, false, A5, W5>(a, P, s);
   }
 }
 
