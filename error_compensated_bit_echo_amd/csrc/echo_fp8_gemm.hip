@@ -88,111 +88,160 @@ __device__ __forceinline__ void store_each(void* out, int64_t at, int64_t left, 
 
 // ---- few rows of A -------------------------------------------------------------
 //
-// 16 CT columns of the output (rows of W) per workgroup of 8 wavefronts, which share
-// k: wavefront w takes the blocks w, w + 8, ... of 128 and reads its codes of W and
-// A straight from memory (W is read once in all, 2 KiB per instruction pair), and
-// the eight sums meet in LDS in a fixed order.  Bound by the bytes of W.
+// 16 CT columns of the output (rows of W) per workgroup of NW wavefronts, which share
+// k: wavefront w takes the blocks w, w + NW, ... of 128 and reads its codes of W and A
+// straight from memory (W is read once in all), and the sums meet in LDS in a fixed
+// order.  Bound by the bytes of W.  Codes are widened to bfloat16 (the matrix cores
+// idle anyway); exponent-byte scales are applied as they are widened.
 
-constexpr int kThinWaves = 8;
-
-// 32 bytes of a row from byte k on, zeros from K on.  The 16-byte runs that hold a
-// valid byte lie within the row's pitch (a multiple of 16).
-__device__ __forceinline__ i32x8 load_frag(const uint8_t* row, int64_t k, int64_t K) {
-  i32x8 f{};
+// A lane's 32 bytes of a block of 128: 16-byte chunks g and g + 4, so that the four
+// lanes of a row read 64 contiguous bytes at a time.  TAIL: the block is cut off by K,
+// and reads as zeros from there.  (The 16-byte runs that hold a valid byte lie within
+// the row's pitch, a multiple of 16.)
+template <bool TAIL>
+__device__ __forceinline__ i32x8 load_frag(const uint8_t* block, int g, int left) {
+  i32x4 x[2] = {};
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
-    const int64_t at = k + 16 * h;
-    const int64_t left = K - at;
-    if (left <= 0) continue;
-    i32x4 x = *reinterpret_cast<const i32x4*>(row + at);
-    if (left < 16) {
+    const int at = 16 * (g + 4 * h);
+    if constexpr (!TAIL) {
+      x[h] = *reinterpret_cast<const i32x4*>(block + at);
+    } else if (at < left) {
+      x[h] = *reinterpret_cast<const i32x4*>(block + at);
 #pragma unroll
       for (int d = 0; d < 4; ++d) {
-        const int64_t n = left - 4 * d;  // valid bytes of this dword
-        if (n <= 0) x[d] = 0;
-        else if (n < 4) x[d] &= (1 << (8 * n)) - 1;
+        const int n = left - at - 4 * d;  // valid bytes of this dword
+        if (n <= 0) x[h][d] = 0;
+        else if (n < 4) x[h][d] &= (1 << (8 * n)) - 1;
       }
     }
-#pragma unroll
-    for (int d = 0; d < 4; ++d) f[4 * h + d] = x[d];
   }
-  return f;
+  return __builtin_shufflevector(x[0], x[1], 0, 1, 2, 3, 4, 5, 6, 7);
 }
 
-// MT tiles of 16 rows of A.
-template <int MT, int CT, bool A5, bool W5, bool E8>
-__global__ __launch_bounds__(64 * kThinWaves) void echo_gemm_fp8_thin_k(const GemmFp8Args a) {
-  __shared__ f32x4 part[kThinWaves][MT][CT][64];
+// MT tiles of 16 rows of A, CT of 16 rows of W; U blocks' loads go out at a time.
+// WB: fp32 scales of blocks of 128 rows of W, one for a tile's 16 columns.
+template <int MT, int CT, int U, int NW, bool WB, bool A5, bool W5, bool E8>
+__global__ __launch_bounds__(64 * NW) void echo_gemm_fp8_thin_k(const GemmFp8Args a) {
+  __shared__ f32x4 part[NW][MT][CT][64];
   const RankPtrs p = rank_ptrs(blockIdx.z);
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, sub = lane & 15, g = lane >> 4;
-  const int64_t m0 = static_cast<int64_t>(blockIdx.y) * (16 * MT), n0 = static_cast<int64_t>(blockIdx.x) * (16 * CT);
-  int64_t m[MT], n[CT];  // the rows this lane supplies, clamped: what lies past the edge is not stored
+  const int lane = threadIdx.x & 63, sub = lane & 15, g = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int m0 = static_cast<int>(blockIdx.y) * (16 * MT), n0 = static_cast<int>(blockIdx.x) * (16 * CT);
+  const int M = static_cast<int>(a.M), N = static_cast<int>(a.N), K = static_cast<int>(a.K);
+  // The rows this lane supplies, clamped (what lies past the edge is not stored), and
+  // where their scales are: with exponent bytes those of the same rows, with fp32 scales
+  // W's of the four columns the lane holds.
+  constexpr int kScalesW = E8 || WB ? 1 : 4;
+  const uint8_t *rowA[MT], *rowW[CT];
+  uint32_t sa[MT], sw[CT][kScalesW];
 #pragma unroll
-  for (int i = 0; i < MT; ++i) m[i] = m0 + 16 * i + sub < a.M ? m0 + 16 * i + sub : a.M - 1;
+  for (int i = 0; i < MT; ++i) {
+    const int m = m0 + 16 * i + sub < M ? m0 + 16 * i + sub : M - 1;
+    rowA[i] = p.A + m * a.lda;
+    sa[i] = static_cast<uint32_t>((m >> a.sa_shift) * a.sa_row);
+  }
 #pragma unroll
-  for (int j = 0; j < CT; ++j) n[j] = n0 + 16 * j + sub < a.N ? n0 + 16 * j + sub : a.N - 1;
+  for (int j = 0; j < CT; ++j) {
+    const int n = n0 + 16 * j + sub < N ? n0 + 16 * j + sub : N - 1;
+    rowW[j] = p.W + n * a.ldw;
+#pragma unroll
+    for (int v = 0; v < kScalesW; ++v) {
+      const int c = E8 ? n : n0 + 16 * j + 4 * g + v < N ? n0 + 16 * j + 4 * g + v : N - 1;
+      sw[j][v] = static_cast<uint32_t>((c >> a.sw_shift) * a.sw_row);
+    }
+  }
   f32x4 acc[MT][CT] = {};
-  const int64_t nb = (a.K + kFp8Block - 1) / kFp8Block;
-#pragma unroll 2
-  for (int64_t b = wave; b < nb; b += kThinWaves) {
+  struct Block {
     i32x8 fa[MT], fw[CT];
+    uint32_t ca[MT], cw[CT][kScalesW];
+  };
+  auto load = [&](Block& x, int b, auto tail) {
+    constexpr bool TAIL = decltype(tail)::value;
+    const int left = K - b * kFp8Block;
 #pragma unroll
-    for (int j = 0; j < CT; ++j) fw[j] = load_frag(p.W + n[j] * a.ldw, b * kFp8Block + 32 * g, a.K);
+    for (int j = 0; j < CT; ++j) x.fw[j] = load_frag<TAIL>(rowW[j] + b * kFp8Block, g, left);
 #pragma unroll
-    for (int i = 0; i < MT; ++i) fa[i] = load_frag(p.A + m[i] * a.lda, b * kFp8Block + 32 * g, a.K);
-    float ca[MT], cw[CT][4];
+    for (int i = 0; i < MT; ++i) x.fa[i] = load_frag<TAIL>(rowA[i] + b * kFp8Block, g, left);
+    constexpr int kBytes = E8 ? 1 : 4;
+    const uint8_t* const pa = static_cast<const uint8_t*>(p.sA) + b * a.sa_k * kBytes;
+    const uint8_t* const pw = static_cast<const uint8_t*>(p.sW) + b * a.sw_k * kBytes;
 #pragma unroll
-    for (int i = 0; i < MT; ++i)
-      ca[i] = scale_value<E8>(scale_bits<E8>(p.sA, (m[i] >> a.sa_shift) * a.sa_row + b * a.sa_k));
+    for (int i = 0; i < MT; ++i) x.ca[i] = scale_bits<E8>(pa, sa[i]);
 #pragma unroll
     for (int j = 0; j < CT; ++j)
 #pragma unroll
-      for (int v = 0; v < 4; ++v) {
-        int64_t nn = n0 + 16 * j + 4 * g + v;
-        nn = nn < a.N ? nn : a.N - 1;
-        cw[j][v] = scale_value<E8>(scale_bits<E8>(p.sW, (nn >> a.sw_shift) * a.sw_row + b * a.sw_k));
-      }
+      for (int v = 0; v < kScalesW; ++v) x.cw[j][v] = scale_bits<E8>(pw, sw[j][v]);
+  };
+  auto multiply = [&](const Block& x) {
     f32x4 t[MT][CT] = {};
 #pragma unroll
     for (int s = 0; s < 4; ++s) {
       bf16x8 wa[CT];
 #pragma unroll
-      for (int j = 0; j < CT; ++j) wa[j] = widen8<W5>(fw[j][2 * s], fw[j][2 * s + 1]);
+      for (int j = 0; j < CT; ++j)
+        wa[j] = widen8<W5>(x.fw[j][2 * s], x.fw[j][2 * s + 1], E8 ? scale_value<E8>(x.cw[j][0]) : 1.0f);
 #pragma unroll
       for (int i = 0; i < MT; ++i) {
-        const bf16x8 aa = widen8<A5>(fa[i][2 * s], fa[i][2 * s + 1]);
+        const bf16x8 aa = widen8<A5>(x.fa[i][2 * s], x.fa[i][2 * s + 1], E8 ? scale_value<E8>(x.ca[i]) : 1.0f);
 #if defined(__HIP_DEVICE_COMPILE__)
 #pragma unroll
-        for (int j = 0; j < CT; ++j) t[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wa[j], aa, t[i][j], 0, 0, 0);
+        for (int j = 0; j < CT; ++j) {
+          f32x4& c = E8 ? acc[i][j] : t[i][j];
+          c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wa[j], aa, c, 0, 0, 0);
+        }
 #endif
       }
     }
+    if constexpr (!E8) {
 #pragma unroll
-    for (int i = 0; i < MT; ++i)
+      for (int i = 0; i < MT; ++i)
 #pragma unroll
-      for (int j = 0; j < CT; ++j)
+        for (int j = 0; j < CT; ++j)
 #pragma unroll
-        for (int v = 0; v < 4; ++v) acc[i][j][v] = __builtin_fmaf(t[i][j][v], ca[i] * cw[j][v], acc[i][j][v]);
+          for (int v = 0; v < 4; ++v)
+            acc[i][j][v] = __builtin_fmaf(t[i][j][v], __uint_as_float(x.ca[i]) * __uint_as_float(x.cw[j][WB ? 0 : v]),
+                                          acc[i][j][v]);
+    }
+  };
+  const int full = K / kFp8Block;
+  int b = wave;
+  for (; b + (U - 1) * NW < full; b += U * NW) {
+    Block x[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) load(x[u], b + u * NW, std::false_type{});
+#pragma unroll
+    for (int u = 0; u < U; ++u) multiply(x[u]);
+  }
+  for (; b < full; b += NW) {
+    Block x;
+    load(x, b, std::false_type{});
+    multiply(x);
+  }
+  if (b == full && K % kFp8Block != 0) {
+    Block x;
+    load(x, b, std::true_type{});
+    multiply(x);
   }
 #pragma unroll
   for (int i = 0; i < MT; ++i)
 #pragma unroll
     for (int j = 0; j < CT; ++j) part[wave][i][j][lane] = acc[i][j];
   __syncthreads();
-  // wavefront w sums and writes the sub-tiles w, w + 8, ...
-  for (int u = wave; u < MT * CT; u += kThinWaves) {
+  // wavefront w sums and writes the sub-tiles w, w + NW, ...
+  for (int u = wave; u < MT * CT; u += NW) {
     const int i = u / CT, j = u - i * CT;
     f32x4 s = part[0][i][j][lane];
 #pragma unroll
-    for (int w = 1; w < kThinWaves; ++w) {
+    for (int w = 1; w < NW; ++w) {
       const f32x4 x = part[w][i][j][lane];
 #pragma unroll
       for (int v = 0; v < 4; ++v) s[v] = s[v] + x[v];
     }
-    const int64_t mm = m0 + 16 * i + sub, nn = n0 + 16 * j + 4 * g;
-    if (mm < a.M) {
+    const int mm = m0 + 16 * i + sub, nn = n0 + 16 * j + 4 * g;
+    if (mm < M) {
       const float v[4] = {s[0], s[1], s[2], s[3]};
-      store_each(p.out, mm * a.ldo + nn, a.N - nn, v, 4, a.out_elem);
+      store_each(p.out, mm * a.ldo + nn, N - nn, v, 4, a.out_elem);
     }
   }
 }
@@ -807,50 +856,80 @@ hipError_t fma_tile(const GemmFp8Args& a, int P, hipStream_t s) {
   return hipGetLastError();
 }
 
-template <int MT, int CT, bool A5, bool W5, bool E8>
+template <int MT, int CT, int U, int NW, bool WB, bool A5, bool W5, bool E8>
 hipError_t thin(const GemmFp8Args& a, int P, hipStream_t s) {
   const dim3 grid(static_cast<unsigned>((a.N + 16 * CT - 1) / (16 * CT)),
                   static_cast<unsigned>((a.M + 16 * MT - 1) / (16 * MT)), static_cast<unsigned>(P));
-  hipLaunchKernelGGL((echo_gemm_fp8_thin_k<MT, CT, A5, W5, E8>), grid, dim3(64 * kThinWaves), 0, s, a);
+  hipLaunchKernelGGL((echo_gemm_fp8_thin_k<MT, CT, U, NW, WB, A5, W5, E8>), grid, dim3(64 * NW), 0, s, a);
   return hipGetLastError();
 }
 
-template <bool A5, bool W5, bool E8>
+// E8: exponent-byte scales.  WB: fp32 scales, W's of blocks of 128 rows.
+//
+// Up to 32 rows of A: the kernel that shares k, by the number of 16-row tiles of W over
+// all ranks, so that there are enough workgroups to fill the chip and as much in flight
+// as possible.  Measured with cold weights, us: P = 8, M = 16, N = 4096, K = 1024:
+// 9.9 with 4 tiles per workgroup of 8 wavefronts, 12.2 with 2 of 16, 15.3 with 1 of 8;
+// P = 8, N = 1024, K = 4096: 10.3 with 2 tiles of 16 wavefronts, 12.5 with 1 of 16; one
+// token against N = K = 8192, where A costs nothing: 19.0 and 15.8.
+// Above that, tiles by the number b of 128 x 128 tiles over all ranks:
+//   b < 192: 64 rows, four wavefronts, 4 slabs (P = 4, M = 128, N = K = 4096: 21.9
+//     against 25.2 with 128 x 128 tiles);
+//   b < 384: 128 x 128, four wavefronts, 2 slabs, two workgroups per CU (M = 1024,
+//     N = K = 4096: 25.4 against 30.6 with 256 x 128 tiles and 40.2 with 64 x 64);
+//   256 x 256 where those number at least 192, three quarters of the CUs (P = 4,
+//     M = 2048, N = K = 4096: 130 against 168 with 128 x 128 tiles);
+//   else 256 x 128, 3 slabs (P = 2, M = 1024, N = K = 4096: 37.3 against 38.5 with
+//     128 x 128 and 76 with 64 x 64).
+// The same with fp32 scales, in tiles of 64 x 128 (23.3 against 28.3 at the first shape;
+// 43.4 against 47.4 and 80 at the last).
+template <bool A5, bool W5, bool E8, bool WB>
 hipError_t launch(const GemmFp8Args& a, int P, hipStream_t s) {
-  if (a.M <= 16 || a.K == 0) return thin<1, 1, A5, W5, E8>(a, P, s);
-  if (a.M <= 32) return thin<2, 1, A5, W5, E8>(a, P, s);
-  const int64_t big = (a.M + 255) / 256 * ((a.N + 255) / 256) * P;
+  const int64_t columns = (a.N + 15) / 16 * P;  // 16 rows of W each
+  if (a.M <= 16 || a.K == 0) {
+    if (columns >= 1024) return thin<1, 4, 1, 8, WB, A5, W5, E8>(a, P, s);
+    if (columns >= 512 && a.M > 4) return thin<1, 2, 1, 16, WB, A5, W5, E8>(a, P, s);
+    return thin<1, 1, 2, 16, WB, A5, W5, E8>(a, P, s);
+  }
+  if (a.M <= 32) return thin<2, 2, 2, 8, WB, A5, W5, E8>(a, P, s);
+  const int64_t b = (a.M + 127) / 128 * ((a.N + 127) / 128) * P;
+  const bool large = (a.M + 255) / 256 * ((a.N + 255) / 256) * P >= 192;
   if (a.out_elem == kElemF32) {
     if constexpr (E8) {
-      if (big >= 256) return tile<256, 256, 4, 2, 2, kWideScaled, A5, W5, E8>(a, P, s);
-      return tile<64, 64, 2, 2, 4, kWideScaled, A5, W5, E8>(a, P, s);
+      if (b < 192) return tile<64, 64, 2, 2, 4, kWideScaled, A5, W5, true>(a, P, s);
+      if (b < 384) return tile<128, 128, 2, 2, 2, kWideScaled, A5, W5, true>(a, P, s);
+      if (large) return tile<256, 256, 4, 2, 2, kWideScaled, A5, W5, true>(a, P, s);
+      return tile<256, 128, 4, 2, 3, kWideScaled, A5, W5, true>(a, P, s);
     } else {
-      if (2 * big >= 256) return tile<256, 128, 4, 2, 3, kWide, A5, W5, E8>(a, P, s);
-      return tile<64, 64, 2, 2, 4, kWide, A5, W5, E8>(a, P, s);
+      if (b < 192) return tile<64, 64, 2, 2, 4, kWide, A5, W5, false>(a, P, s);
+      if (b < 384) return tile<128, 128, 2, 2, 2, kWide, A5, W5, false>(a, P, s);
+      return tile<256, 128, 4, 2, 3, kWide, A5, W5, false>(a, P, s);
     }
   }
   if constexpr (E8) {
-    if (big >= 256) return tile<256, 256, 4, 2, 2, kScaled8, A5, W5, E8>(a, P, s);
-    if (4 * big >= 256) return tile<128, 128, 4, 2, 4, kScaled8, A5, W5, E8>(a, P, s);
-    return tile<64, 64, 2, 2, 4, kScaled8, A5, W5, E8>(a, P, s);
+    if (b < 192) return tile<64, 64, 2, 2, 4, kScaled8, A5, W5, true>(a, P, s);
+    if (b < 384) return tile<128, 128, 2, 2, 2, kScaled8, A5, W5, true>(a, P, s);
+    if (large) return tile<256, 256, 4, 2, 2, kScaled8, A5, W5, true>(a, P, s);
+    return tile<256, 128, 4, 2, 3, kScaled8, A5, W5, true>(a, P, s);
   } else {
-    if (a.sw_shift != 0) {
-      if (big >= 256) return fma_tile<256, 256, 4, 2, 2, true, A5, W5>(a, P, s);
-      return fma_tile<64, 128, 2, 2, 4, true, A5, W5>(a, P, s);
-    }
-    if (big >= 256) return fma_tile<256, 256, 4, 2, 2, false, A5, W5>(a, P, s);
-    return fma_tile<64, 128, 2, 2, 4, false, A5, W5>(a, P, s);
+    if (b < 192) return fma_tile<64, 128, 2, 2, 4, WB, A5, W5>(a, P, s);
+    if (b < 384) return fma_tile<128, 128, 2, 2, 2, WB, A5, W5>(a, P, s);
+    if (large) return fma_tile<256, 256, 4, 2, 2, WB, A5, W5>(a, P, s);
+    return fma_tile<256, 128, 4, 2, 3, WB, A5, W5>(a, P, s);
   }
+}
+
+template <bool A5, bool W5>
+hipError_t launch_formats(const GemmFp8Args& a, int P, bool e8m0, hipStream_t s) {
+  if (e8m0) return launch<A5, W5, true, false>(a, P, s);
+  return a.sw_shift != 0 ? launch<A5, W5, false, true>(a, P, s) : launch<A5, W5, false, false>(a, P, s);
 }
 
 }  // namespace
 
 hipError_t launch_gemm_fp8(const GemmFp8Args& a, int P, bool a_e5m2, bool w_e5m2, bool e8m0, hipStream_t s) {
-  if (e8m0)
-    return a_e5m2 ? (w_e5m2 ? launch<true, true, true>(a, P, s) : launch<true, false, true>(a, P, s))
-                  : (w_e5m2 ? launch<false, true, true>(a, P, s) : launch<false, false, true>(a, P, s));
-  return a_e5m2 ? (w_e5m2 ? launch<true, true, false>(a, P, s) : launch<true, false, false>(a, P, s))
-                : (w_e5m2 ? launch<false, true, false>(a, P, s) : launch<false, false, false>(a, P, s));
+  if (a_e5m2) return w_e5m2 ? launch_formats<true, true>(a, P, e8m0, s) : launch_formats<true, false>(a, P, e8m0, s);
+  return w_e5m2 ? launch_formats<false, true>(a, P, e8m0, s) : launch_formats<false, false>(a, P, e8m0, s);
 }
 
 }  // namespace echo

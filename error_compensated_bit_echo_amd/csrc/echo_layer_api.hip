@@ -76,8 +76,10 @@ echo_status check_fp8(const echo_fp8& f, int32_t P, int64_t rows, int64_t k, boo
   if (f.codes == nullptr || f.scales == nullptr) return ECHO_ERR_ARG;
   if (f.ld < k || f.ld % 16 != 0 || f.ld > echo::kFp8MaxDim) return ECHO_ERR_SHAPE;
   const int64_t n0 = f.block_rows == 1 ? rows : blocks(rows), n1 = blocks(k);
-  if (f.scale_row_stride < 0 || f.scale_k_stride < 0 || f.scale_row_stride > (int64_t{1} << 32) ||
-      f.scale_k_stride > (int64_t{1} << 32))
+  if (f.scale_row_stride < 0 || f.scale_k_stride < 0) return ECHO_ERR_SHAPE;
+  // the kernels address the scales of a block along k through 32-bit offsets
+  constexpr int64_t kMaxExtent = int64_t{1} << 29;
+  if ((n0 > 1 && f.scale_row_stride > kMaxExtent / n0) || (n1 > 1 && f.scale_k_stride > kMaxExtent / n1))
     return ECHO_ERR_SHAPE;
   if (output) {
     // distinct elements: one stride steps over the whole extent of the other dimension

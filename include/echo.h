@@ -324,8 +324,9 @@ typedef enum { ECHO_SCALE_F32 = 0, ECHO_SCALE_E8M0 = 1 } echo_scale_type;
  * stands for codes[i * ld + j] * scales[(i / block_rows) * scale_row_stride +
  * (j / 128) * scale_k_stride].  codes: 16-byte aligned, ld a multiple of 16 and
  * at most 2^22; bytes k .. ld - 1 of a row are never used or written (up to the
- * next multiple of 16 they may be read).  Scales next to each other for
- * consecutive rows (scale_row_stride 1) are read and written fastest. */
+ * next multiple of 16 they may be read).  Each scale stride times its count of
+ * scales is at most 2^29; scales next to each other for consecutive rows
+ * (scale_row_stride 1) are read and written fastest. */
 typedef struct {
   void* const* codes;       /* host array of P device pointers                   */
   void* const* scales;      /* host array of P device pointers                   */
