@@ -288,15 +288,17 @@ __device__ __forceinline__ TileAt tile_at(uint32_t gm, uint32_t gn) {
 }
 
 // The slabs and scales of a tile's K steps.  BYTES: scales are staged as exponent
-// bytes, else as fp32.
-template <int BM, int BN, int NW, int S, bool BYTES, bool E8>
+// bytes, else as fp32.  G: groups of NW wavefronts that share k, each with slabs of its
+// own: step `it` of group g is block G it + g, and all groups take as many steps (past
+// the last block they multiply zeros).
+template <int BM, int BN, int NW, int S, int G, bool BYTES, bool E8>
 struct Slabs {
   static constexpr int kThreads = 64 * NW;
   static constexpr int JA = BM / (8 * NW), JW = BN / (8 * NW), kLoads = JA + JW;  // 1 KiB slab blocks per wavefront
   static constexpr int kSlabA = BM * 128, kSlab = (BM + BN) * 128;
   static constexpr int kPer = (BM + BN + kThreads - 1) / kThreads;  // scales per thread
   static constexpr int kRows = kPer * kThreads;                     // rows with a scale, rounded up to whole threads
-  static constexpr int kBytes = S * kSlab + 3 * 4 * kRows;
+  static constexpr int kBytes = S * kSlab + 3 * 4 * kRows;          // of a group
   static_assert(JA * 8 * NW == BM && JW * 8 * NW == BN, "slab blocks split evenly");
   static_assert(BM % 64 == 0 && BN % 64 == 0, "a wavefront stages scales of one operand");
 
@@ -308,7 +310,7 @@ struct Slabs {
   const uint8_t* sp[kPer];
   int64_t sk[kPer];
   uint32_t sreg[kPer];
-  int K, K16, steps, t, lane, wave;
+  int K, K16, blocks, steps, t, lane, wave, group, sblock;
 
   __device__ __forceinline__ int chunk_of(int row) const { return (lane & 7) ^ ((row >> 1) & 7); }
   __device__ __forceinline__ uint32_t* scales(int ring) const {
@@ -316,13 +318,17 @@ struct Slabs {
   }
 
   __device__ __forceinline__ void init(uint8_t* l, const GemmFp8Args& a, const RankPtrs& p, const TileAt& at) {
-    lds = l;
-    t = threadIdx.x;
+    wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    group = G == 1 ? 0 : wave / NW;
+    wave -= group * NW;
+    lds = l + group * kBytes;
+    t = threadIdx.x - group * kThreads;
     lane = t & 63;
-    wave = __builtin_amdgcn_readfirstlane(t >> 6);
     K = static_cast<int>(a.K);
     K16 = (K + 15) / 16 * 16;
-    steps = (K + 127) / 128;
+    blocks = (K + 127) / 128;
+    steps = (blocks + G - 1) / G;
+    sblock = group;
     const int M = static_cast<int>(a.M), N = static_cast<int>(a.N);
     const int rows_a = M - at.m0 < BM ? M - at.m0 : BM, rows_w = N - at.n0 < BN ? N - at.n0 : BN;
     rA = buffer_rsrc(p.A + at.m0 * a.lda, static_cast<int32_t>((rows_a - 1) * a.lda + K16));
@@ -358,27 +364,28 @@ struct Slabs {
   __device__ __forceinline__ void issue(int buf, int it) {
     uint8_t* As = lds + buf * kSlab + 1024 * JA * wave;
     uint8_t* Ws = lds + buf * kSlab + kSlabA + 1024 * JW * wave;
-    const int chunks = (K16 - it * 128) / 16;
+    int from = (it * G + group) * 128;
+    const int chunks = (K16 - from) / 16;
+    if constexpr (G > 1 && LAST) from = chunks > 0 ? from : 0;  // past K: every chunk is out of range by itself
 #pragma unroll
     for (int j = 0; j < JA; ++j) {
       uint32_t off = offA[j];
       if constexpr (LAST) off = chunk_of(8 * (JA * wave + j) + (lane >> 3)) < chunks ? off : kPastEnd;
-      buffer_load_lds16<0>(rA, As + 1024 * j, off, static_cast<uint32_t>(it * 128));
+      buffer_load_lds16<0>(rA, As + 1024 * j, off, static_cast<uint32_t>(from));
     }
 #pragma unroll
     for (int j = 0; j < JW; ++j) {
       uint32_t off = offW[j];
       if constexpr (LAST) off = chunk_of(8 * (JW * wave + j) + (lane >> 3)) < chunks ? off : kPastEnd;
-      buffer_load_lds16<0>(rW, Ws + 1024 * j, off, static_cast<uint32_t>(it * 128));
+      buffer_load_lds16<0>(rW, Ws + 1024 * j, off, static_cast<uint32_t>(from));
     }
   }
 
   __device__ __forceinline__ void load_scales() {  // the next K step's
+    const int b = G == 1 || sblock < blocks ? sblock : blocks - 1;  // past the last block any scale does
 #pragma unroll
-    for (int u = 0; u < kPer; ++u) {
-      sreg[u] = scale_bits<E8>(sp[u], 0);
-      sp[u] += sk[u];
-    }
+    for (int u = 0; u < kPer; ++u) sreg[u] = scale_bits<E8>(sp[u] + b * sk[u], 0);
+    sblock += G;
   }
   __device__ __forceinline__ void stage_scales(int ring) {
 #pragma unroll
@@ -390,7 +397,7 @@ struct Slabs {
   // would survive a product with zero).
   __device__ __forceinline__ void clear_tail(int buf) {
     const int c = K % 128 / 16, n = K % 16;
-    for (int row = t; row < BM + BN; row += kThreads) {
+    for (int row = (blocks - 1) % G == group ? t : BM + BN; row < BM + BN; row += kThreads) {
       const int in = row < BM ? row : row - BM;
       uint8_t* b = lds + buf * kSlab + row * 128 + 16 * (c ^ ((in >> 1) & 7));
       for (int i = n; i < 16; ++i) b[i] = 0;
@@ -453,6 +460,29 @@ struct Slabs {
   }
 };
 
+// Adds the groups' accumulators (N runs of four per lane) in group 0, in a fixed order:
+// the others leave theirs in their own part of LDS.  False: this wavefront is done.
+template <typename SL, int G, int N>
+__device__ __forceinline__ bool join_groups(uint8_t* lds, const SL& sl, f32x4 (&acc)[N]) {
+  static_assert(SL::kThreads * N * 16 <= SL::kBytes, "a group's accumulators fit its part of LDS");
+  if (sl.group != 0) {
+    f32x4* mine = reinterpret_cast<f32x4*>(lds + sl.group * SL::kBytes) + sl.wave * (64 * N) + sl.lane;
+#pragma unroll
+    for (int i = 0; i < N; ++i) mine[64 * i] = acc[i];
+  }
+  __syncthreads();
+  if (sl.group != 0) return false;
+#pragma unroll
+  for (int g = 1; g < G; ++g) {
+    const f32x4* theirs = reinterpret_cast<const f32x4*>(lds + g * SL::kBytes) + sl.wave * (64 * N) + sl.lane;
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+#pragma unroll
+      for (int v = 0; v < 4; ++v) acc[i][v] = acc[i][v] + theirs[64 * i][v];
+  }
+  return true;
+}
+
 // Writes RW x CW of the tile out of a wavefront's registers, 32 rows at a time, through
 // its own region of LDS (the slabs are free once every wavefront is here): `put(region,
 // pitch, i)` lays rows 32 i .. 32 i + 31 out row-major, and they come back as 16 bytes
@@ -507,16 +537,16 @@ enum TileMode {
 // 64 (l / 32) .. + 63 of the K step, in two half steps.  Accumulator v of lane l is
 // row l % 32 of the tile's A rows and column 8 (v / 4) + 4 (l / 32) + v % 4 of its W
 // rows.
-template <int BM, int BN, int WM, int WN, int S, int MODE, bool A5, bool W5, bool E8>
-__global__ __launch_bounds__(64 * WM * WN) void echo_gemm_fp8_tile_k(const GemmFp8Args a, uint32_t gm, uint32_t gn) {
+template <int BM, int BN, int WM, int WN, int S, int G, int MODE, bool A5, bool W5, bool E8>
+__global__ __launch_bounds__(64 * WM * WN * G) void echo_gemm_fp8_tile_k(const GemmFp8Args a, uint32_t gm, uint32_t gn) {
   constexpr bool kBf16 = MODE == kWide || MODE == kWideScaled;       // else the 8-bit instruction
   constexpr bool kFolded = MODE == kScaled8 || MODE == kWideScaled;  // scales applied with the products
   static_assert(!kFolded || E8, "only exponent bytes fold into the products");
   constexpr int NW = WM * WN, RW = BM / WM, CW = BN / WN, MI = RW / 32, NJ = CW / 32;
   static_assert(MI * 32 * WM == BM && NJ * 32 * WN == BN, "even splits");
-  typedef Slabs<BM, BN, NW, S, MODE == kScaled8, E8> SL;
+  typedef Slabs<BM, BN, NW, S, G, MODE == kScaled8, E8> SL;
   constexpr int kSlab = SL::kSlab, kSlabA = SL::kSlabA;
-  __shared__ __attribute__((aligned(1024))) uint8_t lds[SL::kBytes];
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[G * SL::kBytes];
   const TileAt tile = tile_at<BM, BN>(gm, gn);
   const RankPtrs p = rank_ptrs(tile.rank);
   SL sl;
@@ -544,12 +574,12 @@ __global__ __launch_bounds__(64 * WM * WN) void echo_gemm_fp8_tile_k(const GemmF
 #pragma unroll
     for (int c = 0; c < 2; ++c) at[hs][c] = (lane & 31) * 128 + 16 * ((4 * half + 2 * hs + c) ^ ((lane >> 1) & 7));
   auto read_a = [&](int set, int slab, int hs, int c) {
-    const uint8_t* b = lds + slab * kSlab + RW * wm * 128 + at[hs][c];
+    const uint8_t* b = sl.lds + slab * kSlab + RW * wm * 128 + at[hs][c];
 #pragma unroll
     for (int i = 0; i < MI; ++i) fa[set][i][c] = *reinterpret_cast<const i32x4*>(b + 4096 * i);
   };
   auto read_w = [&](int j, int slab, int hs, int c) {
-    const uint8_t* b = lds + slab * kSlab + kSlabA + CW * wn * 128 + at[hs][c];
+    const uint8_t* b = sl.lds + slab * kSlab + kSlabA + CW * wn * 128 + at[hs][c];
     fw[j][c] = *reinterpret_cast<const i32x4*>(b + 4096 * j);
   };
   // kFolded: the scales of the rows this lane supplies, this step's and the next's
@@ -685,6 +715,14 @@ __global__ __launch_bounds__(64 * WM * WN) void echo_gemm_fp8_tile_k(const GemmF
   sl.run(step);
 
   __syncthreads();
+  if constexpr (G > 1) {
+    f32x4 flat[MI * NJ * 4];
+#pragma unroll
+    for (int i = 0; i < MI * NJ * 16; ++i) flat[i / 4][i % 4] = acc[i / 16 / NJ][i / 16 % NJ][i % 16];
+    if (!join_groups<SL, G>(lds, sl, flat)) return;
+#pragma unroll
+    for (int i = 0; i < MI * NJ * 16; ++i) acc[i / 16 / NJ][i / 16 % NJ][i % 16] = flat[i / 4][i % 4];
+  }
   const auto store = [&](auto elem) {
     constexpr int E = decltype(elem)::value;
     constexpr int kRegion = SL::kBytes / NW / 16 * 16;
@@ -714,13 +752,13 @@ __global__ __launch_bounds__(64 * WM * WN) void echo_gemm_fp8_tile_k(const GemmF
 // row l % 16 of the A rows, columns 4 (l / 16) .. + 3 of the W rows.  A step's fragments
 // of A stay in registers; those of W come one sub-tile ahead.
 // WB: W's scales are of blocks of 128 rows, one for all of a wavefront's columns.
-template <int BM, int BN, int WM, int WN, int S, bool WB, bool A5, bool W5>
-__global__ __launch_bounds__(64 * WM * WN) void echo_gemm_fp8_fma_k(const GemmFp8Args a, uint32_t gm, uint32_t gn) {
+template <int BM, int BN, int WM, int WN, int S, int G, bool WB, bool A5, bool W5>
+__global__ __launch_bounds__(64 * WM * WN * G) void echo_gemm_fp8_fma_k(const GemmFp8Args a, uint32_t gm, uint32_t gn) {
   constexpr int NW = WM * WN, RW = BM / WM, CW = BN / WN, MI = RW / 16, NJ = CW / 16;
   static_assert(MI * 16 * WM == BM && NJ * 16 * WN == BN && CW <= 128 && 128 % CW == 0, "even splits");
   static_assert(NJ % 2 == 0 && NJ >= 4, "fragments of W alternate between two sets");
-  typedef Slabs<BM, BN, NW, S, false, false> SL;
-  __shared__ __attribute__((aligned(1024))) uint8_t lds[SL::kBytes];
+  typedef Slabs<BM, BN, NW, S, G, false, false> SL;
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[G * SL::kBytes];
   const TileAt tile = tile_at<BM, BN>(gm, gn);
   const RankPtrs p = rank_ptrs(tile.rank);
   SL sl;
@@ -736,9 +774,9 @@ __global__ __launch_bounds__(64 * WM * WN) void echo_gemm_fp8_fma_k(const GemmFp
     const i32x4 lo = *reinterpret_cast<const i32x4*>(b + at[0]), hi = *reinterpret_cast<const i32x4*>(b + at[1]);
     return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
   };
-  auto read_a = [&](int slab, int i) { fa[i] = frag(lds + slab * SL::kSlab + (RW * wm + 16 * i) * 128); };
+  auto read_a = [&](int slab, int i) { fa[i] = frag(sl.lds + slab * SL::kSlab + (RW * wm + 16 * i) * 128); };
   auto read_w = [&](int slab, int j) {
-    fw[j & 1] = frag(lds + slab * SL::kSlab + SL::kSlabA + (CW * wn + 16 * j) * 128);
+    fw[j & 1] = frag(sl.lds + slab * SL::kSlab + SL::kSlabA + (CW * wn + 16 * j) * 128);
   };
   // this step's scales: of the lane's rows of A (times W's where one covers all its
   // columns), and of its columns of the sub-tiles at hand (the previous column's last sums are still to come)
@@ -821,6 +859,14 @@ __global__ __launch_bounds__(64 * WM * WN) void echo_gemm_fp8_fma_k(const GemmFp
   sl.run(step);
 
   __syncthreads();
+  if constexpr (G > 1) {
+    f32x4 flat[MI * NJ];
+#pragma unroll
+    for (int i = 0; i < MI * NJ; ++i) flat[i] = acc[i / NJ][i % NJ];
+    if (!join_groups<SL, G>(lds, sl, flat)) return;
+#pragma unroll
+    for (int i = 0; i < MI * NJ; ++i) acc[i / NJ][i % NJ] = flat[i];
+  }
   const auto store = [&](auto elem) {
     constexpr int E = decltype(elem)::value;
     constexpr int kRegion = SL::kBytes / NW / 16 * 16;
@@ -840,18 +886,18 @@ __global__ __launch_bounds__(64 * WM * WN) void echo_gemm_fp8_fma_k(const GemmFp
   else store(std::integral_constant<int, kElemF16>{});
 }
 
-template <int BM, int BN, int WM, int WN, int S, int MODE, bool A5, bool W5, bool E8>
+template <int BM, int BN, int WM, int WN, int S, int G, int MODE, bool A5, bool W5, bool E8>
 hipError_t tile(const GemmFp8Args& a, int P, hipStream_t s) {
   const uint32_t gm = static_cast<uint32_t>((a.M + BM - 1) / BM), gn = static_cast<uint32_t>((a.N + BN - 1) / BN);
-  hipLaunchKernelGGL((echo_gemm_fp8_tile_k<BM, BN, WM, WN, S, MODE, A5, W5, E8>), dim3(gm * gn * P),
-                     dim3(64 * WM * WN), 0, s, a, gm, gn);
+  hipLaunchKernelGGL((echo_gemm_fp8_tile_k<BM, BN, WM, WN, S, G, MODE, A5, W5, E8>), dim3(gm * gn * P),
+                     dim3(64 * WM * WN * G), 0, s, a, gm, gn);
   return hipGetLastError();
 }
 
-template <int BM, int BN, int WM, int WN, int S, bool WB, bool A5, bool W5>
+template <int BM, int BN, int WM, int WN, int S, int G, bool WB, bool A5, bool W5>
 hipError_t fma_tile(const GemmFp8Args& a, int P, hipStream_t s) {
   const uint32_t gm = static_cast<uint32_t>((a.M + BM - 1) / BM), gn = static_cast<uint32_t>((a.N + BN - 1) / BN);
-  hipLaunchKernelGGL((echo_gemm_fp8_fma_k<BM, BN, WM, WN, S, WB, A5, W5>), dim3(gm * gn * P), dim3(64 * WM * WN), 0, s,
+  hipLaunchKernelGGL((echo_gemm_fp8_fma_k<BM, BN, WM, WN, S, G, WB, A5, W5>), dim3(gm * gn * P), dim3(64 * WM * WN * G), 0, s,
                      a, gm, gn);
   return hipGetLastError();
 }
@@ -873,6 +919,10 @@ hipError_t thin(const GemmFp8Args& a, int P, hipStream_t s) {
 // P = 8, N = 1024, K = 4096: 10.3 with 2 tiles of 16 wavefronts, 12.5 with 1 of 16; one
 // token against N = K = 8192, where A costs nothing: 19.0 and 15.8.
 // Above that, tiles by the number b of 128 x 128 tiles over all ranks:
+//   no more 64 x 64 tiles than CUs and K over 1024: a K step of a lone workgroup is bound
+//     by its own chain of waits (0.5 us; more slabs changed nothing), so four groups of
+//     four wavefronts share k (M = 64, N = K = 8192: 19.9 against 23.8 with two groups and
+//     31.8 with one; M = 500, N = 640, K = 7552, fp32 output: 20.7, 23.9 and 31.9);
 //   b < 192: 64 rows, four wavefronts, 4 slabs (P = 4, M = 128, N = K = 4096: 21.9
 //     against 25.2 with 128 x 128 tiles);
 //   b < 384: 128 x 128, four wavefronts, 2 slabs, two workgroups per CU (M = 1024,
@@ -881,8 +931,9 @@ hipError_t thin(const GemmFp8Args& a, int P, hipStream_t s) {
 //     M = 2048, N = K = 4096: 130 against 168 with 128 x 128 tiles);
 //   else 256 x 128, 3 slabs (P = 2, M = 1024, N = K = 4096: 37.3 against 38.5 with
 //     128 x 128 and 76 with 64 x 64).
-// The same with fp32 scales, in tiles of 64 x 128 (23.3 against 28.3 at the first shape;
-// 43.4 against 47.4 and 80 at the last).
+// The same with fp32 scales, in tiles of 64 x 128 (23.3 against 28.3 at the second shape;
+// 43.4 against 47.4 and 80 at the last; two groups where k is shared, P = 4, M = 64,
+// N = K = 4096: 18.6 against 22.2).
 template <bool A5, bool W5, bool E8, bool WB>
 hipError_t launch(const GemmFp8Args& a, int P, hipStream_t s) {
   const int64_t columns = (a.N + 15) / 16 * P;  // 16 rows of W each
@@ -893,29 +944,37 @@ hipError_t launch(const GemmFp8Args& a, int P, hipStream_t s) {
   }
   if (a.M <= 32) return thin<2, 2, 2, 8, WB, A5, W5, E8>(a, P, s);
   const int64_t b = (a.M + 127) / 128 * ((a.N + 127) / 128) * P;
+  // tiles of 64 rows and `cols` columns no more than the CUs, and k long enough to share
+  const auto share_k = [&](int cols) {
+    return (a.M + 63) / 64 * ((a.N + cols - 1) / cols) * P <= 256 && a.K > 1024;
+  };
   const bool large = (a.M + 255) / 256 * ((a.N + 255) / 256) * P >= 192;
   if (a.out_elem == kElemF32) {
     if constexpr (E8) {
-      if (b < 192) return tile<64, 64, 2, 2, 4, kWideScaled, A5, W5, true>(a, P, s);
-      if (b < 384) return tile<128, 128, 2, 2, 2, kWideScaled, A5, W5, true>(a, P, s);
-      if (large) return tile<256, 256, 4, 2, 2, kWideScaled, A5, W5, true>(a, P, s);
-      return tile<256, 128, 4, 2, 3, kWideScaled, A5, W5, true>(a, P, s);
+      if (share_k(64)) return tile<64, 64, 2, 2, 2, 4, kWideScaled, A5, W5, true>(a, P, s);
+      if (b < 192) return tile<64, 64, 2, 2, 4, 1, kWideScaled, A5, W5, true>(a, P, s);
+      if (b < 384) return tile<128, 128, 2, 2, 2, 1, kWideScaled, A5, W5, true>(a, P, s);
+      if (large) return tile<256, 256, 4, 2, 2, 1, kWideScaled, A5, W5, true>(a, P, s);
+      return tile<256, 128, 4, 2, 3, 1, kWideScaled, A5, W5, true>(a, P, s);
     } else {
-      if (b < 192) return tile<64, 64, 2, 2, 4, kWide, A5, W5, false>(a, P, s);
-      if (b < 384) return tile<128, 128, 2, 2, 2, kWide, A5, W5, false>(a, P, s);
-      return tile<256, 128, 4, 2, 3, kWide, A5, W5, false>(a, P, s);
+      if (share_k(64)) return tile<64, 64, 2, 2, 2, 4, kWide, A5, W5, false>(a, P, s);
+      if (b < 192) return tile<64, 64, 2, 2, 4, 1, kWide, A5, W5, false>(a, P, s);
+      if (b < 384) return tile<128, 128, 2, 2, 2, 1, kWide, A5, W5, false>(a, P, s);
+      return tile<256, 128, 4, 2, 3, 1, kWide, A5, W5, false>(a, P, s);
     }
   }
   if constexpr (E8) {
-    if (b < 192) return tile<64, 64, 2, 2, 4, kScaled8, A5, W5, true>(a, P, s);
-    if (b < 384) return tile<128, 128, 2, 2, 2, kScaled8, A5, W5, true>(a, P, s);
-    if (large) return tile<256, 256, 4, 2, 2, kScaled8, A5, W5, true>(a, P, s);
-    return tile<256, 128, 4, 2, 3, kScaled8, A5, W5, true>(a, P, s);
+    if (share_k(64)) return tile<64, 64, 2, 2, 2, 4, kScaled8, A5, W5, true>(a, P, s);
+    if (b < 192) return tile<64, 64, 2, 2, 4, 1, kScaled8, A5, W5, true>(a, P, s);
+    if (b < 384) return tile<128, 128, 2, 2, 2, 1, kScaled8, A5, W5, true>(a, P, s);
+    if (large) return tile<256, 256, 4, 2, 2, 1, kScaled8, A5, W5, true>(a, P, s);
+    return tile<256, 128, 4, 2, 3, 1, kScaled8, A5, W5, true>(a, P, s);
   } else {
-    if (b < 192) return fma_tile<64, 128, 2, 2, 4, WB, A5, W5>(a, P, s);
-    if (b < 384) return fma_tile<128, 128, 2, 2, 2, WB, A5, W5>(a, P, s);
-    if (large) return fma_tile<256, 256, 4, 2, 2, WB, A5, W5>(a, P, s);
-    return fma_tile<256, 128, 4, 2, 3, WB, A5, W5>(a, P, s);
+    if (share_k(128)) return fma_tile<64, 128, 2, 2, 3, 2, WB, A5, W5>(a, P, s);
+    if (b < 192) return fma_tile<64, 128, 2, 2, 4, 1, WB, A5, W5>(a, P, s);
+    if (b < 384) return fma_tile<128, 128, 2, 2, 2, 1, WB, A5, W5>(a, P, s);
+    if (large) return fma_tile<256, 256, 4, 2, 2, 1, WB, A5, W5>(a, P, s);
+    return fma_tile<256, 128, 4, 2, 3, 1, WB, A5, W5>(a, P, s);
   }
 }
 
