@@ -27,6 +27,13 @@ finish the all-reduce; ``"bf16"`` runs the same product written out followed
 by a whole Echo call, which gives bit-identical results.  The same holds for
 ``f`` in the backward pass: the input-gradient products of the column-parallel
 layer run on libecho's kernel, on the backward state.
+
+With ``product="fp8"`` every product of the stack, forward, input gradients and
+weight gradients, runs in 8-bit floating point with a scale per 128 elements
+(e4m3 for activations and weights, e5m2 for gradients); the ranks' partials are
+bfloat16 and reduced by Echo as before, and weight gradients come in fp32.
+``dropout`` puts a dropout on each reduced output before it joins the residual
+stream, with a mask that both passes draw from a counter-based generator.
 """
 from __future__ import annotations
 
@@ -190,7 +197,91 @@ def _fns():
             dw = [a.t().contiguous() @ g for g in gpres]
             return (None, None, da) + tuple(dw)
 
-    return ReduceForward, ReduceBackward, RowParallelEcho, ColumnParallelEcho
+    def quantize(mats, fmt):
+        """Row blocks of fp32 or bf16 matrices [T, K], both ways: (as they are, transposed)."""
+        R, C = mats[0].shape
+        dev = mats[0].device
+        rows = [B.EchoFp8.empty(R, C, fmt, device=dev) for _ in mats]
+        cols = [B.EchoFp8.empty(C, R, fmt, device=dev) for _ in mats]
+        B.echo_quantize_fp8(mats, rows, cols)
+        return rows, cols
+
+    def products(A, W, dtype):
+        out = [torch.empty(A[0][0].shape[0], W[0][0].shape[0], dtype=dtype, device=A[0][0].device) for _ in A]
+        B.echo_gemm_fp8(A, W, out)
+        return out
+
+    class RowParallelFp8(torch.autograd.Function):
+        """g(h_r @ W2_r) in 8-bit products: forward sums bf16(q(h_r) q(W2_r)) over the
+        ranks through Echo; backward gives dh_r = q(g) q(W2_r)^T (bfloat16) and
+        dW2_r = q(h_r^T) q(g^T)^T (fp32).  q is the rounding to 8 bits, with blocks
+        along the dimension that is summed over; it passes gradients straight
+        through.  ``w8``: the weights both ways (TPMLPStack.quantize_weights)."""
+
+        @staticmethod
+        def forward(ctx, group: "EchoGroup", shape, w8, *hw):
+            P = group.P
+            hs, ws = hw[:P], hw[P:]
+            h8, h8t = quantize([h.detach() for h in hs], "e4m3")
+            ctx.P, ctx.w8, ctx.h8t = P, w8, h8t
+            ctx.h_dtype, ctx.w_dtype = hs[0].dtype, ws[0].dtype
+            parts = products(h8, w8[1], torch.bfloat16)
+            return group.allreduce([p.view(-1) for p in parts], B.ECHO_FWD).view(shape)
+
+        @staticmethod
+        def backward(ctx, grad):
+            g8, g8t = quantize([grad.contiguous()], "e5m2")
+            dh = products(g8 * ctx.P, ctx.w8[0], torch.bfloat16)
+            dw = products(ctx.h8t, g8t * ctx.P, torch.float32)
+            return (None, None, None) + tuple(d.to(ctx.h_dtype) for d in dh) + tuple(d.to(ctx.w_dtype) for d in dw)
+
+    class ColumnParallelFp8(torch.autograd.Function):
+        """f(a) @ W1_r in 8-bit products: forward gives every rank's pre-activation
+        q(a) q(W1_r) (bfloat16); backward gives dL/da through Echo on the backward
+        state as the sum of bf16(q(dpre_r) q(W1_r)^T), and dW1_r = q(a^T) q(dpre_r^T)^T
+        (fp32)."""
+
+        @staticmethod
+        def forward(ctx, group: "EchoGroup", w8, a, *w1s):
+            a8, a8t = quantize([a.detach().contiguous()], "e4m3")
+            ctx.group, ctx.w8, ctx.a8t = group, w8, a8t
+            ctx.shape, ctx.a_dtype, ctx.w_dtype = a.shape, a.dtype, w1s[0].dtype
+            return tuple(products(a8 * group.P, w8[1], torch.bfloat16))
+
+        @staticmethod
+        def backward(ctx, *gpres):
+            P = ctx.group.P
+            g8, g8t = quantize([g.contiguous() for g in gpres], "e5m2")
+            parts = products(g8, ctx.w8[0], torch.bfloat16)
+            da = ctx.group.allreduce([p.view(-1) for p in parts], B.ECHO_BWD).view(ctx.shape)
+            dw = products(ctx.a8t * P, g8t, torch.float32)
+            return (None, None, da.to(ctx.a_dtype)) + tuple(d.to(ctx.w_dtype) for d in dw)
+
+    class DropoutAdd(torch.autograd.Function):
+        """residual + dropout(x); backward draws the same mask again.  ``rng`` must still
+        hold the forward pass's values in the backward pass (autograd refuses a changed
+        one)."""
+
+        @staticmethod
+        def forward(ctx, x, residual, p: float, rng, offset: int, first: int):
+            ctx.save_for_backward(rng)
+            ctx.args, ctx.x_dtype = (p, offset, first), x.dtype
+            out = torch.empty_like(residual, memory_format=torch.contiguous_format)
+            return B.echo_dropout_add(x.contiguous(), out, p, rng, residual=residual.contiguous(), offset=offset,
+                                      first=first)
+
+        @staticmethod
+        def backward(ctx, grad):
+            (rng,) = ctx.saved_tensors
+            p, offset, first = ctx.args
+            grad = grad.contiguous()
+            dx = None
+            if ctx.needs_input_grad[0]:
+                dx = torch.empty_like(grad, dtype=ctx.x_dtype)
+                B.echo_dropout_add(grad, dx, p, rng, offset=offset, first=first)
+            return dx, grad if ctx.needs_input_grad[1] else None, None, None, None, None
+
+    return ReduceForward, ReduceBackward, RowParallelEcho, ColumnParallelEcho, RowParallelFp8, ColumnParallelFp8, DropoutAdd
 
 
 _FNS = None
@@ -211,6 +302,44 @@ def column_parallel_echo(group: "EchoGroup", a, ws, fused: bool):
     if _FNS is None:
         _FNS = _fns()
     return _FNS[3].apply(group, fused, a, *ws)
+
+
+def row_parallel_fp8(group: "EchoGroup", hs, ws, shape, w8):
+    """g(sum_r h_r @ W2_r) in 8-bit products (see RowParallelFp8)."""
+    global _FNS
+    if _FNS is None:
+        _FNS = _fns()
+    return _FNS[4].apply(group, shape, w8, *hs, *ws)
+
+
+def column_parallel_fp8(group: "EchoGroup", a, ws, w8):
+    """[a @ W1_r] in 8-bit products, the input gradient through Echo's backward state
+    (see ColumnParallelFp8)."""
+    global _FNS
+    if _FNS is None:
+        _FNS = _fns()
+    return _FNS[5].apply(group, w8, a, *ws)
+
+
+def dropout_add(x, residual, p: float, rng, offset: int = 0, first: int = 0):
+    """residual + dropout(x), differentiable in both; the mask is drawn from ``rng``
+    (int64 device tensor: key, step), ``offset`` and ``first`` in both passes
+    (see echo_dropout_add)."""
+    global _FNS
+    if _FNS is None:
+        _FNS = _fns()
+    return _FNS[6].apply(x, residual, p, rng, offset, first)
+
+
+def quantize_weights_fp8(ws):
+    """P weights [K_in, K_out] in e4m3 with a scale per 128 x 128 block: (as they are,
+    transposed), the operands of the input-gradient and of the forward products."""
+    R, C = ws[0].shape
+    dev = ws[0].device
+    rows = [B.EchoFp8.empty(R, C, block_rows=B.ECHO_FP8_BLOCK, device=dev) for _ in ws]
+    cols = [B.EchoFp8.empty(C, R, block_rows=B.ECHO_FP8_BLOCK, device=dev) for _ in ws]
+    B.echo_quantize_fp8([w.detach() for w in ws], rows, cols)
+    return rows, cols
 
 
 def reduce_forward(group: EchoGroup, partials, shape):
@@ -239,18 +368,26 @@ class TPMLPStack:
     bfloat16 on libecho's kernel, the row-parallel W2 product in the forward
     pass and the column-parallel W1 input-gradient product in the backward
     pass (written out, or with stage 1 in their epilogues; T a multiple of 64,
-    H of 128, F/P of 64)."""
+    H of 128, F/P of 64); "fp8": every product of both passes in 8-bit floating
+    point (any sizes).  ``dropout``: probability with which an element of a reduced
+    output is dropped before the residual add while ``training`` is set; the masks
+    come from ``rng`` (key ``seed``, step), layer l's from step + l, and train_step
+    moves the step on by the number of layers."""
 
     def __init__(self, layers: int, hidden: int, ffn: int, P: int, seed: int = 0, device=None,
-                 product: str = "f32"):
+                 product: str = "f32", dropout: float = 0.0):
         import torch
 
         if ffn % P:
             raise ValueError("ffn must be divisible by P")
-        if product not in ("f32", "bf16", "bf16_fused"):
+        if product not in ("f32", "bf16", "bf16_fused", "fp8"):
             raise ValueError(f"product {product!r}")
+        if not 0.0 <= dropout < 1.0:
+            raise ValueError(f"dropout {dropout!r}")
         self.L, self.H, self.F, self.P, self.product = layers, hidden, ffn, P, product
         dev = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
+        self.dropout, self.training = dropout, True
+        self.rng = torch.tensor([seed, 0], dtype=torch.int64, device=dev) if dropout > 0 else None
         g = torch.Generator(device=dev)
         g.manual_seed(seed)
         self.w1, self.w2 = [], []
@@ -265,23 +402,38 @@ class TPMLPStack:
     def parameters(self):
         return [w for layer in self.w1 + self.w2 for w in layer]
 
-    def forward(self, x, group: EchoGroup):
+    def quantize_weights(self):
+        """The weights of every layer in 8 bits, for ``forward(..., weights8=...)`` as long
+        as they do not change; without it a forward pass quantizes them itself."""
+        return [(quantize_weights_fp8(w1), quantize_weights_fp8(w2)) for w1, w2 in zip(self.w1, self.w2)]
+
+    def forward(self, x, group: EchoGroup, weights8=None):
         import torch
 
+        if weights8 is not None and self.product != "fp8":
+            raise ValueError("weights8 goes with product 'fp8'")
+        gelu = torch.nn.functional.gelu
         for l in range(self.L):
             a = x * torch.rsqrt(x.pow(2).mean(dim=-1, keepdim=True) + 1e-6)
-            if self.product == "f32":
+            if self.product == "fp8":
+                w8 = weights8[l] if weights8 is not None else (quantize_weights_fp8(self.w1[l]),
+                                                               quantize_weights_fp8(self.w2[l]))
+                pres = column_parallel_fp8(group, a, self.w1[l], w8[0])
+                # gelu in fp32 of the bfloat16 pre-activations
+                y = row_parallel_fp8(group, [gelu(p.float()) for p in pres], self.w2[l], x.shape, w8[1])
+            elif self.product == "f32":
                 xs = replicate(group, a)
-                hs = [torch.nn.functional.gelu(xs[r] @ self.w1[l][r]) for r in range(self.P)]
-            else:
-                pres = column_parallel_echo(group, a, self.w1[l], self.product == "bf16_fused")
-                hs = [torch.nn.functional.gelu(p) for p in pres]
-            if self.product == "f32":
+                hs = [gelu(xs[r] @ self.w1[l][r]) for r in range(self.P)]
                 partials = [(hs[r] @ self.w2[l][r]).to(torch.bfloat16) for r in range(self.P)]
                 y = reduce_forward(group, [p.reshape(-1) for p in partials], x.shape)
             else:
+                pres = column_parallel_echo(group, a, self.w1[l], self.product == "bf16_fused")
+                hs = [gelu(p) for p in pres]
                 y = row_parallel_echo(group, hs, self.w2[l], x.shape, self.product == "bf16_fused")
-            x = x + y
+            if self.dropout > 0 and self.training:
+                x = dropout_add(y, x, self.dropout, self.rng, offset=l)
+            else:
+                x = x + y
         return x
 
 
@@ -296,4 +448,6 @@ def train_step(model: TPMLPStack, group: EchoGroup, x0, target):
     y = model.forward(x, group)
     loss = torch.nn.functional.mse_loss(y, target)
     loss.backward()
+    if model.rng is not None and model.training:
+        model.rng[1] += model.L  # the next step draws other masks
     return loss.detach(), x.grad.detach(), [p.grad.detach() for p in model.parameters()]

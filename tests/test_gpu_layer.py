@@ -1,25 +1,13 @@
 """The 8-bit quantizer and product and the residual dropout on the GPU, against
 plain 64-bit references (fp8_helpers.py).
 
-Tolerances.  The quantizer and the dropout are compared bit for bit: the scaling by
-a power of two is exact and the generator is integer arithmetic.  A product's
-element is a sum of K exact products (8-bit mantissas), scaled: added in fp32 in any
-order, with at most one unit in the last place (2^-23) lost per addition and two per
-scaling and block, it is off by at most (K + 4 blocks) 2^-23 sum |a w|, and the
-rounding to the output type adds half a step of the value (finfo.eps / 2).
-
-Outputs of 16 bits come from the 8-bit matrix instruction where A has more than a few
-rows, and that instruction adds each run of 8 consecutive products in fixed point.  The
-run's unit is 2^-13 of the largest 2^(ea + ew) in it (ea, ew: the exponents of the two
-codes, at least the format's lowest), and every product is cut to a multiple of it,
-toward zero.  A product whose own 2^(ea + ew) is the largest has at most 6 fraction
-bits below it (3 + 3 for e4m3) and loses nothing; each of the other 7 loses less than
-one unit.  So a run is off by less than 7 * 2^-13 * max 2^(ea + ew), times the scales,
-and an element by the sum of that over its runs."""
+The quantizer and the dropout are compared bit for bit: the scaling by a power of two
+is exact and the generator is integer arithmetic.  The tolerance of the products is
+fp8_helpers.product_tolerance."""
 import numpy as np
 import pytest
 
-from fp8_helpers import dequantize, dropout_ref, keep_mask, quantize_ref, to_np64
+from fp8_helpers import dropout_ref, keep_mask, product_tolerance, quantize_ref, to_np64, values
 
 pytestmark = pytest.mark.gpu
 
@@ -161,34 +149,10 @@ def operand(E, cuda, seed, rows, k, fmt, scale, block, spread=0.7):
     return m
 
 
-def values(m, block):
-    return dequantize(to_np64(m[0]), to_np64(m[1]), block)
-
-
-def exponents(m, block):
-    """2^e of every code (the lowest normal exponent for subnormals and zero), scaled."""
-    torch = torch_()
-    low = -6 if m[0].dtype == torch.float8_e4m3fn else -14
-    c = np.abs(to_np64(m[0]))
-    e = np.maximum(np.frexp(c)[1] - 1, low)
-    return dequantize(np.where(c > 0, np.ldexp(1.0, e), 2.0 ** low), to_np64(m[1]), block)
-
-
 def assert_product(out, A, W, block_a=1, block_w=1, m=slice(None), n=slice(None)):
     """out (rows m, columns n of the result) against A W^T in 64 bits."""
-    torch = torch_()
-    a, w = values(A, block_a)[m], values(W, block_w)[n]
-    K = a.shape[1]
-    want = a @ w.T
-    tol = (K + 4 * (K // 128 + 1)) * 2.0 ** -23 * (np.abs(a) @ np.abs(w).T)
-    if out.dtype != torch.float32:
-        ea, ew = exponents(A, block_a)[m], exponents(W, block_w)[n]
-        for k in range(0, K, 8):
-            run = np.zeros_like(want)
-            for i in range(k, min(k + 8, K)):
-                np.maximum(run, np.outer(ea[:, i], ew[:, i]), out=run)
-            tol += 7 * 2.0 ** -13 * run
-    tol += torch.finfo(out.dtype).eps / 2 * (np.abs(want) + tol) + (6e-8 if out.dtype == torch.float16 else 0.0)
+    want = values(A, block_a)[m] @ values(W, block_w)[n].T
+    tol = product_tolerance(A, W, out.dtype, block_a, block_w, m, n)
     err = np.abs(to_np64(out) - want)
     assert (err <= tol).all(), f"off by up to {np.max(err / np.maximum(tol, 1e-300)):.3g} of the tolerance"
 
