@@ -387,10 +387,10 @@ struct Slabs {
     for (int u = 0; u < kPer; ++u) sreg[u] = scale_bits<E8>(sp[u] + b * sk[u], 0);
     sblock += G;
   }
-  __device__ __forceinline__ void stage_scales(int ring) {
+  __device__ __forceinline__ void stage_scales(int ring, const uint32_t* from) {
 #pragma unroll
     for (int u = 0; u < kPer; ++u)
-      scales(ring)[t + u * kThreads] = BYTES ? sreg[u] : __float_as_uint(scale_value<E8>(sreg[u]));
+      scales(ring)[t + u * kThreads] = BYTES ? from[u] : __float_as_uint(scale_value<E8>(from[u]));
   }
 
   // Zeros behind K in the last chunk of the last slab, on both sides (a NaN there
@@ -408,13 +408,16 @@ struct Slabs {
   // Step 0's scales staged, step 1's on their way, the loads of the first S steps out and
   // the first slab landed.
   __device__ __forceinline__ void start() {
+    uint32_t first[kPer];  // staged once everything is on its way
     load_scales();
-    stage_scales(0);
+#pragma unroll
+    for (int u = 0; u < kPer; ++u) first[u] = sreg[u];
     if (steps > 1) load_scales();
     for (int s = 0; s < S && s < steps; ++s) {
       if (s + 1 < steps) issue<false>(s, s);
       else issue<true>(s, s);
     }
+    stage_scales(0, first);
     if (steps >= S)
       __builtin_amdgcn_s_waitcnt(vmcnt_at_most_lds_drained((S - 1) * kLoads));
     else
@@ -431,7 +434,7 @@ struct Slabs {
   // for those waits for everything issued earlier.
   template <int ISSUE>
   __device__ __forceinline__ void wait_next(int it, int next, int ring1) {
-    stage_scales(ring1);
+    stage_scales(ring1, sreg);
     __builtin_amdgcn_s_waitcnt(vmcnt_at_most_lds_drained(ISSUE != 0 ? (S - 2) * kLoads : 0));
     __builtin_amdgcn_sched_barrier(0);
     slab_barrier();
