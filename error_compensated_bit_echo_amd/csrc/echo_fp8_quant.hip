@@ -16,10 +16,13 @@
 // chunks are swizzled by the column group and come back as 16-byte runs: X is read
 // once and every code is written once, in full 128-byte lines.  16-bit elements stay
 // packed: maxima two at a time on their magnitudes' bits, conversions two at a time
-// from the packed pair, three instructions per element for both orientations (in fp32
-// it took twelve, and 88 us against HBMTIME for 8192 x 8192 bfloat16 both ways).
-// Without the transpose, and with a scale per row, a unit of 16 lanes quantizes one
-// block of 128 elements on its own (rows of few tokens spread over all CUs).
+// from the packed pair, three instructions per element for both orientations.
+// Measured, 8192 x 8192 both ways: bfloat16 59 us (4.5 TB/s; 88 with every element in
+// fp32, at twelve instructions), fp32 80 us (5.0 TB/s); a large copy reaches 5.1 TB/s.
+// Without the transpose, with a scale per row and fewer than 512 tiles, a unit of 16
+// lanes quantizes one block of 128 elements on its own, so that few tokens spread over
+// all CUs (8 ranks of 64 x 1024: 4.9 us, which is the launch; with 512 tiles and more the
+// tile kernel is faster: 8 x 512 x 2048 7.1 against 7.8 us, 8192 x 8192 39.9 against 48.6).
 #pragma clang fp contract(off)
 
 #include <type_traits>
@@ -491,7 +494,7 @@ template <int X>
 hipError_t launch(const QuantFp8Args& a, int P, bool block128, hipStream_t s) {
   const int64_t nbc = (a.C + kFp8Block - 1) / kFp8Block, nbr = (a.R + kFp8Block - 1) / kFp8Block;
   const bool cols = a.cols.codes[0] != nullptr;
-  if (!cols && !block128) {
+  if (!cols && !block128 && P * nbc * nbr < 512) {
     const int64_t blocks = (a.R * nbc + kThreads / 16 - 1) / (kThreads / 16);
     const dim3 grid(static_cast<unsigned>(blocks < (1 << 20) ? blocks : (1 << 20)), static_cast<unsigned>(P));
     hipLaunchKernelGGL((echo_quant_rows_k<X>), grid, dim3(kThreads), 0, s, a);
@@ -502,6 +505,8 @@ hipError_t launch(const QuantFp8Args& a, int P, bool block128, hipStream_t s) {
     hipLaunchKernelGGL((echo_quant_tile_k<X, true, true>), grid, dim3(kThreads), 0, s, a);
   else if (cols)
     hipLaunchKernelGGL((echo_quant_tile_k<X, true, false>), grid, dim3(kThreads), 0, s, a);
+  else if (!block128)
+    hipLaunchKernelGGL((echo_quant_tile_k<X, false, false>), grid, dim3(kThreads), 0, s, a);
   else
     hipLaunchKernelGGL((echo_quant_tile_k<X, false, true>), grid, dim3(kThreads), 0, s, a);
   return hipGetLastError();

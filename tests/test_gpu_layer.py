@@ -87,6 +87,45 @@ def test_quantizer(E, cuda, R, C, dtype, want, block):
                 assert (raw(o[r].codes)[:, v.shape[1]:] == 0x5A).all(), "bytes behind the rows were written"
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("P,R,C", [(8, 1100, 1000), (1, 4096, 2048), (2, 33000, 130)])
+def test_quantizer_of_many_rows(E, cuda, dtype, P, R, C):
+    """Alone, the codes along the rows are those of the call that writes both orientations
+    (which the other tests check), whatever kernel the number of rows chooses."""
+    torch = torch_()
+    X = [torch.randn(R, C, device=cuda).to(dt(dtype)) for _ in range(P)]
+    X[0][R - 1, C - 1], X[0][5, 7] = float("inf"), float("nan")
+    alone = [E.EchoFp8.empty(R, C, "e5m2", "f32", 1, cuda) for _ in range(P)]
+    both = [E.EchoFp8.empty(R, C, "e5m2", "f32", 1, cuda) for _ in range(P)]
+    cols = [E.EchoFp8.empty(C, R, "e5m2", "f32", 1, cuda) for _ in range(P)]
+    E.echo_quantize_fp8(X, alone)
+    E.echo_quantize_fp8(X, both, cols)
+    for r in range(P):
+        assert torch.equal(alone[r].scales, both[r].scales)
+        assert torch.equal(alone[r].codes.view(torch.uint8), both[r].codes.view(torch.uint8))
+    rows = np.r_[0:3, 5, R - 2:R]
+    x = X[0][torch.from_numpy(rows).to(cuda)]
+    sub = (alone[0].codes[torch.from_numpy(rows).to(cuda)], alone[0].scales[torch.from_numpy(rows).to(cuda)])
+    assert_quantized(sub, to_np64(x), "e5m2", 1)
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "e5m2"])
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_quantizer_of_every_16_bit_value(E, cuda, fmt, dtype):
+    """All bit patterns, each in a block whose scale another element sets."""
+    torch = torch_()
+    bits = torch.arange(65536, dtype=torch.int32).to(torch.int16).view(dt(dtype))
+    x = torch.empty(1024, 128, dtype=dt(dtype))
+    x[:, :64] = bits.view(1024, 64)
+    x[:, 64:] = bits.view(1024, 64)[torch.randperm(1024, generator=torch.Generator().manual_seed(1))]
+    x[::3, 64:] = 0  # and where nothing else does
+    rows, cols = E.EchoFp8.empty(1024, 128, fmt, "e8m0", 1, cuda), E.EchoFp8.empty(128, 1024, fmt, "e8m0", 1, cuda)
+    E.echo_quantize_fp8([x.to(cuda)], [rows], [cols])
+    v = to_np64(x)
+    assert_quantized(rows, v, fmt, 1)
+    assert_quantized(cols, v.T, fmt, 1)
+
+
 @pytest.mark.parametrize("fmt", ["e4m3", "e5m2"])
 @pytest.mark.parametrize("block", [1, 128])
 def test_quantizer_special_values(E, cuda, fmt, block):
