@@ -496,6 +496,7 @@ def echo_dropout_add(x, out, p: float, rng, residual=None, offset: int = 0, firs
     step); ``offset`` is added to the step (which of a step's dropouts this is);
     ``first``: index of the first element in the whole message, for a rank that
     holds a part of it.  out may be x or the residual itself."""
+    first, offset = int(first), int(offset)
     if not 0 <= first < 1 << 63:
         raise EchoError(ECHO_ERR_ARG, f"first {first}")
     offset = (offset + (1 << 63)) % (1 << 64) - (1 << 63)  # the step wraps at 64 bits

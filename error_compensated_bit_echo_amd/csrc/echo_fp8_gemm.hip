@@ -246,6 +246,16 @@ __global__ __launch_bounds__(64 * NW) void echo_gemm_fp8_thin_k(const GemmFp8Arg
   }
 }
 
+// The product over nothing: zeros.
+__global__ __launch_bounds__(256) void echo_gemm_fp8_zero_k(const GemmFp8Args a) {
+  const RankPtrs p = rank_ptrs(blockIdx.z);
+  for (int64_t m = blockIdx.y; m < a.M; m += gridDim.y)
+    for (int64_t n = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; n < a.N; n += static_cast<int64_t>(gridDim.x) * 256) {
+      if (a.out_elem == kElemF32) store1<kElemF32>(p.out, m * a.ldo + n, 0.0f);
+      else store1<kElemBf16>(p.out, m * a.ldo + n, 0.0f);  // the same bits in fp16
+    }
+}
+
 // ---- tiles through LDS -----------------------------------------------------------
 //
 // A workgroup of WM x WN wavefronts computes a BM x BN tile, each wavefront BM / WM
@@ -940,7 +950,7 @@ hipError_t thin(const GemmFp8Args& a, int P, hipStream_t s) {
 template <bool A5, bool W5, bool E8, bool WB>
 hipError_t launch(const GemmFp8Args& a, int P, hipStream_t s) {
   const int64_t columns = (a.N + 15) / 16 * P;  // 16 rows of W each
-  if (a.M <= 16 || a.K == 0) {
+  if (a.M <= 16) {
     if (columns >= 1024) return thin<1, 4, 1, 8, WB, A5, W5, E8>(a, P, s);
     if (columns >= 512 && a.M > 4) return thin<1, 2, 1, 16, WB, A5, W5, E8>(a, P, s);
     return thin<1, 1, 2, 16, WB, A5, W5, E8>(a, P, s);
@@ -990,6 +1000,12 @@ hipError_t launch_formats(const GemmFp8Args& a, int P, bool e8m0, hipStream_t s)
 }  // namespace
 
 hipError_t launch_gemm_fp8(const GemmFp8Args& a, int P, bool a_e5m2, bool w_e5m2, bool e8m0, hipStream_t s) {
+  if (a.K == 0) {
+    const dim3 grid(static_cast<unsigned>((a.N + 255) / 256 < 64 ? (a.N + 255) / 256 : 64),
+                    static_cast<unsigned>(a.M < 4096 ? a.M : 4096), static_cast<unsigned>(P));
+    hipLaunchKernelGGL(echo_gemm_fp8_zero_k, grid, dim3(256), 0, s, a);
+    return hipGetLastError();
+  }
   if (a_e5m2) return w_e5m2 ? launch_formats<true, true>(a, P, e8m0, s) : launch_formats<true, false>(a, P, e8m0, s);
   return w_e5m2 ? launch_formats<false, true>(a, P, e8m0, s) : launch_formats<false, false>(a, P, e8m0, s);
 }

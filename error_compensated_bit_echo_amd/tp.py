@@ -197,6 +197,8 @@ def _fns():
             dw = [a.t().contiguous() @ g for g in gpres]
             return (None, None, da) + tuple(dw)
 
+    once = torch.autograd.function.once_differentiable
+
     def quantize(mats, fmt):
         """Row blocks of fp32 or bf16 matrices [T, K], both ways: (as they are, transposed)."""
         R, C = mats[0].shape
@@ -222,18 +224,23 @@ def _fns():
         def forward(ctx, group: "EchoGroup", shape, w8, *hw):
             P = group.P
             hs, ws = hw[:P], hw[P:]
-            h8, h8t = quantize([h.detach() for h in hs], "e4m3")
+            h8, h8t = quantize([h.detach().contiguous() for h in hs], "e4m3")
             ctx.P, ctx.w8, ctx.h8t = P, w8, h8t
             ctx.h_dtype, ctx.w_dtype = hs[0].dtype, ws[0].dtype
             parts = products(h8, w8[1], torch.bfloat16)
             return group.allreduce([p.view(-1) for p in parts], B.ECHO_FWD).view(shape)
 
         @staticmethod
+        @once
         def backward(ctx, grad):
+            P = ctx.P
             g8, g8t = quantize([grad.contiguous()], "e5m2")
-            dh = products(g8 * ctx.P, ctx.w8[0], torch.bfloat16)
-            dw = products(ctx.h8t, g8t * ctx.P, torch.float32)
-            return (None, None, None) + tuple(d.to(ctx.h_dtype) for d in dh) + tuple(d.to(ctx.w_dtype) for d in dw)
+            dh = dw = (None,) * P
+            if any(ctx.needs_input_grad[3:3 + P]):
+                dh = tuple(d.to(ctx.h_dtype) for d in products(g8 * P, ctx.w8[0], torch.bfloat16))
+            if any(ctx.needs_input_grad[3 + P:]):
+                dw = tuple(d.to(ctx.w_dtype) for d in products(ctx.h8t, g8t * P, torch.float32))
+            return (None, None, None) + dh + dw
 
     class ColumnParallelFp8(torch.autograd.Function):
         """f(a) @ W1_r in 8-bit products: forward gives every rank's pre-activation
@@ -249,13 +256,17 @@ def _fns():
             return tuple(products(a8 * group.P, w8[1], torch.bfloat16))
 
         @staticmethod
+        @once
         def backward(ctx, *gpres):
             P = ctx.group.P
             g8, g8t = quantize([g.contiguous() for g in gpres], "e5m2")
-            parts = products(g8, ctx.w8[0], torch.bfloat16)
-            da = ctx.group.allreduce([p.view(-1) for p in parts], B.ECHO_BWD).view(ctx.shape)
-            dw = products(ctx.a8t * P, g8t, torch.float32)
-            return (None, None, da.to(ctx.a_dtype)) + tuple(d.to(ctx.w_dtype) for d in dw)
+            da, dw = None, (None,) * P
+            if ctx.needs_input_grad[2]:
+                parts = products(g8, ctx.w8[0], torch.bfloat16)
+                da = ctx.group.allreduce([p.view(-1) for p in parts], B.ECHO_BWD).view(ctx.shape).to(ctx.a_dtype)
+            if any(ctx.needs_input_grad[3:]):
+                dw = tuple(d.to(ctx.w_dtype) for d in products(ctx.a8t * P, g8t, torch.float32))
+            return (None, None, da) + dw
 
     class DropoutAdd(torch.autograd.Function):
         """residual + dropout(x); backward draws the same mask again.  ``rng`` must still
@@ -271,6 +282,7 @@ def _fns():
                                       first=first)
 
         @staticmethod
+        @once
         def backward(ctx, grad):
             (rng,) = ctx.saved_tensors
             p, offset, first = ctx.args

@@ -364,12 +364,17 @@ echo_status echo_quantize_fp8(const void* const* X, int32_t P, int64_t rows, int
  * out_r = A_r W_r^T for every rank: A_r [M, K] and W_r [N, K] as echo_fp8 (each
  * of either format and either block_rows, both of the same scale type), out_r
  * [M, N] of out_dtype (fp32, bfloat16 or fp16) with ldo elements between rows,
- * any alignment of the element type.  Products of a block of 128 are added in
- * fp32 on the matrix cores, the blocks' sums, scaled, in fp32; the result is
- * rounded once, to out_dtype.  Scales of any strides of 0 or more.  With the
- * three operands of a linear layer quantized both ways this covers the forward
- * product, the input gradient and the weight gradient.  Deterministic; a row's
- * result does not depend on what other rows hold, NaN and infinities included.
+ * any alignment of the element type.  Sums are held in fp32 and rounded once, to
+ * out_dtype.  fp32 outputs: the products of a block of 128 are added in fp32.
+ * 16-bit outputs of more than 32 rows: by the 8-bit matrix instruction, which adds
+ * each run of 8 consecutive products in fixed point with a unit of 2^-13 of the
+ * largest (an error of 1.5e-5 of the result for normal data), then in fp32.
+ * Where out_dtype is fp32, or M at most 32, and scales are exponent bytes, a code
+ * times its scale has to be a normal bfloat16 (2^-126 to 2^128): a smaller one may
+ * count as zero, a larger one is infinite.  Scales of any strides of 0 or more.
+ * With the operands of a linear layer quantized both ways this covers the forward
+ * product, the input gradient and the weight gradient.  Deterministic; an element
+ * does not depend on what other rows of A and W hold, NaN and infinities included.
  * M, N, K: at most 2^22 each, P * ceil(M / 128) * ceil(N / 128) below 2^21.
  * Errors: ECHO_ERR_ARG (null or misaligned pointer, scale types that differ, bad enum, an output overlapping another
  * output or an input), ECHO_ERR_SHAPE, ECHO_ERR_DTYPE, ECHO_ERR_HIP. */

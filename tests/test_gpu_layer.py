@@ -225,7 +225,7 @@ def test_product(E, cuda, M, N, K, scale, block):
 SWEEP = [(m, n, k, p) for m, n, k, p in (
     (48, 1024, 896, 8), (96, 640, 512, 4), (160, 512, 2176, 1), (192, 768, 320, 2), (384, 1024, 256, 4),
     (640, 896, 384, 1), (768, 1280, 768, 2), (1024, 1024, 200, 1), (1280, 2048, 1152, 1), (2048, 2304, 272, 1),
-    (2300, 2100, 400, 1), (32, 8192, 640, 1), (4, 256, 8192, 2), (8, 16, 4096, 1))]
+    (2300, 2100, 400, 1), (4001, 3003, 333, 1), (2000, 3001, 208, 1), (1023, 1100, 140, 8), (32, 8192, 640, 1), (4, 256, 8192, 2), (8, 16, 4096, 1))]
 
 
 @pytest.mark.parametrize("M,N,K,P", SWEEP)
@@ -263,17 +263,20 @@ def test_product_block_rows_on_both_sides_and_broadcast_scales(E, cuda):
 def test_product_over_nothing_gives_zeros(E, cuda):
     torch = torch_()
     A, W = E.EchoFp8.empty(5, 0, device=cuda), E.EchoFp8.empty(7, 0, device=cuda)
-    out = torch.full((5, 7), 3.0, device=cuda)
-    E.echo_gemm_fp8([A], [W], [out])
-    assert (out == 0).all()
+    for dtype in (torch.float32, torch.bfloat16, torch.float16):
+        out = torch.full((5, 9), 3.0, device=cuda, dtype=dtype)
+        E.echo_gemm_fp8([A], [W], [out[:, :7]])
+        assert (out[:, :7] == 0).all() and (out[:, 7:] == 3).all()
 
 
-@pytest.mark.parametrize("M,N,K", [(4, 64, 300), (70, 140, 300), (300, 300, 300)])
+@pytest.mark.parametrize("M,N,K", [(4, 64, 300), (70, 140, 300), (130, 300, 1500), (2000, 3000, 300), (4000, 3000, 300)])
 @pytest.mark.parametrize("scale", ["e8m0", "f32"])
-def test_nan_stays_in_its_row_and_column(E, cuda, M, N, K, scale):
+@pytest.mark.parametrize("out_dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("block", [1, 128])
+def test_nan_stays_in_its_row_and_column(E, cuda, M, N, K, scale, out_dtype, block):
     torch = torch_()
-    A, W = operand(E, cuda, 1, M, K, "e4m3", scale, 1), operand(E, cuda, 2, N, K, "e4m3", scale, 1)
-    clean = torch.empty(M, N, device=cuda)
+    A, W = operand(E, cuda, 1, M, K, "e4m3", scale, 1), operand(E, cuda, 2, N, K, "e4m3", scale, block)
+    clean = torch.empty(M, N, device=cuda, dtype=dt(out_dtype))
     E.echo_gemm_fp8([A], [W], [clean])
     A.codes.view(torch.uint8)[1, 299] = 0x7F
     W.codes.view(torch.uint8)[3, 0] = 0xFF
@@ -281,7 +284,7 @@ def test_nan_stays_in_its_row_and_column(E, cuda, M, N, K, scale):
         A.scales[2, 1] = float("inf")
     else:
         A.scales.view(torch.uint8)[2, 1] = 0xFF
-    out = torch.empty(M, N, device=cuda)
+    out = torch.empty_like(clean)
     E.echo_gemm_fp8([A], [W], [out])
     hit = torch.zeros(M, N, dtype=torch.bool, device=cuda)
     hit[1:3], hit[:, 3] = True, True
