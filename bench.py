@@ -395,8 +395,8 @@ def tp_report(torch, dev) -> dict:
     hidden 4096, ffn 16384): one training step (forward + backward, 8 Echo calls
     per direction) with Echo, Echo without compensation and exact all-reduces
     (fp32 products), and with Echo and the row-parallel products in bfloat16 on
-    libecho's kernel, written out or with stage 1 fused into them; errors of the
-    loss and the gradients against the exact fp32 step, and step times (median
+    libecho's kernel, written out or with stage 1 fused into them, or with every
+    product in 8-bit floating point; errors of the loss and the gradients against the exact fp32 step, and step times (median
     of three steps after a warm-up step)."""
     from error_compensated_bit_echo_amd import tp
 
@@ -433,8 +433,9 @@ def tp_report(torch, dev) -> dict:
         res[name], ms[name] = timed(model, tp.EchoGroup(P, T * H, mode="echo", device=dev, **kw))
 
     # the row-parallel product in bfloat16 on libecho's kernel, written out then
-    # reduced, or with stage 1 in its epilogue (bit-identical results)
-    for prod in ("bf16", "bf16_fused"):
+    # reduced, or with stage 1 in its epilogue (bit-identical results); every product
+    # in 8-bit floating point
+    for prod in ("bf16", "bf16_fused", "fp8"):
         m2 = tp.TPMLPStack(L, H, F, P, seed=21, device=dev, product=prod)
         res["echo_" + prod], ms["echo_" + prod] = timed(m2, tp.EchoGroup(P, T * H, mode="echo", device=dev))
         if prod == "bf16_fused":  # the fused product with sender feedback and bf16 state
@@ -448,7 +449,7 @@ def tp_report(torch, dev) -> dict:
 
     errs = {}
     for mode in ("echo", "echo_off", *variants, "echo_bf16", "echo_bf16_fused",
-                 "echo_bf16_fused_sender_feedback_bf16_state"):
+                 "echo_bf16_fused_sender_feedback_bf16_state", "echo_fp8"):
         loss, dx, dw = res[mode]
         errs[mode] = {"loss_rel_err": abs(float(loss - res["exact"][0])) / float(res["exact"][0]),
                       "dx0_rel_err": rel(dx, res["exact"][1]),
