@@ -7,10 +7,16 @@
 // key rng[0] give the chunk's eight 16-bit draws, and e is kept iff its draw is
 // at least the threshold.  A thread owns the part of one chunk that lies in one
 // row: eight elements share one generator call, which costs 20 32 x 32 -> 64-bit
-// products and 40 exclusive ors, five 32-bit operations per element.  (With
-// 32-bit draws, four elements a call, the arithmetic rather than memory would
-// bound the bfloat16 forms.)  Nothing is stored but the output, and the result
-// does not depend on how the elements are split over threads.
+// products and 40 exclusive ors, five 32-bit operations per element.  Nothing is
+// stored but the output, and the result does not depend on how the elements are
+// split over threads.
+//
+// Bound by the memory: 16384 x 8192 bfloat16 with a residual takes 140 us, 5.75
+// TB/s of what it has to move (a plain elementwise copy reaches 6.2 on this card);
+// non-temporal loads or stores change nothing there.  Rows of odd lengths: 4095 x
+// 4097 bfloat16 without a residual takes 13.4 us (5.0 TB/s) with the chunks of all
+// rows numbered through, 16.1 us with rows as blocks of the grid's second axis,
+// where the last workgroup of every row is mostly idle.
 #pragma clang fp contract(off)
 
 #include "echo_elem.h"
@@ -47,60 +53,85 @@ __device__ __forceinline__ bool kept(const Draws& d, int lane, uint32_t threshol
   return ((lane & 1) ? w >> 16 : w & 0xFFFFu) >= threshold;
 }
 
-// Rows are blocks of blockIdx.y (and every gridDim.y rows after), chunks of a row
-// are threads of the x dimension (and every grid width after).
+// The part of chunk q0 + q that lies in row `row`.
 template <int X, int O, bool RES>
-__global__ __launch_bounds__(kThreads) void echo_dropout_k(const DropoutArgs a) {
-  const uint64_t key = static_cast<uint64_t>(a.rng[0]);
-  const uint64_t step = static_cast<uint64_t>(a.rng[1]) + static_cast<uint64_t>(a.offset);
-  for (int64_t row = blockIdx.y; row < a.R; row += gridDim.y) {
-    const int64_t e0 = a.first + row * a.C;        // index of the row's first element
-    const int64_t q0 = e0 >> 3;                    // its chunk
-    const int64_t nq = ((e0 + a.C + 7) >> 3) - q0;  // chunks the row touches
-    const int64_t ox = row * a.ldx, orr = row * a.ldr, oo = row * a.ldo;
-    for (int64_t q = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; q < nq;
-         q += static_cast<int64_t>(gridDim.x) * kThreads) {
-      const int64_t j = ((q0 + q) << 3) - e0;  // column of the chunk's first element (may lie before the row)
-      const Draws d = philox10(static_cast<uint64_t>(q0 + q), step, key);
-      if (j >= 0 && j + 8 <= a.C) {
-        float v[8];
-        load8<X>(a.x, ox + j, v);
-        float r[8];
-        if constexpr (RES) load8<O>(a.residual, orr + j, r);
+__device__ __forceinline__ void dropout_chunk(const DropoutArgs& a, uint64_t key, uint64_t step, int64_t row, int64_t q) {
+  const int64_t e0 = a.first + row * a.C;  // index of the row's first element
+  const int64_t chunk = (e0 >> 3) + q;
+  const int64_t j = (chunk << 3) - e0;  // column of the chunk's first element (may lie before the row)
+  if (j >= a.C) return;
+  const int64_t ox = row * a.ldx, orr = row * a.ldr, oo = row * a.ldo;
+  const Draws d = philox10(static_cast<uint64_t>(chunk), step, key);
+  if (j >= 0 && j + 8 <= a.C) {
+    float v[8];
+    load8<X>(a.x, ox + j, v);
+    float r[8];
+    if constexpr (RES) load8<O>(a.residual, orr + j, r);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          v[i] = kept(d, i, a.threshold) ? v[i] * a.scale : 0.0f;
-          if constexpr (RES) v[i] = v[i] + r[i];
-        }
-        store8<O>(a.out, oo + j, v);
-      } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-          if (j + i >= 0 && j + i < a.C) {
-            float y = kept(d, i, a.threshold) ? load1<X>(a.x, ox + j + i) * a.scale : 0.0f;
-            if constexpr (RES) y = y + load1<O>(a.residual, orr + j + i);
-            store1<O>(a.out, oo + j + i, y);
-          }
-      }
+    for (int i = 0; i < 8; ++i) {
+      v[i] = kept(d, i, a.threshold) ? v[i] * a.scale : 0.0f;
+      if constexpr (RES) v[i] = v[i] + r[i];
     }
+    store8<O>(a.out, oo + j, v);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (j + i >= 0 && j + i < a.C) {
+        float y = kept(d, i, a.threshold) ? load1<X>(a.x, ox + j + i) * a.scale : 0.0f;
+        if constexpr (RES) y = y + load1<O>(a.residual, orr + j + i);
+        store1<O>(a.out, oo + j + i, y);
+      }
   }
 }
 
-template <int X, int O>
-hipError_t launch(const DropoutArgs& a, dim3 grid, hipStream_t s) {
-  if (a.residual != nullptr)
-    hipLaunchKernelGGL((echo_dropout_k<X, O, true>), grid, dim3(kThreads), 0, s, a);
-  else
-    hipLaunchKernelGGL((echo_dropout_k<X, O, false>), grid, dim3(kThreads), 0, s, a);
+// A thread a chunk of a row, `per_row` chunks to a row.  FLAT: all rows' chunks are
+// numbered through (their number fits 32 bits), so that rows of any length fill the
+// workgroups; otherwise rows are blocks of blockIdx.y and every gridDim.y rows after.
+template <int X, int O, bool RES, bool FLAT>
+__global__ __launch_bounds__(kThreads) void echo_dropout_k(const DropoutArgs a, int64_t per_row) {
+  const uint64_t key = static_cast<uint64_t>(a.rng[0]);
+  const uint64_t step = static_cast<uint64_t>(a.rng[1]) + static_cast<uint64_t>(a.offset);
+  if constexpr (FLAT) {
+    const uint32_t n = static_cast<uint32_t>(per_row), id = blockIdx.x * kThreads + threadIdx.x;
+    const uint32_t row = id / n;
+    if (row < a.R) dropout_chunk<X, O, RES>(a, key, step, row, id - row * n);
+  } else {
+    for (int64_t row = blockIdx.y; row < a.R; row += gridDim.y)
+      for (int64_t q = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; q < per_row;
+           q += static_cast<int64_t>(gridDim.x) * kThreads)
+        dropout_chunk<X, O, RES>(a, key, step, row, q);
+  }
+}
+
+template <int X, int O, bool RES>
+hipError_t launch_as(const DropoutArgs& a, hipStream_t s) {
+  // a row of C touches at most (C + 7) / 8 + 1 chunks, one less where all start at a chunk's start
+  const bool whole = a.first % 8 == 0 && (a.R == 1 || a.C % 8 == 0);
+  const int64_t per_row = (a.C + 7) / 8 + (whole ? 0 : 1);
+  const int64_t blocks = (per_row + kThreads - 1) / kThreads;
+  if (a.R > 1 && a.R <= ((int64_t{1} << 32) - kThreads) / per_row) {
+    const int64_t all = (a.R * per_row + kThreads - 1) / kThreads;
+    hipLaunchKernelGGL((echo_dropout_k<X, O, RES, true>), dim3(static_cast<unsigned>(all)), dim3(kThreads), 0, s, a,
+                       per_row);
+  } else {
+    const dim3 grid(static_cast<unsigned>(blocks < (1 << 20) ? blocks : (1 << 20)),
+                    static_cast<unsigned>(a.R < 65535 ? a.R : 65535));
+    hipLaunchKernelGGL((echo_dropout_k<X, O, RES, false>), grid, dim3(kThreads), 0, s, a, per_row);
+  }
   return hipGetLastError();
 }
 
+template <int X, int O>
+hipError_t launch(const DropoutArgs& a, hipStream_t s) {
+  return a.residual != nullptr ? launch_as<X, O, true>(a, s) : launch_as<X, O, false>(a, s);
+}
+
 template <int X>
-hipError_t launch_x(const DropoutArgs& a, Elem out, dim3 grid, hipStream_t s) {
+hipError_t launch_x(const DropoutArgs& a, Elem out, hipStream_t s) {
   switch (out) {
-    case kElemF32: return launch<X, kElemF32>(a, grid, s);
-    case kElemBf16: return launch<X, kElemBf16>(a, grid, s);
-    default: return launch<X, kElemF16>(a, grid, s);
+    case kElemF32: return launch<X, kElemF32>(a, s);
+    case kElemBf16: return launch<X, kElemBf16>(a, s);
+    default: return launch<X, kElemF16>(a, s);
   }
 }
 
@@ -114,13 +145,10 @@ hipError_t launch_dropout(const DropoutArgs& given, Elem x, Elem out, hipStream_
     a.C *= a.R;
     a.R = 1;
   }
-  const int64_t per_row = (a.C / 8 + 2 + kThreads - 1) / kThreads;  // a row of C touches at most C/8 + 2 chunks
-  const dim3 grid(static_cast<unsigned>(per_row < (1 << 20) ? per_row : (1 << 20)),
-                  static_cast<unsigned>(a.R < 65535 ? a.R : 65535));
   switch (x) {
-    case kElemF32: return launch_x<kElemF32>(a, out, grid, s);
-    case kElemBf16: return launch_x<kElemBf16>(a, out, grid, s);
-    default: return launch_x<kElemF16>(a, out, grid, s);
+    case kElemF32: return launch_x<kElemF32>(a, out, s);
+    case kElemBf16: return launch_x<kElemBf16>(a, out, s);
+    default: return launch_x<kElemF16>(a, out, s);
   }
 }
 

@@ -437,3 +437,48 @@ def test_captured_calls_follow_their_inputs(E, cuda):
         assert torch.equal(bufs[2], eager[2]) and torch.equal(bufs[0].codes.view(torch.uint8), eager[0].codes.view(torch.uint8))
         seen.append(bufs[2].clone())
     assert not torch.equal(seen[0], seen[1])
+
+
+# ---- beyond 32-bit offsets -----------------------------------------------------------
+
+
+def test_quantizer_and_product_beyond_4_gib(E, cuda):
+    """Matrices of more than 2^32 elements: the last rows agree with those of a small call."""
+    torch = torch_()
+    R, C, N = (1 << 20) + 130, 4224, 48
+    X = torch.empty(R, C, dtype=torch.bfloat16, device=cuda).normal_()
+    rows, cols = E.EchoFp8.empty(R, C, device=cuda), E.EchoFp8.empty(C, R, device=cuda)
+    E.echo_quantize_fp8([X], [rows], [cols])
+    at = R - 258  # a multiple of 128: blocks along the columns start where the whole matrix's do
+    tail = X[at:].contiguous()
+    r, c = E.EchoFp8.empty(258, C, device=cuda), E.EchoFp8.empty(C, 258, device=cuda)
+    E.echo_quantize_fp8([tail], [r], [c])
+    assert at % 128 == 0
+    assert torch.equal(rows.codes[at:].view(torch.uint8), r.codes.view(torch.uint8))
+    assert torch.equal(cols.codes[:, at:].view(torch.uint8), c.codes.view(torch.uint8))
+    assert torch.equal(rows.scales[at:].contiguous().view(torch.uint8), r.scales.contiguous().view(torch.uint8))
+    del X, cols
+    W = operand(E, cuda, 1, N, C, "e4m3", "e8m0", 128)
+    out, small = torch.empty(R, N, dtype=torch.bfloat16, device=cuda), torch.empty(258, N, dtype=torch.bfloat16, device=cuda)
+    E.echo_gemm_fp8([rows], [W], [out])
+    E.echo_gemm_fp8([r], [W], [small])
+    assert_product(small, r, W, 1, 128)
+    assert_product(out[at:], r, W, 1, 128)
+
+
+def test_dropout_beyond_4_gib(E, cuda):
+    torch = torch_()
+    whole = torch.empty((1 << 32) + 72, dtype=torch.bfloat16, device=cuda)
+    with pytest.raises(E.EchoError):  # more columns than a row may have; as eight rows it is in range
+        E.echo_dropout_add(whole, whole, 0.5, rng_tensor(cuda))
+    wide = torch.empty((1 << 20) + 3, 4104, dtype=torch.bfloat16, device=cuda)
+    for x in (whole.view(8, -1), wide[:, :4099]):
+        x.fill_(1.0)
+        R, C = x.shape
+        E.echo_dropout_add(x, x, 0.5, rng_tensor(cuda))
+        tail = torch.ones(min(C, 4099), dtype=torch.bfloat16, device=cuda)
+        want = torch.empty_like(tail)
+        at = R * C - tail.numel()  # of the last row's end
+        E.echo_dropout_add(tail, want, 0.5, rng_tensor(cuda), first=at)
+        assert torch.equal(x[-1, C - tail.numel():], want)
+        assert np.array_equal(f32(want) != 0, keep_mask(at, tail.numel(), STEP, KEY, 0.5))
