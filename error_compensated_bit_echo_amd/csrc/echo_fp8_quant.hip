@@ -17,8 +17,12 @@
 // once and every code is written once, in full 128-byte lines.  16-bit elements stay
 // packed: maxima two at a time on their magnitudes' bits, conversions two at a time
 // from the packed pair, three instructions per element for both orientations.
-// Measured, 8192 x 8192 both ways: bfloat16 59 us (4.5 TB/s; 88 with every element in
-// fp32, at twelve instructions), fp32 80 us (5.0 TB/s); a large copy reaches 5.1 TB/s.
+// Measured, 8192 x 8192 both ways: bfloat16 55 us (4.9 TB/s; with every element in fp32,
+// at twelve instructions, the kernel took half as long again), fp32 75 us (5.35 TB/s).  The
+// memory bounds it: of a copy that writes every line once this card does 5.1 (the
+// library's) to 6.2 TB/s, and the order in which tiles are taken moves the time by up to
+// 15 % (down the columns 68 us; contiguous runs of tiles per XCD 66; one tile after the
+// other 59; side by side in pairs on an XCD, as here, 57, and 55 past the caches).
 // Without the transpose, with a scale per row and fewer than 512 tiles, a unit of 16
 // lanes quantizes one block of 128 elements on its own, so that few tokens spread over
 // all CUs (8 ranks of 64 x 1024: 4.9 us, which is the launch; with 512 tiles and more the
@@ -34,6 +38,7 @@ namespace {
 
 constexpr int kThreads = 256;
 
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
 typedef int16_t i16x2 __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
@@ -428,7 +433,9 @@ __device__ __forceinline__ void quant_tile(const QuantFp8Args& a, const TileOf& 
       if constexpr (!B128) sb = scale_byte(P::to_f32(row16_max(row_max[i])), e5m2);
       if (cg == i) mine = sb;
       const uint2 w = v.row_codes(i, scale_of(sb), e5m2);
-      if (INSIDE || (row0 + i < a.R && left > 0)) store_codes8(qr + (row0 + i) * a.rows.ld + col0, w, left);
+      uint8_t* const p = qr + (row0 + i) * a.rows.ld + col0;
+      if (INSIDE && a.stream) __builtin_nontemporal_store(__builtin_bit_cast(u32x2, w), reinterpret_cast<u32x2*>(p));
+      else if (INSIDE || (row0 + i < a.R && left > 0)) store_codes8(p, w, left);
     }
     if (!B128 && cg < 8 && (INSIDE || row0 + cg < a.R)) store_scale(sr, (row0 + cg) * a.rows.srs + bc * a.rows.sks, mine, e8m0);
   }
@@ -482,7 +489,10 @@ __global__ __launch_bounds__(kThreads) void echo_quant_tile_k(const QuantFp8Args
   __shared__ __attribute__((aligned(16))) uint32_t part[4][16 * Part<X, 8>::kColWords];  // per wavefront: maxima
   const int64_t nbc = (a.C + kFp8Block - 1) / kFp8Block, nbr = (a.R + kFp8Block - 1) / kFp8Block;
   const uint32_t per = static_cast<uint32_t>(nbc * nbr);
-  const uint32_t r = blockIdx.x / per, at = blockIdx.x - r * per;
+  // The hardware hands workgroups to the eight XCDs in turn: of every 16, an XCD gets two
+  // tiles that lie side by side, so that one L2 holds 256 bytes of a row's codes.
+  const uint32_t i = blockIdx.x, id = (i | 15) < gridDim.x ? (i & ~15u) + 2 * (i & 7) + ((i >> 3) & 1) : i;
+  const uint32_t r = id / per, at = id - r * per;
   const int64_t br = at / static_cast<uint32_t>(nbc), bc = at - br * nbc;
   const auto* k = kernel_args<QuantFp8Args>();
   const TileOf o{k->X[r], k->rows.codes[r], k->cols.codes[r], k->rows.scales[r], k->cols.scales[r], br, bc};
@@ -490,17 +500,29 @@ __global__ __launch_bounds__(kThreads) void echo_quant_tile_k(const QuantFp8Args
   else quant_tile<X, COLS, B128, false>(a, o, tile, part);
 }
 
+// A call that reads and writes more than the 256 MB last-level cache leaves nothing useful
+// in it: the codes along the rows, in pieces of 128 bytes, then go past the caches.
+// With the products that read them next, us: 8192 x 8192 bfloat16 both ways 54.7 against
+// 56.4 (169 against 174 with both products), 16384 x 16384 215 against 219 (447 against
+// 456); in a smaller call the product would miss them: 2048 x 4096 9.8 against 10.9, but
+// 50.1 against 45.8 with one product.  (The codes along the columns: slower from 16384 x
+// 16384 on, 243 against 219.)
+constexpr int64_t kCache = int64_t{1} << 28;
+
 template <int X>
-hipError_t launch(const QuantFp8Args& a, int P, bool block128, hipStream_t s) {
-  const int64_t nbc = (a.C + kFp8Block - 1) / kFp8Block, nbr = (a.R + kFp8Block - 1) / kFp8Block;
-  const bool cols = a.cols.codes[0] != nullptr;
+hipError_t launch(const QuantFp8Args& given, int P, bool block128, hipStream_t s) {
+  const int64_t nbc = (given.C + kFp8Block - 1) / kFp8Block, nbr = (given.R + kFp8Block - 1) / kFp8Block;
+  const bool cols = given.cols.codes[0] != nullptr;
   if (!cols && !block128 && P * nbc * nbr < 512) {
-    const int64_t blocks = (a.R * nbc + kThreads / 16 - 1) / (kThreads / 16);
+    const int64_t blocks = (given.R * nbc + kThreads / 16 - 1) / (kThreads / 16);
     const dim3 grid(static_cast<unsigned>(blocks < (1 << 20) ? blocks : (1 << 20)), static_cast<unsigned>(P));
-    hipLaunchKernelGGL((echo_quant_rows_k<X>), grid, dim3(kThreads), 0, s, a);
+    hipLaunchKernelGGL((echo_quant_rows_k<X>), grid, dim3(kThreads), 0, s, given);
     return hipGetLastError();
   }
   const dim3 grid(static_cast<unsigned>(P * nbc * nbr));
+  QuantFp8Args a = given;
+  const int64_t per = (X == kElemF32 ? 4 : 2) + (a.rows.codes[0] != nullptr) + cols;
+  a.stream = P * a.R * a.C * per >= kCache;
   if (cols && block128)
     hipLaunchKernelGGL((echo_quant_tile_k<X, true, true>), grid, dim3(kThreads), 0, s, a);
   else if (cols)

@@ -27,6 +27,7 @@ struct QuantFp8Args {
   int64_t R, C, ldx;  // rows, columns, elements between rows
   Fp8Out rows, cols;  // codes[0] == nullptr: not wanted
   int32_t e5m2, e8m0;
+  int32_t stream;  // set by the launcher: the codes along the rows go past the caches
 };
 // block128: one scale per 128 x 128 block instead of per row and 128 elements
 hipError_t launch_quantize_fp8(const QuantFp8Args& a, int P, Elem x, bool block128, hipStream_t s);
