@@ -466,6 +466,28 @@ def test_quantizer_and_product_beyond_4_gib(E, cuda):
     assert_product(out[at:], r, W, 1, 128)
 
 
+@pytest.mark.parametrize("dtype,block,C", [("f32", 1, 8192), ("f32", 128, 8200), ("f16", 1, 8184), ("bf16", 128, 8192)])
+def test_quantizer_of_more_than_the_last_level_cache(E, cuda, dtype, block, C):
+    """A call of more than 256 MB stores past the caches: each part of its rows agrees
+    with a small call's."""
+    torch = torch_()
+    R, n = 8192 + 70, 1536
+    X = torch.empty(R, C, dtype=getattr(torch, {"f32": "float32", "f16": "float16", "bf16": "bfloat16"}[dtype]),
+                    device=cuda).normal_()
+    def run(x):
+        rows = E.EchoFp8.empty(x.shape[0], C, block_rows=block, device=cuda)
+        cols = E.EchoFp8.empty(C, x.shape[0], block_rows=block, device=cuda)
+        E.echo_quantize_fp8([x], [rows], [cols])
+        return [t.view(torch.uint8) for t in (rows.codes, cols.codes, rows.scales.contiguous(), cols.scales.contiguous())]
+    whole = run(X)
+    for at in range(0, R, n):
+        end = min(R, at + n)
+        part = run(X[at:end])
+        s0, s1 = (at, end) if block == 1 else (at // 128, -(-end // 128))
+        assert torch.equal(whole[0][at:end], part[0]) and torch.equal(whole[1][:, at:end], part[1])
+        assert torch.equal(whole[2][s0:s1], part[2]) and torch.equal(whole[3][:, at // 128:-(-end // 128)], part[3])
+
+
 def test_dropout_beyond_4_gib(E, cuda):
     torch = torch_()
     whole = torch.empty((1 << 32) + 72, dtype=torch.bfloat16, device=cuda)
