@@ -939,22 +939,32 @@ hipError_t thin(const GemmFp8Args& a, int P, hipStream_t s) {
 // 9.9 with 4 tiles per workgroup of 8 wavefronts, 12.2 with 2 of 16, 15.3 with 1 of 8;
 // P = 8, N = 1024, K = 4096: 10.3 with 2 tiles of 16 wavefronts, 12.5 with 1 of 16; one
 // token against N = K = 8192, where A costs nothing: 19.0 and 15.8.
-// Above that, tiles by the number b of 128 x 128 tiles over all ranks:
-//   no more 64 x 64 tiles than CUs and K over 1024: a K step of a lone workgroup is bound
-//     by its own chain of waits (0.5 us; more slabs changed nothing), so four groups of
-//     four wavefronts share k (M = 64, N = K = 8192: 19.9 against 23.8 with two groups and
+// Above that, tiles by the number t of 64 x 64 tiles over all ranks and b of 128 x 128
+// ones; us for bfloat16 outputs with exponent bytes, then fp32 outputs:
+//   t <= 256, the CUs, and K over 1024: a K step of a lone workgroup is bound by its own
+//     chain of waits (0.5 us; more slabs changed nothing), so four groups of four
+//     wavefronts share k (M = 64, N = K = 8192: 19.9 against 23.8 with two groups and
 //     31.8 with one; M = 500, N = 640, K = 7552, fp32 output: 20.7, 23.9 and 31.9);
-//   b < 192: 64 rows, four wavefronts, 4 slabs (P = 4, M = 128, N = K = 4096: 21.9
-//     against 25.2 with 128 x 128 tiles);
-//   b < 384: 128 x 128, four wavefronts, 2 slabs, two workgroups per CU (M = 1024,
-//     N = K = 4096: 25.4 against 30.6 with 256 x 128 tiles and 40.2 with 64 x 64);
+//   t <= 512: two groups, two workgroups per CU (P = 4, M = 128, N = K = 4096: 18.7, 26.5
+//     against 22.2, 28.9 with one and 24.1 with four; P = 8, M = 64: 26.4, 30.7 against
+//     34, 46 with 128 x 128 tiles; P = 4, M = 128, N = 4096, K = 512: 5.9 against 6.2);
+//   b < 192, or M <= 64, where more rows would multiply zeros: 64 x 128, 2 slabs (M = 600,
+//     N = K = 4096: 22.4, 32.9 against 23.2, 34.4 with 128 x 128 tiles and 26.5, 32.9 with
+//     two groups; P = 16, M = 64, N = 4096, K = 1024: 13.5, 16.2 against 15.1, 19.4 and
+//     16.2, 19.9);
+//   b < 384, or M <= 128: 128 x 128, four wavefronts, 2 slabs, two workgroups per CU
+//     (M = 1024, N = K = 4096: 25.4 against 30.6 with 256 x 128 tiles and 40.2 with 64 x 64;
+//     M = 128, N = 65536, K = 4096: 70.2, 77.9 against 74.7, 99.9 with 256 x 256 and 87, 96
+//     with 64 x 128);
 //   256 x 256 where those number at least 192, three quarters of the CUs (P = 4,
 //     M = 2048, N = K = 4096: 130 against 168 with 128 x 128 tiles);
 //   else 256 x 128, 3 slabs (P = 2, M = 1024, N = K = 4096: 37.3 against 38.5 with
 //     128 x 128 and 76 with 64 x 64).
-// The same with fp32 scales, in tiles of 64 x 128 (23.3 against 28.3 at the second shape;
-// 43.4 against 47.4 and 80 at the last; two groups where k is shared, P = 4, M = 64,
-// N = K = 4096: 18.6 against 22.2).
+// The same with fp32 scales and 16-bit outputs, where tiles have 128 columns at least and
+// two groups are the most that fits LDS (P = 4, M = 64, N = K = 4096: 18.6 against 22.2
+// with one; M = 600, N = K = 4096 26.5 with 64 x 128 tiles against 29.3 with 128 x 128).
+// fp32 scales and fp32 outputs take 256 x 128 tiles at most: a block's sum has
+// accumulators of its own.
 template <bool A5, bool W5, bool E8, bool WB>
 hipError_t launch(const GemmFp8Args& a, int P, hipStream_t s) {
   const int64_t columns = (a.N + 15) / 16 * P;  // 16 rows of W each
@@ -965,35 +975,31 @@ hipError_t launch(const GemmFp8Args& a, int P, hipStream_t s) {
   }
   if (a.M <= 32) return thin<2, 2, 2, 8, WB, A5, W5, E8>(a, P, s);
   const int64_t b = (a.M + 127) / 128 * ((a.N + 127) / 128) * P;
-  // tiles of 64 rows and `cols` columns no more than the CUs, and k long enough to share
-  const auto share_k = [&](int cols) {
-    return (a.M + 63) / 64 * ((a.N + cols - 1) / cols) * P <= 256 && a.K > 1024;
-  };
+  const int64_t t = (a.M + 63) / 64 * ((a.N + 63) / 64) * P;
+  const bool four = t <= 256 && a.K > 1024, two = t <= 512, low = b < 192 || a.M <= 64, medium = b < 384 || a.M <= 128;
   const bool large = (a.M + 255) / 256 * ((a.N + 255) / 256) * P >= 192;
   if (a.out_elem == kElemF32) {
+    constexpr TileMode MODE = E8 ? kWideScaled : kWide;
+    if (four) return tile<64, 64, 2, 2, 2, 4, MODE, A5, W5, E8>(a, P, s);
+    if (two) return tile<64, 64, 2, 2, 2, 2, MODE, A5, W5, E8>(a, P, s);
+    if (low) return tile<64, 128, 2, 2, 2, 1, MODE, A5, W5, E8>(a, P, s);
+    if (medium) return tile<128, 128, 2, 2, 2, 1, MODE, A5, W5, E8>(a, P, s);
     if constexpr (E8) {
-      if (share_k(64)) return tile<64, 64, 2, 2, 2, 4, kWideScaled, A5, W5, true>(a, P, s);
-      if (b < 192) return tile<64, 64, 2, 2, 4, 1, kWideScaled, A5, W5, true>(a, P, s);
-      if (b < 384) return tile<128, 128, 2, 2, 2, 1, kWideScaled, A5, W5, true>(a, P, s);
-      if (large) return tile<256, 256, 4, 2, 2, 1, kWideScaled, A5, W5, true>(a, P, s);
-      return tile<256, 128, 4, 2, 3, 1, kWideScaled, A5, W5, true>(a, P, s);
-    } else {
-      if (share_k(64)) return tile<64, 64, 2, 2, 2, 4, kWide, A5, W5, false>(a, P, s);
-      if (b < 192) return tile<64, 64, 2, 2, 4, 1, kWide, A5, W5, false>(a, P, s);
-      if (b < 384) return tile<128, 128, 2, 2, 2, 1, kWide, A5, W5, false>(a, P, s);
-      return tile<256, 128, 4, 2, 3, 1, kWide, A5, W5, false>(a, P, s);
+      if (large) return tile<256, 256, 4, 2, 2, 1, MODE, A5, W5, E8>(a, P, s);
     }
+    return tile<256, 128, 4, 2, 3, 1, MODE, A5, W5, E8>(a, P, s);
   }
   if constexpr (E8) {
-    if (share_k(64)) return tile<64, 64, 2, 2, 2, 4, kScaled8, A5, W5, true>(a, P, s);
-    if (b < 192) return tile<64, 64, 2, 2, 4, 1, kScaled8, A5, W5, true>(a, P, s);
-    if (b < 384) return tile<128, 128, 2, 2, 2, 1, kScaled8, A5, W5, true>(a, P, s);
+    if (four) return tile<64, 64, 2, 2, 2, 4, kScaled8, A5, W5, true>(a, P, s);
+    if (two) return tile<64, 64, 2, 2, 2, 2, kScaled8, A5, W5, true>(a, P, s);
+    if (low) return tile<64, 128, 2, 2, 2, 1, kScaled8, A5, W5, true>(a, P, s);
+    if (medium) return tile<128, 128, 2, 2, 2, 1, kScaled8, A5, W5, true>(a, P, s);
     if (large) return tile<256, 256, 4, 2, 2, 1, kScaled8, A5, W5, true>(a, P, s);
     return tile<256, 128, 4, 2, 3, 1, kScaled8, A5, W5, true>(a, P, s);
   } else {
-    if (share_k(128)) return fma_tile<64, 128, 2, 2, 3, 2, WB, A5, W5>(a, P, s);
-    if (b < 192) return fma_tile<64, 128, 2, 2, 4, 1, WB, A5, W5>(a, P, s);
-    if (b < 384) return fma_tile<128, 128, 2, 2, 2, 1, WB, A5, W5>(a, P, s);
+    if (two) return fma_tile<64, 128, 2, 2, 3, 2, WB, A5, W5>(a, P, s);
+    if (low) return fma_tile<64, 128, 2, 2, 2, 1, WB, A5, W5>(a, P, s);
+    if (medium) return fma_tile<128, 128, 2, 2, 2, 1, WB, A5, W5>(a, P, s);
     if (large) return fma_tile<256, 256, 4, 2, 2, 1, WB, A5, W5>(a, P, s);
     return fma_tile<256, 128, 4, 2, 3, 1, WB, A5, W5>(a, P, s);
   }

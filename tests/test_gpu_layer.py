@@ -247,6 +247,44 @@ def test_product_sizes(E, cuda, M, N, K, P, scale, block, out_dtype):
         assert_product(sub, A[r], W[r], 1, block, m, n)
 
 
+# (M, N, K, P) of few rows for all the columns: two groups that share k, low tiles, and
+# tiles of 128 rows at the most, each at its edges
+FEW_ROWS = [(60, 4090, 130, 8), (128, 2048, 1408, 4), (420, 4100, 260, 1), (65, 1000, 127, 16), (50, 2080, 260, 16),
+            (64, 33000, 144, 1), (600, 4100, 300, 1), (100, 4160, 384, 16), (128, 33000, 130, 2), (300, 520, 1500, 2)]
+
+
+@pytest.mark.parametrize("M,N,K,P", FEW_ROWS)
+@pytest.mark.parametrize("scale,block", [("e8m0", 128), ("f32", 1), ("f32", 128)])
+@pytest.mark.parametrize("out_dtype", ["f32", "bf16"])
+def test_product_of_few_rows(E, cuda, M, N, K, P, scale, block, out_dtype):
+    test_product_sizes(E, cuda, M, N, K, P, scale, block, out_dtype)
+
+
+@pytest.mark.parametrize("M,N,P", [(50, 2080, 16), (600, 4100, 1), (100, 4160, 16), (128, 2048, 4)])
+@pytest.mark.parametrize("scale,out_dtype,block", [("e8m0", "f32", 1), ("e8m0", "bf16", 128), ("f32", "f32", 1),
+                                                   ("f32", "bf16", 128), ("f32", "bf16", 1)])
+def test_nan_of_few_rows_stays_in_its_row_and_column(E, cuda, M, N, P, scale, out_dtype, block):
+    """NaN codes of a row of A and a column of W, behind K and in the last block too."""
+    torch = torch_()
+    K = 300
+    A = [operand(E, cuda, 10 + r, M, K, "e4m3", scale, 1) for r in range(P)]
+    W = [operand(E, cuda, 50 + r, N, K, "e4m3", scale, block) for r in range(P)]
+    out = [torch.zeros(M, N, dtype=dt(out_dtype), device=cuda) for _ in range(P)]
+    for m in A + W:  # what lies behind K in the rows' padding
+        whole = m.codes.as_strided((m.codes.shape[0], 304), (304, 1)).view(torch.uint8)
+        whole[:, K:] = 0x7F
+    A[0].codes.view(torch.uint8)[M // 2, 299] = 0x7F
+    W[P - 1].codes.view(torch.uint8)[N - 1, 7] = 0x7F
+    E.echo_gemm_fp8(A, W, out)
+    for r in range(P):
+        want = torch.zeros(M, N, dtype=torch.bool, device=cuda)
+        if r == 0:
+            want[M // 2] = True
+        if r == P - 1:
+            want[:, N - 1] = True
+        assert torch.equal(out[r].isnan(), want)
+
+
 def test_product_block_rows_on_both_sides_and_broadcast_scales(E, cuda):
     torch = torch_()
     M, N, K = 200, 150, 300
