@@ -948,10 +948,12 @@ hipError_t thin(const GemmFp8Args& a, int P, hipStream_t s) {
 //   t <= 512: two groups, two workgroups per CU (P = 4, M = 128, N = K = 4096: 18.7, 26.5
 //     against 22.2, 28.9 with one and 24.1 with four; P = 8, M = 64: 26.4, 30.7 against
 //     34, 46 with 128 x 128 tiles; P = 4, M = 128, N = 4096, K = 512: 5.9 against 6.2);
-//   b < 192, or M <= 64, where more rows would multiply zeros: 64 x 128, 2 slabs (M = 600,
-//     N = K = 4096: 22.4, 32.9 against 23.2, 34.4 with 128 x 128 tiles and 26.5, 32.9 with
-//     two groups; P = 16, M = 64, N = 4096, K = 1024: 13.5, 16.2 against 15.1, 19.4 and
-//     16.2, 19.9);
+//   b <= 256, M over 64 and K over 1024: 128 x 128, two groups (M = 1024, N = K = 4096:
+//     23.3, 40.1 against 26.0, 40.8 with one; M = 600: 20.9, 32.0 against 24.3, 35.4 with
+//     64 x 128 tiles; at K = 1024 one group is faster, 9.3 against 10.1);
+//   b < 192, or M <= 64, where more rows would multiply zeros: 64 x 128, 2 slabs (P = 16,
+//     M = 64, N = 4096, K = 1024: 13.5, 16.2 against 15.1, 19.4 with 128 x 128 tiles and
+//     16.2, 19.9 with 64 x 64 ones in two groups);
 //   b < 384, or M <= 128: 128 x 128, four wavefronts, 2 slabs, two workgroups per CU
 //     (M = 1024, N = K = 4096: 25.4 against 30.6 with 256 x 128 tiles and 40.2 with 64 x 64;
 //     M = 128, N = 65536, K = 4096: 70.2, 77.9 against 74.7, 99.9 with 256 x 256 and 87, 96
@@ -962,7 +964,7 @@ hipError_t thin(const GemmFp8Args& a, int P, hipStream_t s) {
 //     128 x 128 and 76 with 64 x 64).
 // The same with fp32 scales and 16-bit outputs, where tiles have 128 columns at least and
 // two groups are the most that fits LDS (P = 4, M = 64, N = K = 4096: 18.6 against 22.2
-// with one; M = 600, N = K = 4096 26.5 with 64 x 128 tiles against 29.3 with 128 x 128).
+// with one; M = 1024, N = K = 4096 27.5 with two groups against 33.8).
 // fp32 scales and fp32 outputs take 256 x 128 tiles at most: a block's sum has
 // accumulators of its own.
 template <bool A5, bool W5, bool E8, bool WB>
@@ -977,11 +979,13 @@ hipError_t launch(const GemmFp8Args& a, int P, hipStream_t s) {
   const int64_t b = (a.M + 127) / 128 * ((a.N + 127) / 128) * P;
   const int64_t t = (a.M + 63) / 64 * ((a.N + 63) / 64) * P;
   const bool four = t <= 256 && a.K > 1024, two = t <= 512, low = b < 192 || a.M <= 64, medium = b < 384 || a.M <= 128;
+  const bool pair = b <= 256 && a.M > 64 && a.K > 1024;
   const bool large = (a.M + 255) / 256 * ((a.N + 255) / 256) * P >= 192;
   if (a.out_elem == kElemF32) {
     constexpr TileMode MODE = E8 ? kWideScaled : kWide;
     if (four) return tile<64, 64, 2, 2, 2, 4, MODE, A5, W5, E8>(a, P, s);
     if (two) return tile<64, 64, 2, 2, 2, 2, MODE, A5, W5, E8>(a, P, s);
+    if (pair) return tile<128, 128, 2, 2, 2, 2, MODE, A5, W5, E8>(a, P, s);
     if (low) return tile<64, 128, 2, 2, 2, 1, MODE, A5, W5, E8>(a, P, s);
     if (medium) return tile<128, 128, 2, 2, 2, 1, MODE, A5, W5, E8>(a, P, s);
     if constexpr (E8) {
@@ -992,12 +996,14 @@ hipError_t launch(const GemmFp8Args& a, int P, hipStream_t s) {
   if constexpr (E8) {
     if (four) return tile<64, 64, 2, 2, 2, 4, kScaled8, A5, W5, true>(a, P, s);
     if (two) return tile<64, 64, 2, 2, 2, 2, kScaled8, A5, W5, true>(a, P, s);
+    if (pair) return tile<128, 128, 2, 2, 2, 2, kScaled8, A5, W5, true>(a, P, s);
     if (low) return tile<64, 128, 2, 2, 2, 1, kScaled8, A5, W5, true>(a, P, s);
     if (medium) return tile<128, 128, 2, 2, 2, 1, kScaled8, A5, W5, true>(a, P, s);
     if (large) return tile<256, 256, 4, 2, 2, 1, kScaled8, A5, W5, true>(a, P, s);
     return tile<256, 128, 4, 2, 3, 1, kScaled8, A5, W5, true>(a, P, s);
   } else {
     if (two) return fma_tile<64, 128, 2, 2, 3, 2, WB, A5, W5>(a, P, s);
+    if (pair) return fma_tile<128, 128, 2, 2, 2, 2, WB, A5, W5>(a, P, s);
     if (low) return fma_tile<64, 128, 2, 2, 2, 1, WB, A5, W5>(a, P, s);
     if (medium) return fma_tile<128, 128, 2, 2, 2, 1, WB, A5, W5>(a, P, s);
     if (large) return fma_tile<256, 256, 4, 2, 2, 1, WB, A5, W5>(a, P, s);

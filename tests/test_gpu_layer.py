@@ -260,6 +260,17 @@ def test_product_of_few_rows(E, cuda, M, N, K, P, scale, block, out_dtype):
     test_product_sizes(E, cuda, M, N, K, P, scale, block, out_dtype)
 
 
+# tiles of 128 rows and columns, two groups that share k
+PAIRS = [(600, 4100, 1300, 1), (200, 1100, 1171, 8), (128, 4090, 1090, 8), (1024, 4096, 1152, 1), (130, 2600, 1411, 4)]
+
+
+@pytest.mark.parametrize("M,N,K,P", PAIRS)
+@pytest.mark.parametrize("scale,block", [("e8m0", 128), ("f32", 1), ("f32", 128)])
+@pytest.mark.parametrize("out_dtype", ["f32", "bf16"])
+def test_product_of_a_tile_per_cu(E, cuda, M, N, K, P, scale, block, out_dtype):
+    test_product_sizes(E, cuda, M, N, K, P, scale, block, out_dtype)
+
+
 @pytest.mark.parametrize("M,N,P", [(50, 2080, 16), (600, 4100, 1), (100, 4160, 16), (128, 2048, 4)])
 @pytest.mark.parametrize("scale,out_dtype,block", [("e8m0", "f32", 1), ("e8m0", "bf16", 128), ("f32", "f32", 1),
                                                    ("f32", "bf16", 128), ("f32", "bf16", 1)])
