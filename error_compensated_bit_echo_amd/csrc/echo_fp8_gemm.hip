@@ -398,15 +398,18 @@ struct Slabs {
   }
 
   __device__ __forceinline__ void load_scales() {  // the next K step's
-    const int b = G == 1 || sblock < blocks ? sblock : blocks - 1;  // past the last block any scale does
+    const int b = G == 1 || sblock < blocks ? sblock : blocks - 1;  // past the last block: not used
 #pragma unroll
     for (int u = 0; u < kPer; ++u) sreg[u] = scale_bits<E8>(sp[u] + b * sk[u], 0);
     sblock += G;
   }
-  __device__ __forceinline__ void stage_scales(int ring, const uint32_t* from) {
+  // The scales of step `it`.  Past the last block they are zeros too: the products there
+  // are, and an infinite scale would make NaN of them.
+  __device__ __forceinline__ void stage_scales(int ring, int it, const uint32_t* from) {
+    const bool past = G > 1 && it * G + group >= blocks;
 #pragma unroll
     for (int u = 0; u < kPer; ++u)
-      scales(ring)[t + u * kThreads] = BYTES ? from[u] : __float_as_uint(scale_value<E8>(from[u]));
+      scales(ring)[t + u * kThreads] = past ? 0u : BYTES ? from[u] : __float_as_uint(scale_value<E8>(from[u]));
   }
 
   // Zeros behind K in the last chunk of the last slab, on both sides (a NaN there
@@ -433,7 +436,7 @@ struct Slabs {
       if (s + 1 < steps) issue<false>(s, s);
       else issue<true>(s, s);
     }
-    stage_scales(0, first);
+    stage_scales(0, 0, first);
     if (steps >= S)
       __builtin_amdgcn_s_waitcnt(vmcnt_at_most_lds_drained((S - 1) * kLoads));
     else
@@ -450,7 +453,7 @@ struct Slabs {
   // for those waits for everything issued earlier.
   template <int ISSUE>
   __device__ __forceinline__ void wait_next(int it, int next, int ring1) {
-    stage_scales(ring1, sreg);
+    stage_scales(ring1, it + 1, sreg);
     __builtin_amdgcn_s_waitcnt(vmcnt_at_most_lds_drained(ISSUE != 0 ? (S - 2) * kLoads : 0));
     __builtin_amdgcn_sched_barrier(0);
     slab_barrier();
