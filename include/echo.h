@@ -371,7 +371,11 @@ echo_status echo_quantize_fp8(const void* const* X, int32_t P, int64_t rows, int
  * largest (an error of 1.5e-5 of the result for normal data), then in fp32.
  * Where out_dtype is fp32, or M at most 32, and scales are exponent bytes, a code
  * times its scale has to be a normal bfloat16 (2^-126 to 2^128): a smaller one may
- * count as zero, a larger one is infinite.  Scales of any strides of 0 or more.
+ * count as zero, a larger one is infinite.  fp32 scales of a block are multiplied in
+ * fp32 before its sum is: their product has to be zero or a normal number (2^-126 to
+ * 2^128); a smaller one loses bits or counts as zero, a larger one is infinite, as an
+ * infinite scale is: the block then gives an infinity of the sign of its sum, or NaN
+ * where that is 0.  Scales of any strides of 0 or more.
  * With the operands of a linear layer quantized both ways this covers the forward
  * product, the input gradient and the weight gradient.  Deterministic; an element
  * does not depend on what other rows of A and W hold, NaN and infinities included.

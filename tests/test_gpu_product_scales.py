@@ -57,3 +57,58 @@ def test_infinite_fp32_scales(E, cuda, tiling, out, block, last):
         assert torch.equal(got[r].sign()[want.isinf()].double(), want.sign()[want.isinf()])
         assert torch.equal(got[r][finite], want[finite].to(OUT[out]))
         assert bool(want.isinf().any()) and bool(finite.any())
+
+
+def pinned(cuda, seed, rows, k, values, exponent, scale, fmt="e4m3"):
+    """Random codes out of `values` under one scale 2^exponent."""
+    import torch
+    from product_cases import codes_of
+    g = generator(cuda, seed)
+    v = torch.tensor(values, device=cuda)[torch.randint(len(values), (rows, k), generator=g, device=cuda)]
+    kb = -(-k // 128)
+    if scale == "e8m0":
+        s = torch.full((kb, rows), exponent + 127, dtype=torch.uint8, device=cuda).view(torch.float8_e8m0fnu)
+    else:
+        s = torch.full((kb, rows), 2.0 ** exponent, device=cuda)
+    return codes_of(v, fmt), s.t()
+
+
+def assert_ends(E, cuda, tiling, scale, out, low, high, fmt="e4m3"):
+    """Codes `low[0]` under 2^low[1] against codes `high[0]` under 2^high[1], on either side."""
+    import torch
+    from product_cases import exact
+    M, N, K, P = TILINGS[tiling]
+    for swap in (False, True):
+        (va, ea), (vw, ew) = (high, low) if swap else (low, high)
+        A = [pinned(cuda, 2 * r, M, K, va, ea, scale, fmt) for r in range(P)]
+        W = [pinned(cuda, 2 * r + 1, N, K, vw, ew, scale) for r in range(P)]
+        got = [torch.full((M, N), 7.0, dtype=OUT[out], device=cuda) for _ in range(P)]
+        E.echo_gemm_fp8(A, W, got)
+        for r in range(P):
+            assert torch.equal(got[r], exact(A[r], W[r]).to(OUT[out])), (tiling, swap)
+
+
+WHOLE = [-4.0, -3.0, -1.0, 0.0, 1.0, 2.0, 4.0]
+
+
+@pytest.mark.parametrize("tiling", TILINGS)
+@pytest.mark.parametrize("out", ["f32", "bf16"])
+@pytest.mark.parametrize("fmt", ["e4m3", "e5m2"])
+def test_exponent_scales_at_the_ends_of_their_range(E, cuda, tiling, out, fmt):
+    """Where a code times its scale is a normal bfloat16 the result is that of the definition:
+    exponent byte 0 (2^-127) under codes of at least 2, exponent byte 254 (2^127) under codes
+    below 2."""
+    assert_ends(E, cuda, tiling, "e8m0", out, ([-4.0, -2.0, 0.0, 2.0, 3.0], -127), (WHOLE, 100), fmt)
+    assert_ends(E, cuda, tiling, "e8m0", out, (WHOLE, -100), ([-1.5, -1.0, 0.0, 1.0], 127), fmt)
+
+
+@pytest.mark.parametrize("tiling", TILINGS)
+@pytest.mark.parametrize("out", ["f32", "bf16"])
+def test_fp32_scales_at_the_ends_of_their_range(E, cuda, tiling, out):
+    """Where the product of two scales is a normal fp32 number the result is that of the
+    definition: products of 2^-126 and, over sums that cancel or stay small, 2^104."""
+    assert_ends(E, cuda, tiling, "f32", out, (WHOLE, -126), (WHOLE, 0))
+    assert_ends(E, cuda, tiling, "f32", out, (WHOLE, -63), (WHOLE, -63))
+    assert_ends(E, cuda, tiling, "f32", out, (WHOLE, 120), (WHOLE, -16))
+    assert_ends(E, cuda, tiling, "f32", out, (WHOLE, 52), (WHOLE, 52))
+    assert_ends(E, cuda, tiling, "f32", out, ([0.0], 64), (WHOLE, 63))
