@@ -394,7 +394,7 @@ class TPMLPStack:
             raise ValueError("ffn must be divisible by P")
         if product not in ("f32", "bf16", "bf16_fused", "fp8"):
             raise ValueError(f"product {product!r}")
-        if not 0.0 <= dropout < 1.0:
+        if not 0.0 <= dropout <= 1.0 - 2.0 ** -16:  # what echo_dropout_add takes
             raise ValueError(f"dropout {dropout!r}")
         self.L, self.H, self.F, self.P, self.product = layers, hidden, ffn, P, product
         dev = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
