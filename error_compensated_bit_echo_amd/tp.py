@@ -208,6 +208,21 @@ def _fns():
         B.echo_quantize_fp8(mats, rows, cols)
         return rows, cols
 
+    def flat(*lists):
+        """The tensors of lists of 8-bit matrices, for save_for_backward."""
+        return [t for mats in lists for m in mats for t in m]
+
+    def matrices(tensors):
+        """8-bit matrices from saved tensors.  A hook may have moved them: codes that lost
+        their rows' padding on the way get it back."""
+        mats = []
+        for codes, scales in zip(tensors[::2], tensors[1::2]):
+            if codes.shape[0] > 1 and codes.stride(0) % 16:
+                padded = codes.new_empty(codes.shape[0], (codes.shape[1] + 15) // 16 * 16)[:, :codes.shape[1]]
+                codes = padded.copy_(codes)
+            mats.append((codes, scales))
+        return mats
+
     def products(A, W, dtype):
         out = [torch.empty(A[0][0].shape[0], W[0][0].shape[0], dtype=dtype, device=A[0][0].device) for _ in A]
         B.echo_gemm_fp8(A, W, out)
@@ -225,8 +240,8 @@ def _fns():
             P = group.P
             hs, ws = hw[:P], hw[P:]
             h8, h8t = quantize([h.detach().contiguous() for h in hs], "e4m3")
-            ctx.P, ctx.w8, ctx.h8t = P, w8, h8t
-            ctx.h_dtype, ctx.w_dtype = hs[0].dtype, ws[0].dtype
+            ctx.save_for_backward(*flat(h8t, w8[0]))
+            ctx.P, ctx.h_dtype, ctx.w_dtype = P, hs[0].dtype, ws[0].dtype
             parts = products(h8, w8[1], torch.bfloat16)
             return group.allreduce([p.view(-1) for p in parts], B.ECHO_FWD).view(shape)
 
@@ -234,12 +249,13 @@ def _fns():
         @once
         def backward(ctx, grad):
             P = ctx.P
+            saved = ctx.saved_tensors
             g8, g8t = quantize([grad.contiguous()], "e5m2")
             dh = dw = (None,) * P
             if any(ctx.needs_input_grad[3:3 + P]):
-                dh = tuple(d.to(ctx.h_dtype) for d in products(g8 * P, ctx.w8[0], torch.bfloat16))
+                dh = tuple(d.to(ctx.h_dtype) for d in products(g8 * P, matrices(saved[2 * P:]), torch.bfloat16))
             if any(ctx.needs_input_grad[3 + P:]):
-                dw = tuple(d.to(ctx.w_dtype) for d in products(ctx.h8t, g8t * P, torch.float32))
+                dw = tuple(d.to(ctx.w_dtype) for d in products(matrices(saved[:2 * P]), g8t * P, torch.float32))
             return (None, None, None) + dh + dw
 
     class ColumnParallelFp8(torch.autograd.Function):
@@ -251,21 +267,22 @@ def _fns():
         @staticmethod
         def forward(ctx, group: "EchoGroup", w8, a, *w1s):
             a8, a8t = quantize([a.detach().contiguous()], "e4m3")
-            ctx.group, ctx.w8, ctx.a8t = group, w8, a8t
-            ctx.shape, ctx.a_dtype, ctx.w_dtype = a.shape, a.dtype, w1s[0].dtype
+            ctx.save_for_backward(*flat(a8t, w8[0]))
+            ctx.group, ctx.shape, ctx.a_dtype, ctx.w_dtype = group, a.shape, a.dtype, w1s[0].dtype
             return tuple(products(a8 * group.P, w8[1], torch.bfloat16))
 
         @staticmethod
         @once
         def backward(ctx, *gpres):
             P = ctx.group.P
+            saved = ctx.saved_tensors
             g8, g8t = quantize([g.contiguous() for g in gpres], "e5m2")
             da, dw = None, (None,) * P
             if ctx.needs_input_grad[2]:
-                parts = products(g8, ctx.w8[0], torch.bfloat16)
+                parts = products(g8, matrices(saved[2:]), torch.bfloat16)
                 da = ctx.group.allreduce([p.view(-1) for p in parts], B.ECHO_BWD).view(ctx.shape).to(ctx.a_dtype)
             if any(ctx.needs_input_grad[3:]):
-                dw = tuple(d.to(ctx.w_dtype) for d in products(ctx.a8t * P, g8t, torch.float32))
+                dw = tuple(d.to(ctx.w_dtype) for d in products(matrices(saved[:2]) * P, g8t, torch.float32))
             return (None, None, da) + dw
 
     class DropoutAdd(torch.autograd.Function):
