@@ -199,14 +199,22 @@ def _fns():
 
     once = torch.autograd.function.once_differentiable
 
-    def quantize(mats, fmt):
-        """Row blocks of fp32 or bf16 matrices [T, K], both ways: (as they are, transposed)."""
+    def quantize(mats, fmt, straight=True, transposed=True):
+        """Row blocks of fp32 or bf16 matrices [T, K], as they are and transposed (None: not
+        wanted)."""
         R, C = mats[0].shape
         dev = mats[0].device
-        rows = [B.EchoFp8.empty(R, C, fmt, device=dev) for _ in mats]
-        cols = [B.EchoFp8.empty(C, R, fmt, device=dev) for _ in mats]
+        rows = [B.EchoFp8.empty(R, C, fmt, device=dev) for _ in mats] if straight else None
+        cols = [B.EchoFp8.empty(C, R, fmt, device=dev) for _ in mats] if transposed else None
         B.echo_quantize_fp8(mats, rows, cols)
         return rows, cols
+
+    def kept(acts8t, w8, for_inputs, for_weights):
+        """The operands of the backward products: transposed activations for the weights'
+        gradients, weights for the inputs' (empty where not wanted)."""
+        if for_inputs and w8[0] is None:
+            raise ValueError("the weights were laid out for a pass without gradients")
+        return (acts8t if for_weights else []), (w8[0] if for_inputs else [])
 
     def flat(*lists):
         """The tensors of lists of 8-bit matrices, for save_for_backward."""
@@ -233,15 +241,18 @@ def _fns():
         ranks through Echo; backward gives dh_r = q(g) q(W2_r)^T (bfloat16) and
         dW2_r = q(h_r^T) q(g^T)^T (fp32).  q is the rounding to 8 bits, with blocks
         along the dimension that is summed over; it passes gradients straight
-        through.  ``w8``: the weights both ways (TPMLPStack.quantize_weights)."""
+        through.  ``w8``: the weights both ways (TPMLPStack.quantize_weights).  Only what
+        the gradients asked for need is laid out and kept; ``grads`` false: none."""
 
         @staticmethod
-        def forward(ctx, group: "EchoGroup", shape, w8, *hw):
+        def forward(ctx, group: "EchoGroup", shape, w8, grads: bool, *hw):
             P = group.P
             hs, ws = hw[:P], hw[P:]
-            h8, h8t = quantize([h.detach().contiguous() for h in hs], "e4m3")
-            ctx.save_for_backward(*flat(h8t, w8[0]))
-            ctx.P, ctx.h_dtype, ctx.w_dtype = P, hs[0].dtype, ws[0].dtype
+            for_h, for_w = (grads and any(ctx.needs_input_grad[i:i + P]) for i in (4, 4 + P))
+            h8, h8t = quantize([h.detach().contiguous() for h in hs], "e4m3", True, for_w)
+            h8t, w8b = kept(h8t, w8, for_h, for_w)
+            ctx.save_for_backward(*flat(h8t, w8b))
+            ctx.P, ctx.n_acts, ctx.h_dtype, ctx.w_dtype = P, 2 * len(h8t), hs[0].dtype, ws[0].dtype
             parts = products(h8, w8[1], torch.bfloat16)
             return group.allreduce([p.view(-1) for p in parts], B.ECHO_FWD).view(shape)
 
@@ -250,13 +261,14 @@ def _fns():
         def backward(ctx, grad):
             P = ctx.P
             saved = ctx.saved_tensors
-            g8, g8t = quantize([grad.contiguous()], "e5m2")
+            for_h, for_w = (any(ctx.needs_input_grad[i:i + P]) for i in (4, 4 + P))
+            g8, g8t = quantize([grad.contiguous()], "e5m2", for_h, for_w)
             dh = dw = (None,) * P
-            if any(ctx.needs_input_grad[3:3 + P]):
-                dh = tuple(d.to(ctx.h_dtype) for d in products(g8 * P, matrices(saved[2 * P:]), torch.bfloat16))
-            if any(ctx.needs_input_grad[3 + P:]):
-                dw = tuple(d.to(ctx.w_dtype) for d in products(matrices(saved[:2 * P]), g8t * P, torch.float32))
-            return (None, None, None) + dh + dw
+            if for_h:
+                dh = tuple(d.to(ctx.h_dtype) for d in products(g8 * P, matrices(saved[ctx.n_acts:]), torch.bfloat16))
+            if for_w:
+                dw = tuple(d.to(ctx.w_dtype) for d in products(matrices(saved[:ctx.n_acts]), g8t * P, torch.float32))
+            return (None, None, None, None) + dh + dw
 
     class ColumnParallelFp8(torch.autograd.Function):
         """f(a) @ W1_r in 8-bit products: forward gives every rank's pre-activation
@@ -265,9 +277,12 @@ def _fns():
         (fp32)."""
 
         @staticmethod
-        def forward(ctx, group: "EchoGroup", w8, a, *w1s):
-            a8, a8t = quantize([a.detach().contiguous()], "e4m3")
-            ctx.save_for_backward(*flat(a8t, w8[0]))
+        def forward(ctx, group: "EchoGroup", w8, grads: bool, a, *w1s):
+            for_a, for_w = grads and ctx.needs_input_grad[3], grads and any(ctx.needs_input_grad[4:])
+            a8, a8t = quantize([a.detach().contiguous()], "e4m3", True, for_w)
+            a8t, w8b = kept(a8t, w8, for_a, for_w)
+            ctx.save_for_backward(*flat(a8t, w8b))
+            ctx.n_acts = 2 * len(a8t)
             ctx.group, ctx.shape, ctx.a_dtype, ctx.w_dtype = group, a.shape, a.dtype, w1s[0].dtype
             return tuple(products(a8 * group.P, w8[1], torch.bfloat16))
 
@@ -276,14 +291,15 @@ def _fns():
         def backward(ctx, *gpres):
             P = ctx.group.P
             saved = ctx.saved_tensors
-            g8, g8t = quantize([g.contiguous() for g in gpres], "e5m2")
+            for_a, for_w = ctx.needs_input_grad[3], any(ctx.needs_input_grad[4:])
+            g8, g8t = quantize([g.contiguous() for g in gpres], "e5m2", for_a, for_w)
             da, dw = None, (None,) * P
-            if ctx.needs_input_grad[2]:
-                parts = products(g8, matrices(saved[2:]), torch.bfloat16)
+            if for_a:
+                parts = products(g8, matrices(saved[ctx.n_acts:]), torch.bfloat16)
                 da = ctx.group.allreduce([p.view(-1) for p in parts], B.ECHO_BWD).view(ctx.shape).to(ctx.a_dtype)
-            if any(ctx.needs_input_grad[3:]):
-                dw = tuple(d.to(ctx.w_dtype) for d in products(matrices(saved[:2]) * P, g8t, torch.float32))
-            return (None, None, da) + dw
+            if for_w:
+                dw = tuple(d.to(ctx.w_dtype) for d in products(matrices(saved[:ctx.n_acts]) * P, g8t, torch.float32))
+            return (None, None, None, da) + dw
 
     class DropoutAdd(torch.autograd.Function):
         """residual + dropout(x); backward draws the same mask again.  ``rng`` must still
@@ -316,6 +332,11 @@ def _fns():
 _FNS = None
 
 
+def _grad_enabled() -> bool:
+    import torch
+    return torch.is_grad_enabled()  # always false inside a Function's forward
+
+
 def row_parallel_echo(group: "EchoGroup", hs, ws, shape, fused: bool):
     """g(sum_r h_r @ W2_r) with bf16 products on libecho's kernel (see RowParallelEcho)."""
     global _FNS
@@ -338,7 +359,7 @@ def row_parallel_fp8(group: "EchoGroup", hs, ws, shape, w8):
     global _FNS
     if _FNS is None:
         _FNS = _fns()
-    return _FNS[4].apply(group, shape, w8, *hs, *ws)
+    return _FNS[4].apply(group, shape, w8, _grad_enabled(), *hs, *ws)
 
 
 def column_parallel_fp8(group: "EchoGroup", a, ws, w8):
@@ -347,7 +368,7 @@ def column_parallel_fp8(group: "EchoGroup", a, ws, w8):
     global _FNS
     if _FNS is None:
         _FNS = _fns()
-    return _FNS[5].apply(group, w8, a, *ws)
+    return _FNS[5].apply(group, w8, _grad_enabled(), a, *ws)
 
 
 def dropout_add(x, residual, p: float, rng, offset: int = 0, first: int = 0):
@@ -360,12 +381,13 @@ def dropout_add(x, residual, p: float, rng, offset: int = 0, first: int = 0):
     return _FNS[6].apply(x, residual, p, rng, offset, first)
 
 
-def quantize_weights_fp8(ws):
+def quantize_weights_fp8(ws, backward: bool = True):
     """P weights [K_in, K_out] in e4m3 with a scale per 128 x 128 block: (as they are,
-    transposed), the operands of the input-gradient and of the forward products."""
+    transposed), the operands of the input-gradient and of the forward products; the
+    first None without ``backward``."""
     R, C = ws[0].shape
     dev = ws[0].device
-    rows = [B.EchoFp8.empty(R, C, block_rows=B.ECHO_FP8_BLOCK, device=dev) for _ in ws]
+    rows = [B.EchoFp8.empty(R, C, block_rows=B.ECHO_FP8_BLOCK, device=dev) for _ in ws] if backward else None
     cols = [B.EchoFp8.empty(C, R, block_rows=B.ECHO_FP8_BLOCK, device=dev) for _ in ws]
     B.echo_quantize_fp8([w.detach() for w in ws], rows, cols)
     return rows, cols
@@ -445,8 +467,8 @@ class TPMLPStack:
         for l in range(self.L):
             a = x * torch.rsqrt(x.pow(2).mean(dim=-1, keepdim=True) + 1e-6)
             if self.product == "fp8":
-                w8 = weights8[l] if weights8 is not None else (quantize_weights_fp8(self.w1[l]),
-                                                               quantize_weights_fp8(self.w2[l]))
+                w8 = weights8[l] if weights8 is not None else [quantize_weights_fp8(w, torch.is_grad_enabled())
+                                                               for w in (self.w1[l], self.w2[l])]
                 pres = column_parallel_fp8(group, a, self.w1[l], w8[0])
                 # gelu in fp32 of the bfloat16 pre-activations
                 y = row_parallel_fp8(group, [gelu(p.float()) for p in pres], self.w2[l], x.shape, w8[1])

@@ -78,3 +78,71 @@ def test_hooks_see_the_saved_operands_and_may_move_them(cuda, tp, layer):
         _, outs, grads, inputs = layer(tp, cuda)
         got = backward(outs, grads, inputs)
     assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+@pytest.fixture
+def quantized(tp, monkeypatch):
+    """Records (rows of X, rows wanted, columns wanted) of every call of the quantizer."""
+    calls = []
+    plain = tp.B.echo_quantize_fp8
+
+    def record(X, rows=None, cols=None, stream=None):
+        calls.append((tuple(X[0].shape), rows is not None, cols is not None))
+        return plain(X, rows, cols, stream)
+
+    monkeypatch.setattr(tp.B, "echo_quantize_fp8", record)
+    return calls
+
+
+@pytest.mark.parametrize("layer", [row, column])
+def test_a_pass_without_gradients_lays_nothing_out_for_them(cuda, tp, quantized, layer):
+    import torch
+    _, want, _, _ = layer(tp, cuda)
+    quantized.clear()
+    with torch.no_grad():
+        _, got, _, _ = layer(tp, cuda)
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    acts = (T, F // P) if layer is row else (T, H)
+    assert [c for c in quantized if c[0] == acts] == [(acts, True, False)]
+
+
+@pytest.mark.parametrize("layer", [row, column])
+def test_only_the_gradients_asked_for_are_laid_out_for(cuda, tp, quantized, layer):
+    import torch
+    _, outs, grads, inputs = layer(tp, cuda)
+    want = backward(outs, grads, inputs)
+    n_w = P
+    acts, back = ((T, F // P), (T, H)) if layer is row else ((T, H), (T, F // P))
+    for w_grad, x_grad in ((True, False), (False, True)):
+        quantized.clear()
+        group, outs, grads, inputs = layer(tp, cuda, w_grad, x_grad)
+        assert [c for c in quantized if c[0] == acts] == [(acts, True, w_grad)]
+        quantized.clear()
+        reductions = len(group.log)
+        got = backward(outs, grads, inputs)
+        assert quantized == [(back, x_grad, w_grad)]
+        assert len(group.log) - reductions == (1 if layer is column and x_grad else 0)
+        for i, (a, b) in enumerate(zip(got, want)):
+            asked = w_grad if i >= len(inputs) - n_w else x_grad
+            assert (a is None) if not asked else torch.equal(a, b)
+
+
+def test_stack_without_gradients_lays_out_one_orientation(cuda, tp, quantized):
+    """Weights too, where the pass quantizes them itself."""
+    import torch
+    model = tp.TPMLPStack(2, H, F, P, seed=11, device=cuda, product="fp8")
+    x = tensors(cuda, 12, (T, H))[0]
+    group = tp.EchoGroup(P, T * H, mode="exact", device=cuda)
+    want = model.forward(x, group).detach()
+    assert any(rows and cols for _, rows, cols in quantized)
+    quantized.clear()
+    with torch.no_grad():
+        got = model.forward(x, group)
+    assert torch.equal(got, want) and len(quantized) == 8
+    assert not any(rows and cols for _, rows, cols in quantized)
+    # weights laid out for such a pass alone do not serve a backward pass
+    w8 = tp.quantize_weights_fp8(model.w1[0], backward=False)
+    with pytest.raises(ValueError):
+        tp.column_parallel_fp8(group, x.clone().requires_grad_(), model.w1[0], w8)
+    with torch.no_grad():
+        tp.column_parallel_fp8(group, x, model.w1[0], w8)
