@@ -488,15 +488,16 @@ class TPMLPStack:
         return x
 
 
-def train_step(model: TPMLPStack, group: EchoGroup, x0, target):
-    """One forward + backward; returns (loss, dL/dx0, [dL/dW...])."""
+def train_step(model: TPMLPStack, group: EchoGroup, x0, target, weights8=None):
+    """One forward + backward; returns (loss, dL/dx0, [dL/dW...]).  ``weights8``: the
+    weights in 8 bits (quantize_weights), for several steps before they change."""
     import torch
 
     group.reset()
     x = x0.detach().clone().requires_grad_()
     for p in model.parameters():
         p.grad = None
-    y = model.forward(x, group)
+    y = model.forward(x, group, weights8=weights8)
     loss = torch.nn.functional.mse_loss(y, target)
     loss.backward()
     if model.rng is not None and model.training:
