@@ -23,6 +23,12 @@ int64_t blocks(int64_t n) { return (n + ECHO_FP8_BLOCK - 1) / ECHO_FP8_BLOCK; }
 // (quantizer) or 512 (product) to a tile, a quarter of a tile at the smallest.
 constexpr int64_t kMaxTiles = (int64_t{1} << 21) - 1;
 
+// Whether rows `ld` elements of `es` bytes apart do not overlap and span at most 2^48
+// bytes: beyond what a device addresses, and far from where the arithmetic below wraps.
+bool pitch_fits(int64_t rows, int64_t cols, int64_t ld, int64_t es) {
+  return rows <= 1 || (ld >= cols && ld <= (int64_t{1} << 48) / (rows * es));
+}
+
 // The memory a strided matrix takes: `count` runs of `width` bytes, `pitch` bytes
 // from one run's start to the next's (pitch 0 where there is one run).
 struct Area {
@@ -115,7 +121,7 @@ echo_status echo_quantize_fp8(const void* const* X, int32_t P, int64_t rows, int
   if (rows == 0 || cols == 0) return ECHO_OK;
   if (P * blocks(rows) * blocks(cols) > kMaxTiles) return ECHO_ERR_SHAPE;
   if (X == nullptr) return ECHO_ERR_ARG;
-  if ((rows > 1 && ldx < cols) || ldx > (int64_t{1} << 40)) return ECHO_ERR_SHAPE;
+  if (!pitch_fits(rows, cols, ldx, es) || ldx > (int64_t{1} << 40)) return ECHO_ERR_SHAPE;
   echo_status e;
   if (along_rows != nullptr && (e = check_fp8(*along_rows, P, rows, cols, true)) != ECHO_OK) return e;
   if (along_cols != nullptr && (e = check_fp8(*along_cols, P, cols, rows, true)) != ECHO_OK) return e;
@@ -172,7 +178,7 @@ echo_status echo_gemm_fp8(const echo_fp8* A, const echo_fp8* W, void* const* out
   if (M == 0 || N == 0) return ECHO_OK;
   if (P * blocks(M) * blocks(N) > kMaxTiles) return ECHO_ERR_SHAPE;
   if (out == nullptr) return ECHO_ERR_ARG;
-  if ((M > 1 && ldo < N) || ldo > (int64_t{1} << 40)) return ECHO_ERR_SHAPE;
+  if (!pitch_fits(M, N, ldo, es) || ldo > (int64_t{1} << 40)) return ECHO_ERR_SHAPE;
   echo_status e;
   if (K > 0) {
     if ((e = check_fp8(*A, P, M, K, false)) != ECHO_OK) return e;
@@ -233,7 +239,9 @@ echo_status echo_dropout_add(const void* x, const void* residual, void* out, int
   const int64_t n = rows * cols;
   if (first < 0 || first > (int64_t{1} << 62) - n) return ECHO_ERR_ARG;
   if (n == 0) return ECHO_OK;
-  if (rows > 1 && (ldx < cols || ldo < cols || (residual != nullptr && ldr < cols))) return ECHO_ERR_SHAPE;
+  if (!pitch_fits(rows, cols, ldx, ex) || !pitch_fits(rows, cols, ldo, eo) ||
+      (residual != nullptr && !pitch_fits(rows, cols, ldr, eo)))
+    return ECHO_ERR_SHAPE;
   if (ldx > kMaxElems || ldr > kMaxElems || ldo > kMaxElems) return ECHO_ERR_SHAPE;
   if (x == nullptr || out == nullptr || rng == nullptr) return ECHO_ERR_ARG;
   if (!aligned(x, static_cast<uintptr_t>(ex)) || !aligned(out, static_cast<uintptr_t>(eo)) ||
