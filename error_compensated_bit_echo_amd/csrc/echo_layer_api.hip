@@ -29,6 +29,9 @@ bool pitch_fits(int64_t rows, int64_t cols, int64_t ld, int64_t es) {
   return rows <= 1 || (ld >= cols && ld <= (int64_t{1} << 48) / (rows * es));
 }
 
+// The pitch of `rows` rows of `cols`: where there is one row, `ld` says nothing.
+int64_t pitch_of(int64_t rows, int64_t cols, int64_t ld) { return rows > 1 ? ld : cols; }
+
 // The memory a strided matrix takes: `count` runs of `width` bytes, `pitch` bytes
 // from one run's start to the next's (pitch 0 where there is one run).
 struct Area {
@@ -121,7 +124,8 @@ echo_status echo_quantize_fp8(const void* const* X, int32_t P, int64_t rows, int
   if (rows == 0 || cols == 0) return ECHO_OK;
   if (P * blocks(rows) * blocks(cols) > kMaxTiles) return ECHO_ERR_SHAPE;
   if (X == nullptr) return ECHO_ERR_ARG;
-  if (!pitch_fits(rows, cols, ldx, es) || ldx > (int64_t{1} << 40)) return ECHO_ERR_SHAPE;
+  ldx = pitch_of(rows, cols, ldx);
+  if (!pitch_fits(rows, cols, ldx, es)) return ECHO_ERR_SHAPE;
   echo_status e;
   if (along_rows != nullptr && (e = check_fp8(*along_rows, P, rows, cols, true)) != ECHO_OK) return e;
   if (along_cols != nullptr && (e = check_fp8(*along_cols, P, cols, rows, true)) != ECHO_OK) return e;
@@ -178,7 +182,8 @@ echo_status echo_gemm_fp8(const echo_fp8* A, const echo_fp8* W, void* const* out
   if (M == 0 || N == 0) return ECHO_OK;
   if (P * blocks(M) * blocks(N) > kMaxTiles) return ECHO_ERR_SHAPE;
   if (out == nullptr) return ECHO_ERR_ARG;
-  if (!pitch_fits(M, N, ldo, es) || ldo > (int64_t{1} << 40)) return ECHO_ERR_SHAPE;
+  ldo = pitch_of(M, N, ldo);
+  if (!pitch_fits(M, N, ldo, es)) return ECHO_ERR_SHAPE;
   echo_status e;
   if (K > 0) {
     if ((e = check_fp8(*A, P, M, K, false)) != ECHO_OK) return e;
@@ -239,10 +244,11 @@ echo_status echo_dropout_add(const void* x, const void* residual, void* out, int
   const int64_t n = rows * cols;
   if (first < 0 || first > (int64_t{1} << 62) - n) return ECHO_ERR_ARG;
   if (n == 0) return ECHO_OK;
-  if (!pitch_fits(rows, cols, ldx, ex) || !pitch_fits(rows, cols, ldo, eo) ||
-      (residual != nullptr && !pitch_fits(rows, cols, ldr, eo)))
+  ldx = pitch_of(rows, cols, ldx);
+  ldo = pitch_of(rows, cols, ldo);
+  ldr = residual != nullptr ? pitch_of(rows, cols, ldr) : cols;
+  if (!pitch_fits(rows, cols, ldx, ex) || !pitch_fits(rows, cols, ldo, eo) || !pitch_fits(rows, cols, ldr, eo))
     return ECHO_ERR_SHAPE;
-  if (ldx > kMaxElems || ldr > kMaxElems || ldo > kMaxElems) return ECHO_ERR_SHAPE;
   if (x == nullptr || out == nullptr || rng == nullptr) return ECHO_ERR_ARG;
   if (!aligned(x, static_cast<uintptr_t>(ex)) || !aligned(out, static_cast<uintptr_t>(eo)) ||
       !aligned(residual, static_cast<uintptr_t>(eo)) || !aligned(rng, 8))
@@ -250,8 +256,8 @@ echo_status echo_dropout_add(const void* x, const void* residual, void* out, int
   const Area ao = area(out, rows, cols * eo, ldo * eo), ax = area(x, rows, cols * ex, ldx * ex);
   const Area ag = area(rng, 1, 16, 0);
   // in place: every element is read and written by one thread, the read first
-  const bool on_x = out == x && ex == eo && (rows == 1 || ldx == ldo);
-  const bool on_r = out == residual && (rows == 1 || ldr == ldo);
+  const bool on_x = out == x && ex == eo && ldx == ldo;
+  const bool on_r = out == residual && ldr == ldo;
   if ((!on_x && overlap(ao, ax)) || overlap(ao, ag)) return ECHO_ERR_ARG;
   if (residual != nullptr && !on_r && overlap(ao, area(residual, rows, cols * eo, ldr * eo))) return ECHO_ERR_ARG;
   echo::DropoutArgs a{};

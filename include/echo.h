@@ -307,7 +307,7 @@ echo_status echo_debug_views(const echo_state* st, echo_dir dir, echo_views* out
  * zeros), and the conventions above hold otherwise (stream order, validation
  * before any launch, one kernel launch per call, no allocation, no workspace,
  * so calls may be captured and may run on several streams at once).  A matrix
- * spans at most 2^48 bytes.
+ * spans at most 2^48 bytes; the pitch in elements of a single row is not used.
  * Non-finite values are specified for these operators.  */
 
 /* 8-bit formats: e4m3 (bias 7, largest 448, no infinity, NaN 0x7F/0xFF) and
