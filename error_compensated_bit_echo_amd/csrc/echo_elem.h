@@ -50,14 +50,6 @@ __device__ __forceinline__ void load8(const void* base, int64_t at, float v[8]) 
   for (int i = 0; i < 8; ++i) v[i] = static_cast<float>(x[i]);
 }
 
-// Elements at .. at + n - 1 (n < 8); the rest reads as zeros.
-template <int E>
-__device__ __forceinline__ void load_part(const void* base, int64_t at, int n, float v[8]) {
-  typedef typename ElemOf<E>::T T;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) v[i] = i < n ? static_cast<float>(static_cast<const T*>(base)[at + i]) : 0.0f;
-}
-
 template <int E>
 __device__ __forceinline__ float load1(const void* base, int64_t at) {
   return static_cast<float>(static_cast<const typename ElemOf<E>::T*>(base)[at]);
