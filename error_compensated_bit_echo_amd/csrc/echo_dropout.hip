@@ -6,10 +6,10 @@
 // random numbers: as easy as 1, 2, 3", SC 2011) with counter (chunk, step) and
 // key rng[0] give the chunk's eight 16-bit draws, and e is kept iff its draw is
 // at least the threshold.  A thread owns the part of one chunk that lies in one
-// row: eight elements share one generator call, which costs 20 32 x 32 -> 64-bit
-// products and 40 exclusive ors, five 32-bit operations per element.  Nothing is
-// stored but the output, and the result does not depend on how the elements are
-// split over threads.
+// row: eight elements share one generator call, which costs 20 products of 32 x 32
+// to 64 bits and 40 exclusive ors, an instruction each: seven and a half an element,
+// the key's additions being scalar.  Nothing is stored but the output, and the result
+// does not depend on how the elements are split over threads.
 //
 // Bound by the memory: 16384 x 8192 bfloat16 with a residual takes 140 us, 5.75
 // TB/s of what it has to move (a plain elementwise copy reaches 6.2 on this card);

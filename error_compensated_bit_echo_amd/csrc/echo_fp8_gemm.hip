@@ -92,9 +92,11 @@ __device__ __forceinline__ void store_each(void* out, int64_t at, int64_t left, 
 // k: wavefront w takes the blocks w, w + NW, ... of 128 and reads its codes of W and A
 // straight from memory (W is read once in all), and the sums meet in LDS in a fixed
 // order.  Codes are widened to bfloat16 (the matrix cores idle anyway); exponent-byte
-// scales are applied as they are widened.  Bound by the bytes of W and by the launch: one
-// token against N = K = 8192 takes 14.4 us from call to call, 4.7 TB/s of codes (reading
-// alone reaches 7.1, and an empty call takes 4).
+// scales are applied as they are widened.  One token against N = K = 8192: the kernel takes
+// 14.9 us (16.0 over weights that no cache holds), 4.5 TB/s of codes, where reading alone
+// reaches 7.1; from call to call 14.5, so the launch is hidden behind the kernel before it.
+// The wavefronts wait for 53 % of their cycles: each has two rounds of loads, the second
+// issued when the first has been multiplied.
 
 // A lane's 32 bytes of a block of 128: 16-byte chunks g and g + 4, so that the four
 // lanes of a row read 64 contiguous bytes at a time.  TAIL: the block is cut off by K,
@@ -276,10 +278,12 @@ __global__ __launch_bounds__(256) void echo_gemm_fp8_zero_k(const GemmFp8Args a)
 // Rows past the edge read as zeros (the buffer resources end with the matrix), and
 // so does what lies past K in the last step: 16-byte chunks by an offset out of
 // range, the bytes behind K in the last chunk by one pass over the slab.
-// Measured: M = N = K = 8192 450 us (2.44 PFLOP/s) and, with fp32 outputs, 736 (1.49;
-// the library's bfloat16 product reaches 1.44); P = 4, M = 2048, N = K = 4096 121 us (2.27).
-// At these sizes the power bounds it: the matrix cores are busy 57 % of the cycles of the
-// 8-bit form and 77 % of the bfloat16 one, and the clock falls to 2.0 and 1.7 GHz.
+// Measured: M = N = K = 8192 402 us (2.74 PFLOP/s; the library's product without block
+// scales 339) and, with fp32 outputs, 738 (1.49; the library's bfloat16 product reaches
+// 1.44); P = 4, M = 2048, N = K = 4096 108-125 us on three machines (2.2-2.5).  The matrix
+// cores are busy 74 % of the CUs' busy cycles at 8192 (80 % with fp32 outputs) and 67 % at
+// the shorter k, where a tile's first loads and its store weigh more; the clock falls to
+// 1.7 GHz at 8192 and 1.9 at the shorter k.
 
 // An offset past the end of every buffer resource here (they stay below 2^31 bytes).
 constexpr uint32_t kPastEnd = 0x80000000u;
@@ -774,8 +778,10 @@ __global__ __launch_bounds__(64 * WM * WN * G) void echo_gemm_fp8_tile_k(const G
 // row l % 16 of the A rows, columns 4 (l / 16) .. + 3 of the W rows.  A step's fragments
 // of A stay in registers; those of W come one sub-tile ahead.
 // WB: W's scales are of blocks of 128 rows, one for all of a wavefront's columns.
-// Measured: P = 2, M = N = K = 4096 138 us (1.99 PFLOP/s; exponent bytes, which the
-// instruction applies, 121), bound by the vector instructions beside the matrix cores.
+// Measured: P = 2, M = N = K = 4096 130 us, 150 with a scale per row of W (2.1 and 1.8
+// PFLOP/s; exponent bytes, which the instruction applies, 107).  The matrix cores are busy
+// 49 and 42 % of the cycles: 47 and 42 % of the LDS's active cycles are bank conflicts of the
+// fragment reads, and the 256 x 256 tile spills 64 and 104 bytes of registers a lane.
 template <int BM, int BN, int WM, int WN, int S, int G, bool WB, bool A5, bool W5>
 __global__ __launch_bounds__(64 * WM * WN * G) void echo_gemm_fp8_fma_k(const GemmFp8Args a, uint32_t gm, uint32_t gn) {
   constexpr int NW = WM * WN, RW = BM / WM, CW = BN / WN, MI = RW / 16, NJ = CW / 16;
@@ -945,7 +951,8 @@ hipError_t thin(const GemmFp8Args& a, int P, hipStream_t s) {
 // Above that, tiles by the number t of 64 x 64 tiles over all ranks and b of 128 x 128
 // ones; us for bfloat16 outputs with exponent bytes, then fp32 outputs:
 //   t <= 256, the CUs, and K over 1024: a K step of a lone workgroup is bound by its own
-//     chain of waits (0.5 us; more slabs changed nothing), so four groups of four
+//     chain of waits (0.5 us; more slabs alone changed nothing, as a step's scales are
+//     loaded one step ahead whatever the number of slabs), so four groups of four
 //     wavefronts share k (M = 64, N = K = 8192: 19.9 against 23.8 with two groups and
 //     31.8 with one; M = 500, N = 640, K = 7552, fp32 output: 20.7, 23.9 and 31.9);
 //   t <= 512: two groups, two workgroups per CU (P = 4, M = 128, N = K = 4096: 18.7, 26.5
@@ -958,9 +965,10 @@ hipError_t thin(const GemmFp8Args& a, int P, hipStream_t s) {
 //     M = 64, N = 4096, K = 1024: 13.5, 16.2 against 15.1, 19.4 with 128 x 128 tiles and
 //     16.2, 19.9 with 64 x 64 ones in two groups);
 //   b < 384, or M <= 128: 128 x 128, four wavefronts, 2 slabs, two workgroups per CU
-//     (M = 1024, N = K = 4096: 25.4 against 30.6 with 256 x 128 tiles and 40.2 with 64 x 64;
-//     M = 128, N = 65536, K = 4096: 70.2, 77.9 against 74.7, 99.9 with 256 x 256 and 87, 96
-//     with 64 x 128);
+//     (M = 1024, N = 4096, K = 1024: 9.6, 14.5 against 12.1, 17.2 with 256 x 128 tiles and
+//     10.0, 14.3 with 64 x 128; M = 1280, N = K = 4096: 29.5, 48.3 against 30.1, 44.5 and
+//     30.8, 46.4; M = 128, N = 65536, K = 4096: 70.2, 77.9 against 74.7, 99.9 with
+//     256 x 256 and 87, 96 with 64 x 128);
 //   256 x 256 where those number at least 192, three quarters of the CUs (P = 4,
 //     M = 2048, N = K = 4096: 130 against 168 with 128 x 128 tiles);
 //   else 256 x 128, 3 slabs (P = 2, M = 1024, N = K = 4096: 37.3 against 38.5 with
@@ -968,8 +976,15 @@ hipError_t thin(const GemmFp8Args& a, int P, hipStream_t s) {
 // The same with fp32 scales and 16-bit outputs, where tiles have 128 columns at least and
 // two groups are the most that fits LDS (P = 4, M = 64, N = K = 4096: 18.6 against 22.2
 // with one; M = 1024, N = K = 4096 27.5 with two groups against 33.8).
+// (b < 384: M = 1024, N = 4096, K = 1024 11.4 against 13.6 with 256 x 128 and 10.7 with
+// 64 x 128; M = 1280, N = K = 4096 39.5 against 36.6 and 36.4.)
 // fp32 scales and fp32 outputs take 256 x 128 tiles at most: a block's sum has
-// accumulators of its own.
+// accumulators of its own (b < 384, same sizes: 15.9 against 20.0 and 15.6; 78.7 against
+// 58.8 and 61.7, where the rule made for the other forms loses).
+// The rules count tiles and look at M; they do not see how the last round of tiles fills
+// the CUs or how much of a tile lies past N: M = 2304, N = 8192, K = 4096 (288 tiles of
+// 256 x 256) takes 92 us where M = 2048 takes 55, and M = 65536, N = 64, K = 4096 58,
+// reading its operands 38.
 template <bool A5, bool W5, bool E8, bool WB>
 hipError_t launch(const GemmFp8Args& a, int P, hipStream_t s) {
   const int64_t columns = (a.N + 15) / 16 * P;  // 16 rows of W each
