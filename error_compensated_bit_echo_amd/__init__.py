@@ -13,6 +13,8 @@ _BINDING_NAMES = {
     "echo_reduce_noalloc", "ECHO_STATIC_SCRATCH_BYTES",
     "echo_wire_bytes", "echo_debug_views", "echo_status_str", "library_path",
     "load_library", "EchoFp8", "echo_quantize_fp8", "echo_gemm_fp8", "echo_dropout_add",
+    "EchoBlock", "echo_block_norm", "echo_block_norm_workspace", "echo_block_norm_backward", "echo_clip_workspace",
+    "echo_grad_norm", "echo_clip_grads", "echo_embed", "echo_embed_workspace", "echo_embed_backward",
 }
 
 

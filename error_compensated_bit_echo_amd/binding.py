@@ -93,6 +93,28 @@ class _Fp8Struct(ctypes.Structure):
     ]
 
 
+class EchoBlock(ctypes.Structure):
+    """echo_block of the C ABI."""
+
+    _fields_ = [
+        ("rows", ctypes.c_int64),
+        ("cols", ctypes.c_int64),
+        ("gate", ctypes.c_void_p),
+        ("ld_gate", ctypes.c_int64),
+        ("gate_rows", ctypes.c_int64),
+        ("w_post", ctypes.c_void_p),
+        ("w_pre", ctypes.c_void_p),
+        ("residual_scale", ctypes.c_double),
+        ("weight_offset", ctypes.c_double),
+        ("eps", ctypes.c_double),
+        ("x_dtype", ctypes.c_int32),
+        ("y_dtype", ctypes.c_int32),
+        ("a_dtype", ctypes.c_int32),
+        ("param_dtype", ctypes.c_int32),
+        ("post_norm", ctypes.c_int32),
+    ]
+
+
 class EchoError(RuntimeError):
     def __init__(self, status: int, what: str = ""):
         self.status = status
@@ -118,7 +140,8 @@ def load_library():
         build.build_library()
     lib = ctypes.CDLL(path)
     vp, sz, i32, u64p = ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int, ctypes.POINTER(ctypes.c_uint64)
-    cfgp, fp8p = ctypes.POINTER(EchoConfig), ctypes.POINTER(_Fp8Struct)
+    cfgp, fp8p, blkp = ctypes.POINTER(EchoConfig), ctypes.POINTER(_Fp8Struct), ctypes.POINTER(EchoBlock)
+    i64p, i32p = ctypes.POINTER(ctypes.c_int64), ctypes.POINTER(ctypes.c_int32)
     sig = {
         "echo_workspace_bytes": (sz, [cfgp]),
         "echo_init_state": (i32, [cfgp, vp, sz, vp, ctypes.POINTER(vp)]),
@@ -142,6 +165,18 @@ def load_library():
                                 ctypes.c_int64, ctypes.c_int64, ctypes.c_int32, vp]),
         "echo_dropout_add": (i32, [vp, vp, vp] + [ctypes.c_int64] * 5 + [ctypes.c_int32, ctypes.c_int32,
                                    ctypes.c_double, vp, ctypes.c_int64, ctypes.c_int64, vp]),
+        "echo_block_norm": (i32, [blkp] + [vp, ctypes.c_int64] * 4 + [vp]),
+        "echo_block_norm_workspace": (sz, [ctypes.c_int64] * 3),
+        "echo_block_norm_backward": (i32, [blkp] + [vp, ctypes.c_int64] * 7 + [vp, vp, vp, sz, vp]),
+        "echo_clip_workspace": (sz, [ctypes.c_int64]),
+        "echo_grad_norm": (i32, [ctypes.POINTER(vp), i64p, i32p, ctypes.c_int64, vp, vp, sz, vp]),
+        "echo_clip_grads": (i32, [ctypes.POINTER(vp), ctypes.POINTER(vp), i64p, i32p, ctypes.c_int64, ctypes.c_double,
+                                  vp, vp, sz, vp]),
+        "echo_embed": (i32, [ctypes.POINTER(vp), vp, ctypes.POINTER(vp), ctypes.c_int32] + [ctypes.c_int64] * 5 +
+                       [ctypes.c_int32] * 3 + [ctypes.c_int64, ctypes.c_double, vp]),
+        "echo_embed_workspace": (sz, [ctypes.c_int64] * 2),
+        "echo_embed_backward": (i32, [vp, vp, ctypes.POINTER(vp), ctypes.c_int32] + [ctypes.c_int64] * 5 +
+                                [ctypes.c_int32] * 3 + [ctypes.c_int64, ctypes.c_double, vp, sz, vp]),
     }
     for name, (res, args) in sig.items():
         f = getattr(lib, name)
@@ -503,3 +538,83 @@ def echo_dropout_add(x, out, p: float, rng, residual=None, offset: int = 0, firs
     _raise_if((_marshal or _native()).dropout_add(x, residual, out, p, rng, offset, first,
                                                   None if stream is None else stream.cuda_stream, _raw_current))
     return out
+
+
+# ---- operators of a training step around the blocks --------------------------
+
+
+def echo_block_norm(x, out=None, a=None, *, y=None, gate=None, w_post=None, w_pre=None, post_norm: bool = False,
+                    residual_scale: float = 1.0, weight_offset: float = 0.0, eps: float = 1e-6, stream=None):
+    """The end of one block and the start of the next: out = residual_scale * x + gate
+    * n with n = rmsnorm(y) * (weight_offset + w_post) (``post_norm``) or y, and a =
+    rmsnorm(out) * (weight_offset + w_pre).  Without ``y`` a is the norm of x; without
+    ``a`` only the stream is written.  x, y, out and a are of one shape [.., cols]
+    (float32 and one 16-bit type; x and out of one type); ``gate`` is [cols], or [g,
+    cols] with g a divisor of the rows: one for each run of rows / g of them.
+    ``out`` may be x itself."""
+    _raise_if((_marshal or _native()).block_norm(x, out, a, y, gate, w_post, w_pre, post_norm, residual_scale,
+                                                 weight_offset, eps, None if stream is None else stream.cuda_stream,
+                                                 _raw_current))
+
+
+def echo_block_norm_workspace(rows: int, cols: int, gate_rows: int = 0) -> int:
+    """Bytes of workspace of echo_block_norm_backward with gradients of parameters."""
+    return int(load_library().echo_block_norm_workspace(rows, cols, gate_rows))
+
+
+def echo_block_norm_backward(out, *, dout=None, da=None, dx=None, y=None, dy=None, gate=None, dgate=None, w_post=None,
+                             dw_post=None, w_pre=None, dw_pre=None, post_norm: bool = False, residual_scale: float = 1.0,
+                             weight_offset: float = 0.0, eps: float = 1e-6, workspace=None, stream=None):
+    """Gradients of echo_block_norm: from its ``out`` (x where there was no y), ``y`` and
+    the gradients ``dout`` and ``da`` to ``dx``, ``dy``, ``dgate``, ``dw_post`` and
+    ``dw_pre``, each of the type of what it is the gradient of, or None.  ``dx`` may be
+    dout itself.  ``workspace``: uint8 tensor of echo_block_norm_workspace bytes; by
+    default torch provides one for the call (not with a ``stream``)."""
+    _raise_if((_marshal or _native()).block_norm_backward(
+        out, dout, da, dx, y, dy, dgate, dw_post, dw_pre, gate, w_post, w_pre, post_norm, residual_scale, weight_offset,
+        eps, workspace, None if stream is None else stream.cuda_stream, _raw_current))
+
+
+def echo_clip_workspace(n_tensors: int) -> int:
+    """Bytes of workspace of echo_grad_norm and echo_clip_grads."""
+    return int(load_library().echo_clip_workspace(n_tensors))
+
+
+def echo_grad_norm(grads: Sequence, norm, workspace=None, stream=None):
+    """norm (one float32 element on the GPU) = the norm of all elements of ``grads``
+    (float32, bfloat16 and float16 tensors in any mix)."""
+    _raise_if((_marshal or _native()).grad_norm(grads, norm, workspace, None if stream is None else stream.cuda_stream,
+                                                _raw_current))
+    return norm
+
+
+def echo_clip_grads(grads: Sequence, max_norm: float, norm, out: Sequence = None, workspace=None, stream=None):
+    """norm = the norm of all elements of ``grads``, and every tensor times min(1,
+    max_norm / (norm + 1e-6)), into ``out`` (tensors like the gradients) or in place."""
+    _raise_if((_marshal or _native()).clip_grads(grads, norm, workspace, out, max_norm,
+                                                 None if stream is None else stream.cuda_stream, _raw_current))
+    return norm
+
+
+def echo_embed(tables: Sequence, tokens, out: Sequence, scale: float = 1.0, first: int = 0, stream=None):
+    """out[r][t] = scale * tables[r][tokens[t] - first - r * rows] where that row is in
+    the table, zeros elsewhere: the partial embeddings of ranks that hold consecutive
+    stretches of ``rows`` of the vocabulary.  Tokens int64 or int32 of any shape; out[r]
+    [number of tokens, cols]."""
+    _raise_if((_marshal or _native()).embed(tables, tokens, out, scale, first,
+                                            None if stream is None else stream.cuda_stream, _raw_current))
+    return out
+
+
+def echo_embed_workspace(n_tokens: int, cols: int) -> int:
+    """Bytes of workspace of echo_embed_backward."""
+    return int(load_library().echo_embed_workspace(n_tokens, cols))
+
+
+def echo_embed_backward(dout, tokens, dtables: Sequence, scale: float = 1.0, first: int = 0, workspace=None, stream=None):
+    """dtables[r] = the gradient of tables[r] under the gradient ``dout`` [number of
+    tokens, cols] of the sum of the partials; rows without a token become zeros.
+    ``workspace`` as for echo_block_norm_backward."""
+    _raise_if((_marshal or _native()).embed_backward(dout, tokens, dtables, scale, first, workspace,
+                                                     None if stream is None else stream.cuda_stream, _raw_current))
+    return dtables

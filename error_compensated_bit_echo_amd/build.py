@@ -19,9 +19,11 @@ INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libecho.so")
 SOURCES = ["echo_kernels.hip"] + [f"echo_owner_p{lo}_{lo + 1}.hip" for lo in range(1, 17, 2)] + \
     ["echo_gemm.hip", "echo_scratch.hip", "echo_api.hip",
-     "echo_fp8_quant.hip", "echo_fp8_gemm.hip", "echo_dropout.hip", "echo_layer_api.hip"]
+     "echo_fp8_quant.hip", "echo_fp8_gemm.hip", "echo_dropout.hip", "echo_layer_api.hip",
+     "echo_block_norm.hip", "echo_block_norm_bwd.hip", "echo_clip.hip", "echo_embed.hip", "echo_embed_bwd.hip", "echo_step_api.hip"]
 HEADERS = ["echo_internal.h", "echo_div7.h", "echo_quant.h", "echo_device.h", "echo_owner.h",
-           "echo_layer_internal.h", "echo_elem.h", "echo_slab.h"]
+           "echo_layer_internal.h", "echo_elem.h", "echo_slab.h",
+           "echo_layer_check.h", "echo_step_internal.h", "echo_row.h"]
 ARCH = "gfx950"
 
 # -ffp-contract=off: every multiply and add is its own IEEE operation (the

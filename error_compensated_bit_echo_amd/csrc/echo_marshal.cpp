@@ -9,9 +9,11 @@
 #include <Python.h>
 
 #include <hip/hip_runtime_api.h>
+#include <ATen/ops/empty.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <string>
+#include <vector>
 
 #include "echo.h"
 
@@ -314,10 +316,315 @@ PyObject* dropout_add(PyObject*, PyObject* const* args, Py_ssize_t n) {
   });
 }
 
+// ---- operators of a training step around the blocks -------------------------------
+
+const at::Tensor* optional_tensor(PyObject* o, const char* what) { return o == Py_None ? nullptr : &tensor(o, what); }
+
+// Where a tensor lies.  One without elements lies nowhere: an address that is never used
+// says that it was given.
+void* address(const at::Tensor& t) {
+  alignas(16) static char given;
+  return t.numel() > 0 ? t.data_ptr() : &given;
+}
+
+// A tensor of x's shape on the call's GPU, or none.
+struct RowsOf {
+  void* p = nullptr;
+  int64_t ld = 0;
+  int32_t type = ECHO_F32;
+};
+
+RowsOf rows_like(const at::Tensor* t, const at::Tensor& like, Device* dev, int64_t* rows, int64_t* cols, const char* what) {
+  RowsOf r;
+  if (t == nullptr) return r;
+  dev->on(*t, what);
+  row_layout(*t, like, rows, cols, &r.ld, what);
+  r.p = address(*t);
+  r.type = elem_type(t->scalar_type(), what);
+  return r;
+}
+
+// A vector of `cols` elements of the parameters' type, or none.
+void* weight(const at::Tensor* t, int64_t cols, at::ScalarType* type, Device* dev, const char* what) {
+  if (t == nullptr) return nullptr;
+  dev->on(*t, what);
+  if (t->layout() != at::kStrided || t->dim() != 1 || t->size(0) != cols || !t->is_contiguous())
+    refuse(ECHO_ERR_ARG, std::string(what) + ": a contiguous vector as long as the rows expected");
+  if (*type != at::ScalarType::Undefined && *type != t->scalar_type())
+    refuse(ECHO_ERR_DTYPE, "the gate, the weights and their gradients must be of one type");
+  *type = t->scalar_type();
+  return t->data_ptr();
+}
+
+// A gate [cols] or [gate_rows, cols] with contiguous rows, or none.
+void* gate_of(const at::Tensor* t, int64_t cols, int64_t* rows, int64_t* ld, at::ScalarType* type, Device* dev,
+              const char* what) {
+  if (t == nullptr) return nullptr;
+  dev->on(*t, what);
+  if (t->layout() != at::kStrided || t->dim() < 1 || t->dim() > 2 || t->size(-1) != cols || (cols > 1 && t->stride(-1) != 1))
+    refuse(ECHO_ERR_ARG, std::string(what) + ": a vector or matrix with contiguous rows as long as x's expected");
+  if (*type != at::ScalarType::Undefined && *type != t->scalar_type())
+    refuse(ECHO_ERR_DTYPE, "the gate, the weights and their gradients must be of one type");
+  *type = t->scalar_type();
+  *rows = t->dim() == 2 ? t->size(0) : 1;
+  *ld = t->dim() == 2 ? t->stride(0) : cols;
+  return t->data_ptr();
+}
+
+double number(PyObject* o) {
+  const double v = PyFloat_AsDouble(o);
+  if (v == -1.0 && PyErr_Occurred()) throw Raised{};
+  return v;
+}
+
+bool truth(PyObject* o) {
+  const int v = PyObject_IsTrue(o);
+  if (v < 0) throw Raised{};
+  return v != 0;
+}
+
+// The caller's workspace, or one from torch's allocator for this call (`owned`): freed to
+// the stream that is current, so only for calls on that stream.
+void* workspace_of(PyObject* given, PyObject* stream, size_t need, const Device& dev, at::Tensor* owned, size_t* bytes) {
+  *bytes = 0;
+  if (given != Py_None) {
+    const at::Tensor& t = tensor(given, "workspace");
+    if (t.scalar_type() != at::kByte || !t.is_contiguous() || !t.device().is_cuda() || t.device().index() != dev.index)
+      refuse(ECHO_ERR_ARG, "workspace: a contiguous uint8 tensor on the tensors' GPU expected");
+    *bytes = static_cast<size_t>(t.numel());
+    return t.numel() > 0 ? t.data_ptr() : nullptr;
+  }
+  if (need == 0) return nullptr;
+  if (stream != Py_None) refuse(ECHO_ERR_WORKSPACE, "a call on a stream of its own takes the caller's workspace");
+  *owned = at::empty({static_cast<int64_t>(need)}, at::TensorOptions().dtype(at::kByte).device(
+                                                       at::Device(at::kCUDA, static_cast<c10::DeviceIndex>(dev.index))));
+  *bytes = need;
+  return owned->data_ptr();
+}
+
+struct Block {
+  echo_block c{};
+  int64_t rows = 0, cols = 0;
+  at::ScalarType params = at::ScalarType::Undefined;
+};
+
+// args: gate, w_post, w_pre, post_norm, residual_scale, weight_offset, eps
+void block_params(Block* b, PyObject* const* args, Device* dev) {
+  b->c.gate = gate_of(optional_tensor(args[0], "gate"), b->cols, &b->c.gate_rows, &b->c.ld_gate, &b->params, dev, "gate");
+  b->c.w_post = weight(optional_tensor(args[1], "w_post"), b->cols, &b->params, dev, "w_post");
+  b->c.w_pre = weight(optional_tensor(args[2], "w_pre"), b->cols, &b->params, dev, "w_pre");
+  b->c.post_norm = truth(args[3]);
+  b->c.residual_scale = number(args[4]);
+  b->c.weight_offset = number(args[5]);
+  b->c.eps = number(args[6]);
+  b->c.rows = b->rows;
+  b->c.cols = b->cols;
+  b->c.param_dtype = b->params == at::ScalarType::Undefined ? ECHO_F32 : elem_type(b->params, "weights");
+}
+
+// (x, out or None, a or None, y or None, gate, w_post, w_pre, post_norm, residual_scale, weight_offset, eps, stream, current)
+PyObject* block_norm(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  if (!arguments(n, 13)) return nullptr;
+  return guarded([&]() -> PyObject* {
+    const at::Tensor& x = tensor(args[0], "x");
+    Device dev;
+    Block b;
+    const RowsOf mx = rows_like(&x, x, &dev, &b.rows, &b.cols, "x");
+    const RowsOf mo = rows_like(optional_tensor(args[1], "out"), x, &dev, &b.rows, &b.cols, "out");
+    const RowsOf ma = rows_like(optional_tensor(args[2], "a"), x, &dev, &b.rows, &b.cols, "a");
+    const RowsOf my = rows_like(optional_tensor(args[3], "y"), x, &dev, &b.rows, &b.cols, "y");
+    if (args[1] != Py_None && mo.type != mx.type) refuse(ECHO_ERR_DTYPE, "x and out must be of one type");
+    block_params(&b, args + 4, &dev);
+    b.c.x_dtype = mx.type;
+    b.c.y_dtype = args[3] != Py_None ? my.type : mx.type;
+    b.c.a_dtype = args[2] != Py_None ? ma.type : mx.type;
+    const OnDevice on(dev.index);
+    return answer(echo_block_norm(&b.c, mx.p, mx.ld, my.p, my.ld, mo.p, mo.ld, ma.p, ma.ld,
+                                  stream_of(args[11], args[12], dev.index)),
+                  "echo_block_norm");
+  });
+}
+
+// (out, dout, da, dx, y, dy, dgate, dw_post, dw_pre, gate, w_post, w_pre, post_norm, residual_scale, weight_offset, eps,
+// workspace, stream, current)
+PyObject* block_norm_backward(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  if (!arguments(n, 19)) return nullptr;
+  return guarded([&]() -> PyObject* {
+    const at::Tensor& out = tensor(args[0], "out");
+    Device dev;
+    Block b;
+    const auto rows = [&](int i, const char* what) {
+      return rows_like(optional_tensor(args[i], what), out, &dev, &b.rows, &b.cols, what);
+    };
+    const RowsOf mo = rows(0, "out"), mdo = rows(1, "dout"), mda = rows(2, "da"), mdx = rows(3, "dx"), my = rows(4, "y"),
+                 mdy = rows(5, "dy");
+    if ((mdo.p != nullptr && mdo.type != mo.type) || (mdx.p != nullptr && mdx.type != mo.type) ||
+        (mdy.p != nullptr && my.p != nullptr && mdy.type != my.type))
+      refuse(ECHO_ERR_DTYPE, "a gradient must be of the type of what it is the gradient of");
+    block_params(&b, args + 9, &dev);
+    int64_t gate_rows = b.c.gate_rows, ldg = 0;
+    void* dgate = gate_of(optional_tensor(args[6], "dgate"), b.cols, &gate_rows, &ldg, &b.params, &dev, "dgate");
+    if (dgate != nullptr && gate_rows != b.c.gate_rows) refuse(ECHO_ERR_ARG, "dgate: the gate's shape expected");
+    void* dw_post = weight(optional_tensor(args[7], "dw_post"), b.cols, &b.params, &dev, "dw_post");
+    void* dw_pre = weight(optional_tensor(args[8], "dw_pre"), b.cols, &b.params, &dev, "dw_pre");
+    b.c.x_dtype = mo.type;
+    b.c.y_dtype = args[4] != Py_None ? my.type : mo.type;
+    b.c.a_dtype = args[2] != Py_None ? mda.type : mo.type;
+    const OnDevice on(dev.index);
+    at::Tensor owned;
+    size_t bytes = 0;
+    const bool sums = dgate != nullptr || dw_post != nullptr || dw_pre != nullptr;
+    const size_t need = sums ? echo_block_norm_workspace(b.rows, b.cols, b.c.gate != nullptr ? b.c.gate_rows : 0) : 0;
+    void* ws = workspace_of(args[16], args[17], need, dev, &owned, &bytes);
+    return answer(echo_block_norm_backward(&b.c, mo.p, mo.ld, my.p, my.ld, mdo.p, mdo.ld, mda.p, mda.ld, mdx.p, mdx.ld,
+                                           mdy.p, mdy.ld, dgate, ldg, dw_post, dw_pre, ws, bytes,
+                                           stream_of(args[17], args[18], dev.index)),
+                  "echo_block_norm_backward");
+  });
+}
+
+// Pointers, lengths and types of a list of tensors.
+struct Tensors {
+  std::vector<void*> p;
+  std::vector<int64_t> n;
+  std::vector<int32_t> type;
+};
+
+void tensor_list(Tensors* l, const Items& x, Device* dev, const char* what) {
+  const size_t n = static_cast<size_t>(x.size());
+  l->p.reserve(n);
+  l->n.reserve(n);
+  l->type.reserve(n);
+  for (size_t i = 0; i < n; ++i) {
+    const at::Tensor& t = tensor(x[static_cast<Py_ssize_t>(i)], what);
+    dev->on(t, what);
+    if (t.layout() != at::kStrided || !t.is_non_overlapping_and_dense())
+      refuse(ECHO_ERR_ARG, std::string(what) + " must be tensors whose elements lie together");
+    l->p.push_back(t.data_ptr());
+    l->n.push_back(t.numel());
+    l->type.push_back(elem_type(t.scalar_type(), what));
+  }
+}
+
+// (grads, norm, workspace, stream, current), or (grads, norm, workspace, out or None, max_norm, stream, current)
+PyObject* clip(PyObject* const* args, bool scale) {
+  return guarded([&]() -> PyObject* {
+    const Items G(args[0], "grads");
+    const at::Tensor& norm = tensor(args[1], "norm");
+    PyObject *stream = args[scale ? 5 : 3], *current = args[scale ? 6 : 4];
+    Device dev;
+    dev.on(norm, "norm");
+    if (norm.scalar_type() != at::kFloat || norm.numel() != 1) refuse(ECHO_ERR_ARG, "norm: one element of float32 expected");
+    Tensors g, o;
+    tensor_list(&g, G, &dev, "grads");
+    const int64_t count = static_cast<int64_t>(g.p.size());
+    if (scale && args[3] != Py_None) {
+      const Items O(args[3], "out");
+      if (O.size() != G.size()) refuse(ECHO_ERR_ARG, "out: as many tensors as gradients expected");
+      tensor_list(&o, O, &dev, "out");
+      for (Py_ssize_t i = 0; i < O.size(); ++i) {
+        const at::Tensor &a = tensor(G[i], "grads"), &b = tensor(O[i], "out");
+        if (a.scalar_type() != b.scalar_type() || a.sizes() != b.sizes() || (a.numel() > 1 && a.strides() != b.strides()))
+          refuse(ECHO_ERR_ARG, "out: tensors like the gradients expected");
+      }
+    }
+    const OnDevice on(dev.index);
+    at::Tensor owned;
+    size_t bytes = 0;
+    void* ws = workspace_of(args[2], stream, echo_clip_workspace(count), dev, &owned, &bytes);
+    float* to = static_cast<float*>(norm.data_ptr());
+    const echo_stream_t s = stream_of(stream, current, dev.index);
+    if (!scale)
+      return answer(echo_grad_norm(g.p.data(), g.n.data(), g.type.data(), count, to, ws, bytes, s), "echo_grad_norm");
+    return answer(echo_clip_grads(g.p.data(), (args[3] != Py_None ? o : g).p.data(), g.n.data(), g.type.data(), count,
+                                  number(args[4]), to, ws, bytes, s),
+                  "echo_clip_grads");
+  });
+}
+
+PyObject* grad_norm(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  return arguments(n, 5) ? clip(args, false) : nullptr;
+}
+
+PyObject* clip_grads(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  return arguments(n, 7) ? clip(args, true) : nullptr;
+}
+
+// Token ids of any shape, contiguous.
+int32_t token_bytes(const at::Tensor& t, Device* dev) {
+  dev->on(t, "tokens");
+  if (t.scalar_type() != at::kLong && t.scalar_type() != at::kInt) refuse(ECHO_ERR_DTYPE, "tokens: int64 or int32 expected");
+  if (t.layout() != at::kStrided || !t.is_contiguous()) refuse(ECHO_ERR_ARG, "tokens must be contiguous");
+  return t.scalar_type() == at::kLong ? 8 : 4;
+}
+
+int64_t whole(PyObject* o) {
+  const long long v = PyLong_AsLongLong(o);
+  if (v == -1 && PyErr_Occurred()) throw Raised{};
+  return v;
+}
+
+// (tables, tokens, out, scale, first, stream, current)
+PyObject* embed(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  if (!arguments(n, 7)) return nullptr;
+  return guarded([&]() -> PyObject* {
+    const Items E(args[0], "tables"), O(args[2], "out");
+    const int P = ranks(E, "tables");
+    const at::Tensor& tokens = tensor(args[1], "tokens");
+    Device dev;
+    const Mats e = matrices(E, P, &dev, "tables"), o = matrices(O, P, &dev, "out");
+    const int32_t wide = token_bytes(tokens, &dev);
+    if (o.rows != tokens.numel() || o.cols != e.cols)
+      refuse(ECHO_ERR_ARG, "out must be [" + std::to_string(tokens.numel()) + ", " + std::to_string(e.cols) + "]");
+    const OnDevice on(dev.index);
+    return answer(echo_embed(e.ptr, tokens.data_ptr(), o.ptr, P, e.rows, e.cols, e.s0, o.rows, o.s0, elem_type(e.type, "tables"),
+                             elem_type(o.type, "out"), wide, whole(args[4]), number(args[3]),
+                             stream_of(args[5], args[6], dev.index)),
+                  "echo_embed");
+  });
+}
+
+// (dout, tokens, dtables, scale, first, workspace, stream, current)
+PyObject* embed_backward(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  if (!arguments(n, 8)) return nullptr;
+  return guarded([&]() -> PyObject* {
+    const Items E(args[2], "dtables");
+    const int P = ranks(E, "dtables");
+    const at::Tensor &dout = tensor(args[0], "dout"), &tokens = tensor(args[1], "tokens");
+    Device dev;
+    const Mats e = matrices(E, P, &dev, "dtables");
+    const int32_t wide = token_bytes(tokens, &dev);
+    Mats d;
+    take(&d, 0, dout, &dev, "dout");
+    if (d.cols > 1 && d.s1 != 1) refuse(ECHO_ERR_ARG, "dout must have contiguous rows");
+    if (d.rows != tokens.numel() || d.cols != e.cols)
+      refuse(ECHO_ERR_ARG, "dout must be [" + std::to_string(tokens.numel()) + ", " + std::to_string(e.cols) + "]");
+    const OnDevice on(dev.index);
+    at::Tensor owned;
+    size_t bytes = 0;
+    void* ws = workspace_of(args[5], args[6], echo_embed_workspace(d.rows, d.cols), dev, &owned, &bytes);
+    return answer(echo_embed_backward(d.ptr[0], tokens.data_ptr(), e.ptr, P, e.rows, e.cols, e.s0, d.rows, d.s0,
+                                      elem_type(d.type, "dout"), elem_type(e.type, "dtables"), wide, whole(args[4]),
+                                      number(args[3]), ws, bytes, stream_of(args[6], args[7], dev.index)),
+                  "echo_embed_backward");
+  });
+}
+
+template <PyObject* (*F)(PyObject*, PyObject* const*, Py_ssize_t)>
+PyMethodDef method(const char* name) {
+  return {name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(F)), METH_FASTCALL, nullptr};
+}
+
 PyMethodDef methods[] = {
-    {"quantize_fp8", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(quantize_fp8)), METH_FASTCALL, nullptr},
-    {"gemm_fp8", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(gemm_fp8)), METH_FASTCALL, nullptr},
-    {"dropout_add", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(dropout_add)), METH_FASTCALL, nullptr},
+    method<quantize_fp8>("quantize_fp8"),
+    method<gemm_fp8>("gemm_fp8"),
+    method<dropout_add>("dropout_add"),
+    method<block_norm>("block_norm"),
+    method<block_norm_backward>("block_norm_backward"),
+    method<grad_norm>("grad_norm"),
+    method<clip_grads>("clip_grads"),
+    method<embed>("embed"),
+    method<embed_backward>("embed_backward"),
     {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef module_def = {PyModuleDef_HEAD_INIT, "_echo_marshal", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};

@@ -1,0 +1,164 @@
+// What the row-wise kernels of the training step share: sums over a wavefront and a
+// workgroup, rows cut into chunks of 8 columns, element types known at run time.
+#pragma once
+
+#pragma clang fp contract(off)
+
+#include "echo_elem.h"
+#include "echo_step_internal.h"
+
+namespace echo {
+namespace {
+
+constexpr int kMaxThreads = 1024;
+constexpr int kMaxWaves = kMaxThreads / 64;
+
+template <int CTRL>
+__device__ __forceinline__ float dpp(float v) {
+  return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, 0xF, 0xF, true));
+}
+
+// The sum over the wavefront's 64 lanes, in every lane: four exchanges within rows of 16
+// lanes, then the four rows' sums through scalar registers.  All lanes are active.
+__device__ __forceinline__ float wave_sum(float v) {
+  v = v + dpp<0xB1>(v);   // quad_perm [1, 0, 3, 2]
+  v = v + dpp<0x4E>(v);   // quad_perm [2, 3, 0, 1]
+  v = v + dpp<0x141>(v);  // row_half_mirror
+  v = v + dpp<0x140>(v);  // row_mirror
+  const int b = __float_as_int(v);
+  return (__int_as_float(__builtin_amdgcn_readlane(b, 0)) + __int_as_float(__builtin_amdgcn_readlane(b, 16))) +
+         (__int_as_float(__builtin_amdgcn_readlane(b, 32)) + __int_as_float(__builtin_amdgcn_readlane(b, 48)));
+}
+
+// Sums of N values over the workgroup, in every thread.  Consecutive calls alternate
+// between two slots: a slot is written again only behind the barrier of the call between,
+// which every thread reaches after it has read it.
+template <int N>
+struct Slots {
+  float v[2][N][kMaxWaves];
+};
+
+template <int N, int M>
+__device__ __forceinline__ void block_sums(float (&v)[N], Slots<M>* lds, int* turn) {
+  static_assert(N <= M, "slots");
+  const int waves = static_cast<int>(blockDim.x) >> 6;
+#pragma unroll
+  for (int i = 0; i < N; ++i) v[i] = wave_sum(v[i]);
+  if (waves == 1) return;
+  const int slot = *turn;
+  *turn ^= 1;
+  const int wave = static_cast<int>(threadIdx.x) >> 6, lane = static_cast<int>(threadIdx.x) & 63;
+  if (lane == 0) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) lds->v[slot][i][wave] = v[i];
+  }
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    // up to 16 wavefronts: a row of 16 lanes holds their sums, every row the same
+    float w = (lane & 15) < waves ? lds->v[slot][i][lane & 15] : 0.0f;
+    w = w + dpp<0xB1>(w);
+    w = w + dpp<0x4E>(w);
+    w = w + dpp<0x141>(w);
+    v[i] = w + dpp<0x140>(w);
+  }
+}
+
+// A run of up to 8 columns: n of them lie in the row.
+template <int E>
+__device__ __forceinline__ void load_run(const void* base, int64_t at, int n, float v[8]) {
+  if (n >= 8) {
+    load8<E>(base, at, v);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = i < n ? load1<E>(base, at + i) : 0.0f;
+  }
+}
+
+template <int E>
+__device__ __forceinline__ void store_run(void* base, int64_t at, int n, const float v[8]) {
+  if (n >= 8) {
+    store8<E>(base, at, v);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i < n) store1<E>(base, at + i, v[i]);
+  }
+}
+
+// The same where the type is an argument of the launch.
+__device__ __forceinline__ void load_run(int elem, const void* base, int64_t at, int n, float v[8]) {
+  if (elem == kElemF32) load_run<kElemF32>(base, at, n, v);
+  else if (elem == kElemBf16) load_run<kElemBf16>(base, at, n, v);
+  else load_run<kElemF16>(base, at, n, v);
+}
+
+__device__ __forceinline__ void store_run(int elem, void* base, int64_t at, int n, const float v[8]) {
+  if (elem == kElemF32) store_run<kElemF32>(base, at, n, v);
+  else if (elem == kElemBf16) store_run<kElemBf16>(base, at, n, v);
+  else store_run<kElemF16>(base, at, n, v);
+}
+
+// v as it reads back from an element of the type.
+template <int E>
+__device__ __forceinline__ float stored(float v) {
+  return static_cast<float>(narrow<E>(v));
+}
+
+__device__ __forceinline__ float sum8(const float v[8]) {
+  return ((v[0] + v[1]) + (v[2] + v[3])) + ((v[4] + v[5]) + (v[6] + v[7]));
+}
+
+// The columns of a row that a thread's run i of `runs` holds: consecutive threads take
+// consecutive runs of 8.
+__device__ __forceinline__ int64_t run_at(int64_t i) {
+  return (i * blockDim.x + threadIdx.x) * 8;
+}
+__device__ __forceinline__ int run_length(int64_t at, int64_t C) {
+  const int64_t n = C - at;
+  return n >= 8 ? 8 : n > 0 ? static_cast<int>(n) : 0;
+}
+
+// The factor of a norm's weight: offset + w, 1 without a weight.
+__device__ __forceinline__ void load_weight(const BlockParams& p, const void* w, int64_t at, int n, float v[8]) {
+  if (w == nullptr) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = 1.0f;
+    return;
+  }
+  load_run(p.elem, w, at, n, v);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = v[i] + p.offset;
+}
+
+// 1 / sqrt(mean of the squares + eps)
+__device__ __forceinline__ float reciprocal_rms(float squares, const BlockParams& p) {
+  return 1.0f / sqrtf(squares / static_cast<float>(p.C) + p.eps);
+}
+
+}  // namespace
+
+// Threads for rows of C columns, 8 * `runs` of them to a thread.
+inline int row_threads(int64_t C, int runs) {
+  const int64_t t = (C + 8 * runs - 1) / (8 * runs);
+  return static_cast<int>(t >= kMaxThreads ? kMaxThreads : (t + 63) / 64 * 64);
+}
+
+// Calls f with the three types as constants; bfloat16 and fp16 do not come together.
+template <typename F>
+hipError_t with_types(Elem x, Elem y, Elem a, F f) {
+#define ECHO_TYPES(X, Y, A)                                            \
+  if (x == X && y == Y && a == A)                                      \
+    return f(std::integral_constant<int, X>{}, std::integral_constant<int, Y>{}, std::integral_constant<int, A>{});
+#define ECHO_TYPES_WITH(H)                                                                              \
+  ECHO_TYPES(H, H, H) ECHO_TYPES(H, H, kElemF32) ECHO_TYPES(H, kElemF32, H) ECHO_TYPES(H, kElemF32, kElemF32) \
+  ECHO_TYPES(kElemF32, H, H) ECHO_TYPES(kElemF32, H, kElemF32) ECHO_TYPES(kElemF32, kElemF32, H)
+  ECHO_TYPES_WITH(kElemBf16)
+  ECHO_TYPES_WITH(kElemF16)
+  ECHO_TYPES(kElemF32, kElemF32, kElemF32)
+#undef ECHO_TYPES_WITH
+#undef ECHO_TYPES
+  return hipErrorInvalidValue;
+}
+
+}  // namespace echo

@@ -417,6 +417,148 @@ echo_status echo_dropout_add(const void* x, const void* residual, void* out, int
                              double p, const int64_t* rng, int64_t offset, int64_t first,
                              echo_stream_t stream);
 
+/* ---- operators of a training step around the blocks -------------------------
+ * What a step of a tensor-parallel stack runs before, between and after the
+ * blocks whose partial results the all-reduce adds: the norms with the residual
+ * add, the gradients' common norm, and the embedding whose vocabulary is split
+ * over the ranks.  The conventions of the layer operators hold (tensors on the
+ * device that is current at the call, stream order, validation before any
+ * launch, no allocation on the device), but a call may launch several kernels
+ * and some take a workspace, which the caller owns and which one call at a time
+ * may use.  fp32 goes with either 16-bit type in one call; bfloat16 and fp16 do
+ * not go together (ECHO_ERR_DTYPE), except in the list of a clipping call.
+ * Results do not depend on timing; non-finite values are specified. */
+
+/* The end of one block and the start of the next, for a residual stream x and
+ * the block's reduced output y, both [rows, cols]:
+ *   n   = y * rs(y) * (weight_offset + w_post) with post_norm, else y
+ *   out = residual_scale * x + gate * n
+ *   a   = out * rs(out) * (weight_offset + w_pre)
+ * rs(v) = 1 / sqrt(mean of v^2 over the row + eps).  A factor whose weight is
+ * NULL is 1 (weight_offset goes with a weight only).  gate: [gate_rows, cols],
+ * row i of the matrices takes row i / (rows / gate_rows): 1 for a learned gate
+ * of the layer, the number of sequences for one each, rows for one per token.
+ * Without y, out is x, and post_norm 0, gate and w_post NULL and residual_scale
+ * 1 are asked for. */
+typedef struct {
+  int64_t rows, cols;     /* rows: at most 2^31 - 1, cols: 2^22, product: 2^40 */
+  const void* gate;       /* [gate_rows, cols], or NULL                        */
+  int64_t ld_gate;        /* elements between its rows                         */
+  int64_t gate_rows;      /* at least 1, divides rows                          */
+  const void* w_post;     /* [cols], or NULL                                   */
+  const void* w_pre;      /* [cols], or NULL                                   */
+  double residual_scale;  /* finite                                            */
+  double weight_offset;   /* finite; 1 for weights stored as deviations from 1 */
+  double eps;             /* at least 2^-126                                   */
+  int32_t x_dtype;        /* the stream: x and out                             */
+  int32_t y_dtype;        /* the block's output                                */
+  int32_t a_dtype;        /* the next block's input                            */
+  int32_t param_dtype;    /* gate, w_post, w_pre                               */
+  int32_t post_norm;      /* 0 or 1                                            */
+} echo_block;
+
+/* Source: none on the pages (the norms and the residual add around the blocks
+ * that «Почему обычное 4-битное суммирование портит модель» reduces).
+ * out and a as echo_block says, in one pass.  y and out: both or neither; a NULL:
+ * not wanted (w_pre is NULL then).  Sums and products are fp32 operations (a
+ * row's mean square has to be below 2^128); out and a are rounded once each, and
+ * a starts from out as it is stored, so that the norm of the stored stream gives
+ * the same.  A NaN makes its row of out (where y has a post-norm) and of a NaN;
+ * an infinity gives NaN in its own place and 0 in the others.
+ * ld*: elements between rows, any alignment of the element type.  out may be x
+ * itself (same pointer and pitch); outputs overlap nothing else.  One launch.
+ * Errors: ECHO_ERR_ARG (null or misaligned pointer, parameters without y, an
+ * overlap), ECHO_ERR_SHAPE, ECHO_ERR_DTYPE, ECHO_ERR_HIP. */
+echo_status echo_block_norm(const echo_block* b, const void* x, int64_t ldx, const void* y, int64_t ldy, void* out,
+                            int64_t ldo, void* a, int64_t lda, echo_stream_t stream);
+
+/* Source: none on the pages (host bookkeeping).
+ * Bytes of workspace of echo_block_norm_backward where it gives gradients of
+ * parameters; gate_rows 0 without a gate.  0 for sizes that it refuses. */
+size_t echo_block_norm_workspace(int64_t rows, int64_t cols, int64_t gate_rows);
+
+/* Source: none on the pages (the backward pass of echo_block_norm).
+ * From out as the forward pass stored it (x where there is no y), y, and the
+ * gradients dout of out and da of a (either NULL: 0): dx, dy, dgate, dw_post and
+ * dw_pre (each NULL: not wanted), of the types and shapes of what they are
+ * gradients of.  With t the whole gradient of out,
+ *   u = da (weight_offset + w_pre),  t = dout + rs u - out rs^3 mean(u out),  rs = rs(out)
+ *   dx = residual_scale t,  dn = gate t,  dgate = sum of t n over the gate's rows
+ *   v = dn (weight_offset + w_post),  dy = ry v - y ry^3 mean(v y),  ry = rs(y)
+ *   dw_post = sum of dn y ry,  dw_pre = sum of da out rs over the rows.
+ * Sums over rows are fp32, in an order that the sizes fix; every output is
+ * rounded once.  dx may be dout itself.  With no rows, gradients of parameters
+ * are zeros.  workspace: echo_block_norm_workspace bytes, 16-byte aligned, NULL
+ * where only dx and dy are wanted.  At most two launches.  Errors as above, and
+ * ECHO_ERR_WORKSPACE. */
+echo_status echo_block_norm_backward(const echo_block* b, const void* out, int64_t ldo, const void* y, int64_t ldy,
+                                     const void* dout, int64_t lddo, const void* da, int64_t ldda, void* dx, int64_t lddx,
+                                     void* dy, int64_t lddy, void* dgate, int64_t ld_dgate, void* dw_post, void* dw_pre,
+                                     void* workspace, size_t workspace_bytes, echo_stream_t stream);
+
+/* Source: none on the pages (host bookkeeping).
+ * Bytes of workspace of echo_grad_norm and echo_clip_grads. */
+size_t echo_clip_workspace(int64_t n_tensors);
+
+/* Source: none on the pages (the gradients of the weights that a training step's
+ * backward pass leaves).
+ * *norm (device, fp32) = sqrt of the sum of squares of all elements of n_tensors
+ * contiguous tensors (numel and dtypes: host arrays; fp32, bfloat16 and fp16 in
+ * any mix, any alignment of the element type, lengths of 0 allowed).  Squares and
+ * sums are held in 64 bits, in an order that the lengths fix.  norm lies in none
+ * of the tensors; tensors may overlap each other.
+ * n_tensors: at most 2^24; numel: 2^40; below 2^31 chunks of 16384 elements in
+ * all.  workspace: 8-byte aligned.  A launch for every 120 tensors, and one more.
+ * Errors: ECHO_ERR_ARG, ECHO_ERR_SHAPE, ECHO_ERR_DTYPE, ECHO_ERR_WORKSPACE (also
+ * where the host has no memory for the check of overlaps), ECHO_ERR_HIP. */
+echo_status echo_grad_norm(const void* const* grads, const int64_t* numel, const int32_t* dtypes, int64_t n_tensors,
+                           float* norm, void* workspace, size_t workspace_bytes, echo_stream_t stream);
+
+/* Source: none on the pages (clipping before the optimizer's step).
+ * *norm as echo_grad_norm gives it, and out_i = g_i * f for every tensor, f =
+ * fp32(min(1, max_norm / (norm + 1e-6))) with the norm in 64 bits; the product is
+ * an fp32 operation, rounded once to the tensor's type.  An infinite norm gives f
+ * = 0 (and NaN where the element is infinite), a NaN makes every element NaN.
+ * out_i may be g_i itself (it is not touched then where f is 1) and overlaps no
+ * other tensor.  max_norm: finite, at least 0.  Two launches for every 120
+ * tensors.  Limits, workspace and errors as above. */
+echo_status echo_clip_grads(const void* const* grads, void* const* out, const int64_t* numel, const int32_t* dtypes,
+                            int64_t n_tensors, double max_norm, float* norm, void* workspace, size_t workspace_bytes,
+                            echo_stream_t stream);
+
+/* Source: none on the pages (the embedding before the blocks; its partials are
+ * added by the same all-reduce).
+ * out_r[t] = scale * table_r[tokens[t] - first - r * rows] for every rank r of P
+ * where that row is in [0, rows), a row of zeros elsewhere: table_r [rows, cols]
+ * (ldt elements between rows) holds the r-th stretch of the vocabulary, so that
+ * the sum over all ranks is the embedding.  Tokens: n_tokens integers of
+ * token_bytes 4 or 8, any value.  out_r [n_tokens, cols] (ldo elements between
+ * rows).  The product is an fp32 operation, rounded once to out_dtype.
+ * rows: P * rows at most 2^31 - 2; cols at most 2^22; n_tokens at most 2^27;
+ * 0 <= first <= 2^62; scale finite.  Outputs overlap nothing.  One launch.
+ * Errors: ECHO_ERR_ARG, ECHO_ERR_SHAPE, ECHO_ERR_DTYPE, ECHO_ERR_HIP. */
+echo_status echo_embed(const void* const* tables, const void* tokens, void* const* out, int32_t P, int64_t rows,
+                       int64_t cols, int64_t ldt, int64_t n_tokens, int64_t ldo, int32_t table_dtype, int32_t out_dtype,
+                       int32_t token_bytes, int64_t first, double scale, echo_stream_t stream);
+
+/* Source: none on the pages (host bookkeeping).
+ * Bytes of workspace of echo_embed_backward. */
+size_t echo_embed_workspace(int64_t n_tokens, int64_t cols);
+
+/* Source: none on the pages (the backward pass of echo_embed).
+ * dtable_r[v] = scale * (sum of dout[t] over the tokens t with tokens[t] - first
+ * - r * rows = v), zeros for rows without a token; all of every dtable_r is
+ * written.  dout [n_tokens, cols] of out_dtype (lddo elements between rows), the
+ * gradient of the sum over ranks.  Sums are fp32, over rising t within stretches
+ * whose length the sizes fix, then over the stretches; they are rounded once,
+ * after the scale.  Limits as for echo_embed.
+ * workspace: echo_embed_workspace bytes, 256-byte aligned.  Errors as above, and
+ * ECHO_ERR_WORKSPACE. */
+echo_status echo_embed_backward(const void* dout, const void* tokens, void* const* dtables, int32_t P, int64_t rows,
+                                int64_t cols, int64_t ldt, int64_t n_tokens, int64_t lddo, int32_t out_dtype,
+                                int32_t table_dtype, int32_t token_bytes, int64_t first, double scale, void* workspace,
+                                size_t workspace_bytes, echo_stream_t stream);
+
 /* Source: none on the pages (error reporting of this library).
  * Static description of a status code. */
 const char* echo_status_str(echo_status s);
