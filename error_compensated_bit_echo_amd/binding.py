@@ -558,7 +558,7 @@ def echo_block_norm(x, out=None, a=None, *, y=None, gate=None, w_post=None, w_pr
 
 
 def echo_block_norm_workspace(rows: int, cols: int, gate_rows: int = 0) -> int:
-    """Bytes of workspace of echo_block_norm_backward with gradients of parameters."""
+    """Bytes of workspace of echo_block_norm_backward."""
     return int(load_library().echo_block_norm_workspace(rows, cols, gate_rows))
 
 

@@ -12,83 +12,107 @@
 namespace echo {
 namespace {
 
-template <int X, int Y, int A, int RUNS>
-__global__ __launch_bounds__(kMaxThreads) void echo_block_norm_k(const BlockNormArgs a) {
+// EARLY: the parameters are loaded with the row.  Behind the row's statistics they come from
+// the L2 cache a workgroup at a time, which costs 3 to 8 %, but their registers would leave
+// one workgroup of 1024 threads and two runs to a CU (8192 x 12288 bfloat16: 196 us, against
+// 147 with two).
+template <int X, int Y, int A, int RUNS, int MAXT, bool EARLY>
+__global__ __launch_bounds__(MAXT) void echo_block_norm_k(const BlockNormArgs a, int64_t row0) {
   __shared__ Slots<1> lds;
   int turn = 0;
   const int64_t C = a.p.C;
-  for (int64_t row = blockIdx.x; row < a.p.R; row += gridDim.x) {
-    float v[RUNS][8];
+  const int e = a.p.elem;
+  {
+    const int64_t row = row0 + blockIdx.x;
+    const int64_t gate_row = a.p.gate != nullptr ? row / a.p.rows_per_gate * a.p.ldg : 0;
+    Run run[RUNS];
+    Raw<X> rx[RUNS];
+    Raw<Y> ry[RUNS];
+    RawParam rpost[RUNS], rgate[RUNS], rpre[RUNS];
 #pragma unroll
     for (int k = 0; k < RUNS; ++k) {
-      const int64_t at = run_at(k);
-      load_run<X>(a.x, row * a.ldx + at, run_length(at, C), v[k]);
+      run[k] = run_of(k, C);
+      if (a.y != nullptr) load_raw<Y>(a.y, row * a.ldy, run[k].at, &ry[k]);
+      load_raw<X>(a.x, row * a.ldx, run[k].at, &rx[k]);
     }
+#pragma unroll
+    for (int k = 0; k < RUNS; ++k) {
+      if (EARLY && a.p.w_post != nullptr) load_raw(e, a.p.w_post, 0, run[k].at, &rpost[k]);
+      if (EARLY && a.p.gate != nullptr) load_raw(e, a.p.gate, gate_row, run[k].at, &rgate[k]);
+      if (EARLY && a.p.w_pre != nullptr) load_raw(e, a.p.w_pre, 0, run[k].at, &rpre[k]);
+    }
+    float v[RUNS][8];
+    float s[1] = {0.0f};
     if (a.y != nullptr) {
-      float y[RUNS][8];
-#pragma unroll
-      for (int k = 0; k < RUNS; ++k) {
-        const int64_t at = run_at(k);
-        load_run<Y>(a.y, row * a.ldy + at, run_length(at, C), y[k]);
-      }
+      float rs = 1.0f;
       if (a.p.post) {
-        float s[1] = {0.0f};
 #pragma unroll
-        for (int k = 0; k < RUNS; ++k)
+        for (int k = 0; k < RUNS; ++k) {
+          float y[8];
+          widen<Y>(ry[k], y);
+          clear_below(run[k].lo, y);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) s[0] = s[0] + y[k][i] * y[k][i];
+          for (int i = 0; i < 8; ++i) s[0] = s[0] + y[i] * y[i];
+        }
         block_sums(s, &lds, &turn);
-        const float rs = reciprocal_rms(s[0], a.p);
-#pragma unroll
-        for (int k = 0; k < RUNS; ++k) {
-          const int64_t at = run_at(k);
-          float w[8];
-          load_weight(a.p, a.p.w_post, at, run_length(at, C), w);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) y[k][i] = y[k][i] * rs * w[i];
-        }
-      }
-      if (a.p.gate != nullptr) {
-        const int64_t g = row / a.p.rows_per_gate * a.p.ldg;
-#pragma unroll
-        for (int k = 0; k < RUNS; ++k) {
-          const int64_t at = run_at(k);
-          float w[8];
-          load_run(a.p.elem, a.p.gate, g + at, run_length(at, C), w);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) y[k][i] = y[k][i] * w[i];
-        }
+        rs = reciprocal_rms(s[0], a.p);
+        s[0] = 0.0f;
       }
 #pragma unroll
       for (int k = 0; k < RUNS; ++k) {
-        const int64_t at = run_at(k);
+        float y[8], w[8];
+        widen<Y>(ry[k], y);
+        if (a.p.post) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[k][i] = stored<X>(a.p.alpha * v[k][i] + y[k][i]);
-        store_run<X>(a.out, row * a.ldo + at, run_length(at, C), v[k]);
+          for (int i = 0; i < 8; ++i) y[i] = y[i] * rs;
+          if (a.p.w_post != nullptr) {
+            if (!EARLY) load_raw(e, a.p.w_post, 0, run[k].at, &rpost[k]);
+          widen(e, rpost[k], w);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) y[i] = y[i] * (w[i] + a.p.offset);
+          }
+        }
+        if (a.p.gate != nullptr) {
+          if (!EARLY) load_raw(e, a.p.gate, gate_row, run[k].at, &rgate[k]);
+        widen(e, rgate[k], w);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) y[i] = y[i] * w[i];
+        }
+        widen<X>(rx[k], v[k]);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[k][i] = stored<X>(a.p.alpha * v[k][i] + y[i]);
+        store_from<X>(a.out, row * a.ldo, run[k], v[k]);
       }
+    } else {
+#pragma unroll
+      for (int k = 0; k < RUNS; ++k) widen<X>(rx[k], v[k]);
     }
-    if (a.a != nullptr) {
-      float s[1] = {0.0f};
+    if (a.a == nullptr) return;
 #pragma unroll
-      for (int k = 0; k < RUNS; ++k)
+    for (int k = 0; k < RUNS; ++k) {
+      clear_below(run[k].lo, v[k]);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) s[0] = s[0] + v[k][i] * v[k][i];
-      block_sums(s, &lds, &turn);
-      const float rs = reciprocal_rms(s[0], a.p);
+      for (int i = 0; i < 8; ++i) s[0] = s[0] + v[k][i] * v[k][i];
+    }
+    block_sums(s, &lds, &turn);
+    const float rs = reciprocal_rms(s[0], a.p);
 #pragma unroll
-      for (int k = 0; k < RUNS; ++k) {
-        const int64_t at = run_at(k);
+    for (int k = 0; k < RUNS; ++k) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[k][i] = v[k][i] * rs;
+      if (a.p.w_pre != nullptr) {
         float w[8];
-        load_weight(a.p, a.p.w_pre, at, run_length(at, C), w);
+        if (!EARLY) load_raw(e, a.p.w_pre, 0, run[k].at, &rpre[k]);
+        widen(e, rpre[k], w);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) w[i] = v[k][i] * rs * w[i];
-        store_run<A>(a.a, row * a.lda + at, run_length(at, C), w);
+        for (int i = 0; i < 8; ++i) v[k][i] = v[k][i] * (w[i] + a.p.offset);
       }
+      store_from<A>(a.a, row * a.lda, run[k], v[k]);
     }
   }
 }
 
-// Rows longer than the registers hold: the row is read again (from the caches) for each
+// Rows longer than the registers hold, and rows of fewer than 8 columns: the row is read again (from the caches) for each
 // statistic.  A thread reads back only what it wrote itself.
 template <int X, int Y, int A>
 __global__ __launch_bounds__(kMaxThreads) void echo_block_norm_long_k(const BlockNormArgs a) {
@@ -155,20 +179,32 @@ __global__ __launch_bounds__(kMaxThreads) void echo_block_norm_long_k(const Bloc
   }
 }
 
-template <int X, int Y, int A, int RUNS>
-hipError_t launch_runs(const BlockNormArgs& a, unsigned grid, hipStream_t s) {
-  hipLaunchKernelGGL((echo_block_norm_k<X, Y, A, RUNS>), dim3(grid), dim3(row_threads(a.p.C, RUNS)), 0, s, a);
-  return hipGetLastError();
+template <int X, int Y, int A, int RUNS, int MAXT, bool EARLY>
+hipError_t launch_runs(const BlockNormArgs& a, hipStream_t s) {
+  const int threads = row_threads(a.p.C, RUNS);
+  const int64_t most = ((int64_t{1} << 32) - 1) / threads;  // a launch numbers its threads in 32 bits
+  for (int64_t row = 0; row < a.p.R; row += most) {
+    const int64_t rows = a.p.R - row < most ? a.p.R - row : most;
+    hipLaunchKernelGGL((echo_block_norm_k<X, Y, A, RUNS, MAXT, EARLY>), dim3(static_cast<unsigned>(rows)), dim3(threads), 0, s, a, row);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 
 }  // namespace
 
 hipError_t launch_block_norm(const BlockNormArgs& a, Elem x, Elem y, Elem out_a, hipStream_t s) {
-  const unsigned grid = static_cast<unsigned>(a.p.R < (int64_t{1} << 20) ? a.p.R : (int64_t{1} << 20));
   return with_types(x, y, out_a, [&](auto X, auto Y, auto A) {
     const int64_t per = 8 * kMaxThreads;
-    if (a.p.C <= per) return launch_runs<X(), Y(), A(), 1>(a, grid, s);
-    if (a.p.C <= 2 * per) return launch_runs<X(), Y(), A(), 2>(a, grid, s);
+    // two runs to a thread where there are rows for several workgroups to a CU (16384 x 8192
+    // bfloat16: 207 us, one run 215; 65536 x 2048: 184 and 192), one where a row should be as
+    // short as it can (64 x 4096: 4.0 us, two runs 4.5), or is short (262144 x 512: 181 and 220)
+    if (a.p.C >= 8 && a.p.C <= per)
+      return a.p.C > 1024 && a.p.R > 2048 ? launch_runs<X(), Y(), A(), 2, 512, true>(a, s)
+                                          : launch_runs<X(), Y(), A(), 1, 1024, true>(a, s);
+    if (a.p.C >= 8 && a.p.C <= 2 * per) return launch_runs<X(), Y(), A(), 2, 1024, false>(a, s);
+    const unsigned grid = static_cast<unsigned>(a.p.R < (int64_t{1} << 20) ? a.p.R : (int64_t{1} << 20));
     hipLaunchKernelGGL((echo_block_norm_long_k<X(), Y(), A()>), dim3(grid), dim3(kMaxThreads), 0, s, a);
     return hipGetLastError();
   });

@@ -14,26 +14,6 @@
 
 namespace echo {
 
-// 512 workgroups where the rows suffice: two to a CU.
-constexpr int64_t kBwdGroups = 512;
-
-BlockSplit block_split(int64_t R, int64_t n_gates) {
-  BlockSplit s{};
-  if (R == 0) return s;
-  const int64_t per_gate = R / n_gates;
-  if (n_gates < kBwdGroups) {
-    const int64_t most = kBwdGroups / n_gates;  // workgroups to a gate
-    s.rows = (per_gate + most - 1) / most;
-    s.chunks = (per_gate + s.rows - 1) / s.rows;
-    s.groups = n_gates * s.chunks;
-  } else {
-    s.gates = (n_gates + kBwdGroups - 1) / kBwdGroups;
-    s.groups = (n_gates + s.gates - 1) / s.gates;
-    s.rows = s.gates * per_gate;
-  }
-  return s;
-}
-
 namespace {
 
 enum Sum { kSumPre = 0, kSumPost = 1, kSumGate = 2, kSums = 3 };
@@ -43,232 +23,421 @@ __device__ __forceinline__ float* part_at(const BlockNormBwdArgs& a, int64_t gro
 }
 
 // The rows of workgroup blockIdx.x.
-__device__ __forceinline__ void rows_of(const BlockNormBwdArgs& a, const BlockSplit& sp, int64_t* lo, int64_t* hi) {
+struct Rows {
+  int64_t lo, hi, step;
+};
+__device__ __forceinline__ Rows rows_of(const BlockNormBwdArgs& a, const BlockSplit& sp) {
   if (sp.chunks != 0) {
     const int64_t g = blockIdx.x / sp.chunks, c = blockIdx.x % sp.chunks;
-    *lo = g * a.p.rows_per_gate + c * sp.rows;
-    const int64_t end = (g + 1) * a.p.rows_per_gate;
-    *hi = *lo + sp.rows < end ? *lo + sp.rows : end;
-  } else {
-    *lo = blockIdx.x * sp.rows;
-    *hi = *lo + sp.rows < a.p.R ? *lo + sp.rows : a.p.R;
+    return Rows{g * a.p.rows_per_gate + c, (g + 1) * a.p.rows_per_gate, sp.chunks};
   }
+  const int64_t lo = blockIdx.x * sp.rows, hi = lo + sp.rows;
+  return Rows{lo, hi < a.p.R ? hi : a.p.R, 1};
+}
+
+// A row's inputs as they are loaded.
+template <int X, int Y, int A>
+struct RawRow {
+  Raw<X> s, dout;
+  Raw<A> da;
+  Raw<Y> y;
+  __device__ __forceinline__ void load(const BlockNormBwdArgs& a, int64_t row, uint32_t at) {
+    load_raw<X>(a.out, row * a.ldo, at, &s);
+    if (a.da != nullptr) load_raw<A>(a.da, row * a.ldda, at, &da);
+    if (a.y != nullptr) load_raw<Y>(a.y, row * a.ldy, at, &y);
+    if (a.dout != nullptr) load_raw<X>(a.dout, row * a.lddo, at, &dout);
+  }
+  __device__ __forceinline__ void load_any(const BlockNormBwdArgs& a, int64_t row, Run run) {
+    echo::load_any<X>(a.out, row * a.ldo, run, &s);
+    if (a.da != nullptr) echo::load_any<A>(a.da, row * a.ldda, run, &da);
+    if (a.y != nullptr) echo::load_any<Y>(a.y, row * a.ldy, run, &y);
+    if (a.dout != nullptr) echo::load_any<X>(a.dout, row * a.lddo, run, &dout);
+  }
+};
+
+// A thread's 8 factors of a weight or gate in LDS, which only it reads: 32 bytes a thread.
+struct Factors {
+  float4* v;
+  __device__ __forceinline__ void put(const float w[8]) const {
+    v[threadIdx.x] = make_float4(w[0], w[1], w[2], w[3]);
+    v[blockDim.x + threadIdx.x] = make_float4(w[4], w[5], w[6], w[7]);
+  }
+  __device__ __forceinline__ void get(float w[8]) const {
+    const float4 a = v[threadIdx.x], b = v[blockDim.x + threadIdx.x];
+    w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w;
+    w[4] = b.x, w[5] = b.y, w[6] = b.z, w[7] = b.w;
+  }
+};
+
+__device__ __forceinline__ void factor_of(int e, bool given, float offset, const RawParam& r, int lo, float w[8]) {
+  if (given) {
+    widen(e, r, w);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w[i] = w[i] + offset;
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w[i] = 1.0f;
+  }
+  clear_below(lo, w);
 }
 
 template <int X, int Y, int A>
 __global__ __launch_bounds__(kMaxThreads) void echo_block_norm_bwd_k(const BlockNormBwdArgs a, const BlockSplit sp) {
   __shared__ Slots<3> lds;
+  extern __shared__ float4 factors[];
+  const Factors pre{factors}, post{factors + 2 * blockDim.x}, gates{factors + 4 * blockDim.x};
   int turn = 0;
-  const int64_t C = a.p.C, at = run_at(0);
-  const int n = run_length(at, C);
+  const int64_t C = a.p.C;
+  const Run run = run_of(0, C);
+  const uint32_t at = run.at;
   const float cols = static_cast<float>(C);
-  float wp[8], wq[8], acc[kSums][8];
-  load_weight(a.p, a.p.w_pre, at, n, wp);
-  load_weight(a.p, a.p.w_post, at, n, wq);
+  const int e = a.p.elem;
+  const Rows rows = rows_of(a, sp);
+  RawRow<X, Y, A> next;
+  next.load(a, rows.lo, at);
+  float acc[kSums][8];
+  {
+    RawParam r[2];
+    float w[8];
+    if (a.p.w_pre != nullptr) load_raw(e, a.p.w_pre, 0, at, &r[0]);
+    if (a.p.w_post != nullptr) load_raw(e, a.p.w_post, 0, at, &r[1]);
+    factor_of(e, a.p.w_pre != nullptr, a.p.offset, r[0], run.lo, w);
+    pre.put(w);
+    factor_of(e, a.p.w_post != nullptr, a.p.offset, r[1], run.lo, w);
+    post.put(w);
+  }
 #pragma unroll
   for (int i = 0; i < 8; ++i) acc[kSumPre][i] = acc[kSumPost][i] = acc[kSumGate][i] = 0.0f;
-  int64_t lo, hi;
-  rows_of(a, sp, &lo, &hi);
-  for (int64_t row = lo; row < hi; ++row) {
-    float s[8], da[8], t[8], y[8];
-    load_run<X>(a.out, row * a.ldo + at, n, s);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) da[i] = t[i] = y[i] = 0.0f;
-    if (a.da != nullptr) load_run<A>(a.da, row * a.ldda + at, n, da);
-    if (a.dout != nullptr) load_run<X>(a.dout, row * a.lddo + at, n, t);
-    if (a.y != nullptr) load_run<Y>(a.y, row * a.ldy + at, n, y);
+  for (int64_t row = rows.lo; row < rows.hi; row += rows.step) {
+    const RawRow<X, Y, A> raw = next;
+    if (row + rows.step < rows.hi) next.load(a, row + rows.step, at);  // in flight while this row is worked on
+    if (a.p.gate != nullptr && (row == rows.lo || (sp.chunks == 0 && row % a.p.rows_per_gate == 0))) {
+      RawParam r;
+      float w[8];
+      load_raw(e, a.p.gate, row / a.p.rows_per_gate * a.p.ldg, at, &r);
+      widen(e, r, w);
+      clear_below(run.lo, w);
+      gates.put(w);
+    }
+    float s[8], t[8], y[8], w[8];
+    widen<X>(raw.s, s);
+    clear_below(run.lo, s);
     float m[3] = {0.0f, 0.0f, 0.0f};
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      m[0] = m[0] + s[i] * s[i];
-      m[1] = m[1] + da[i] * wp[i] * s[i];
-      m[2] = m[2] + y[i] * y[i];
+    for (int i = 0; i < 8; ++i) m[0] = m[0] + s[i] * s[i];
+    if (a.da != nullptr) {
+      float da[8];
+      widen<A>(raw.da, da);
+      clear_below(run.lo, da);
+      pre.get(w);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) m[1] = m[1] + da[i] * w[i] * s[i];
+    }
+    if (a.y != nullptr) {
+      widen<Y>(raw.y, y);
+      clear_below(run.lo, y);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) m[2] = m[2] + y[i] * y[i];
     }
     block_sums(m, &lds, &turn);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) t[i] = 0.0f;
+    if (a.dout != nullptr) {
+      widen<X>(raw.dout, t);
+      clear_below(run.lo, t);
+    }
     if (a.da != nullptr) {
+      float da[8];
+      widen<A>(raw.da, da);
+      clear_below(run.lo, da);
+      pre.get(w);
       const float rs = reciprocal_rms(m[0], a.p), k = rs * rs * (m[1] / cols);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        t[i] = t[i] + rs * (da[i] * wp[i] - s[i] * k);
+        t[i] = t[i] + rs * (da[i] * w[i] - s[i] * k);
         acc[kSumPre][i] = acc[kSumPre][i] + da[i] * (s[i] * rs);
       }
     }
     if (a.dx != nullptr) {
-      float dx[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) dx[i] = a.p.alpha * t[i];
-      store_run<X>(a.dx, row * a.lddx + at, n, dx);
+      for (int i = 0; i < 8; ++i) s[i] = a.p.alpha * t[i];
+      store_from<X>(a.dx, row * a.lddx, run, s);
     }
     if (a.y == nullptr) continue;
     float gate[8];
     if (a.p.gate != nullptr) {
-      load_run(a.p.elem, a.p.gate, row / a.p.rows_per_gate * a.p.ldg + at, n, gate);
+      gates.get(gate);
     } else {
 #pragma unroll
       for (int i = 0; i < 8; ++i) gate[i] = 1.0f;
     }
-    float dy[8];
     if (a.p.post) {
       const float ry = reciprocal_rms(m[2], a.p);
       float q[1] = {0.0f};
+      post.get(w);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const float yh = y[i] * ry, dn = gate[i] * t[i];
-        acc[kSumGate][i] = acc[kSumGate][i] + t[i] * (yh * wq[i]);
+        acc[kSumGate][i] = acc[kSumGate][i] + t[i] * (yh * w[i]);
         acc[kSumPost][i] = acc[kSumPost][i] + dn * yh;
-        dy[i] = dn * wq[i];
-        q[0] = q[0] + dy[i] * y[i];
+        t[i] = dn * w[i];
+        q[0] = q[0] + t[i] * y[i];
       }
       block_sums(q, &lds, &turn);
       const float k = ry * ry * (q[0] / cols);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) dy[i] = ry * (dy[i] - y[i] * k);
+      for (int i = 0; i < 8; ++i) t[i] = ry * (t[i] - y[i] * k);
     } else {
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         acc[kSumGate][i] = acc[kSumGate][i] + t[i] * y[i];
-        dy[i] = gate[i] * t[i];
+        t[i] = gate[i] * t[i];
       }
     }
-    if (a.dy != nullptr) store_run<Y>(a.dy, row * a.lddy + at, n, dy);
+    if (a.dy != nullptr) store_from<Y>(a.dy, row * a.lddy, run, t);
     if (sp.chunks == 0 && a.dgate != nullptr && (row + 1) % a.p.rows_per_gate == 0) {
       // the last row of a gate that is this workgroup's alone
-      store_run(a.p.elem, a.dgate, row / a.p.rows_per_gate * a.lddg + at, n, acc[kSumGate]);
+      store_from(e, a.dgate, row / a.p.rows_per_gate * a.lddg, run, acc[kSumGate]);
 #pragma unroll
       for (int i = 0; i < 8; ++i) acc[kSumGate][i] = 0.0f;
     }
   }
-  if (a.dw_pre != nullptr) store_run<kElemF32>(part_at(a, blockIdx.x, kSumPre), at, n, acc[kSumPre]);
-  if (a.dw_post != nullptr) store_run<kElemF32>(part_at(a, blockIdx.x, kSumPost), at, n, acc[kSumPost]);
+  if (a.dw_pre != nullptr) store_from<kElemF32>(part_at(a, blockIdx.x, kSumPre), 0, run, acc[kSumPre]);
+  if (a.dw_post != nullptr) store_from<kElemF32>(part_at(a, blockIdx.x, kSumPost), 0, run, acc[kSumPost]);
   if (a.dgate != nullptr && sp.chunks != 0)
-    store_run<kElemF32>(part_at(a, blockIdx.x, kSumGate), at, n, acc[kSumGate]);
+    store_from<kElemF32>(part_at(a, blockIdx.x, kSumGate), 0, run, acc[kSumGate]);
 }
 
-__device__ __forceinline__ void add_to(float* p, int64_t at, int n, bool first, const float v[8]) {
-  float o[8];
-  if (first) {
-    store_run<kElemF32>(p, at, n, v);
-    return;
-  }
-  load_run<kElemF32>(p, at, n, o);
-#pragma unroll
-  for (int i = 0; i < 8; ++i) o[i] = o[i] + v[i];
-  store_run<kElemF32>(p, at, n, o);
+// ---- rows that do not fit: statistics, then a pass by columns -------------------------------
+
+// rs(out), its square times mean(u out), rs(y), its square times mean(v y)
+__device__ __forceinline__ float4 stats_of(const BlockNormBwdArgs& a, const float m[3]) {
+  const float rs = reciprocal_rms(m[0], a.p), ry = a.p.post ? reciprocal_rms(m[2], a.p) : 1.0f;
+  return make_float4(rs, rs * rs * (m[1] / static_cast<float>(a.p.C)), ry, 0.0f);
 }
 
-// Rows of more than 8 * kMaxThreads columns: the inputs are read again for each statistic
-// and the column sums are kept in the workspace, each by the thread that owns its columns.
+// A thread's share of the three sums, from its 8 columns.
 template <int X, int Y, int A>
-__global__ __launch_bounds__(kMaxThreads) void echo_block_norm_bwd_long_k(const BlockNormBwdArgs a, const BlockSplit sp) {
+__device__ __forceinline__ void add_squares(const BlockNormBwdArgs& a, const RawRow<X, Y, A>& raw, const RawParam& pre, int lo,
+                                            float m[3]) {
+  float s[8], v[8], w[8];
+  widen<X>(raw.s, s);
+  clear_below(lo, s);
+  if (a.da != nullptr) {
+    widen<A>(raw.da, v);
+    clear_below(lo, v);
+    factor_of(a.p.elem, a.p.w_pre != nullptr, a.p.offset, pre, lo, w);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = v[i] * w[i] * s[i];
+    m[1] = m[1] + sum8(v);
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) s[i] = s[i] * s[i];
+  m[0] = m[0] + sum8(s);
+  if (a.y != nullptr) {
+    widen<Y>(raw.y, v);
+    clear_below(lo, v);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = v[i] * v[i];
+    m[2] = m[2] + sum8(v);
+  }
+}
+
+// The whole gradient of the stream's 8 columns.
+template <int X, int Y, int A>
+__device__ __forceinline__ void stream_gradient(const BlockNormBwdArgs& a, const RawRow<X, Y, A>& raw, const float pre[8], int lo,
+                                                float4 st, float t[8], float dw[8]) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) t[i] = dw[i] = 0.0f;
+  if (a.dout != nullptr) {
+    widen<X>(raw.dout, t);
+    clear_below(lo, t);
+  }
+  if (a.da != nullptr) {
+    float s[8], da[8];
+    widen<X>(raw.s, s);
+    clear_below(lo, s);
+    widen<A>(raw.da, da);
+    clear_below(lo, da);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      t[i] = t[i] + st.x * (da[i] * pre[i] - s[i] * st.y);
+      dw[i] = da[i] * (s[i] * st.x);
+    }
+  }
+}
+
+// sum v y over 8 columns.
+template <int X, int Y, int A>
+__device__ __forceinline__ float post_product(const BlockNormBwdArgs& a, const RawRow<X, Y, A>& raw, const RawParam (&r)[3], int lo,
+                                              float4 st) {
+  const int e = a.p.elem;
+  float t[8], y[8], w[8], unused[8];
+  factor_of(e, a.p.w_pre != nullptr, a.p.offset, r[0], lo, w);
+  stream_gradient<X, Y, A>(a, raw, w, lo, st, t, unused);
+  widen<Y>(raw.y, y);
+  clear_below(lo, y);
+  factor_of(e, a.p.w_post != nullptr, a.p.offset, r[1], lo, w);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) t[i] = t[i] * w[i] * y[i];
+  if (a.p.gate != nullptr) {
+    factor_of(e, true, 0.0f, r[2], lo, w);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) t[i] = t[i] * w[i];
+  }
+  return sum8(t);
+}
+
+__device__ __forceinline__ void load_params(const BlockNormBwdArgs& a, int64_t gate_row, uint32_t at, RawParam (&r)[3]) {
+  if (a.p.w_pre != nullptr) load_raw(a.p.elem, a.p.w_pre, 0, at, &r[0]);
+  if (a.p.w_post != nullptr) load_raw(a.p.elem, a.p.w_post, 0, at, &r[1]);
+  if (a.p.gate != nullptr) load_raw(a.p.elem, a.p.gate, gate_row * a.p.ldg, at, &r[2]);
+}
+
+__device__ __forceinline__ void load_any_params(const BlockNormBwdArgs& a, int64_t gate_row, Run run, RawParam (&r)[3]) {
+  if (a.p.w_pre != nullptr) load_any(a.p.elem, a.p.w_pre, 0, run, &r[0]);
+  if (a.p.w_post != nullptr) load_any(a.p.elem, a.p.w_post, 0, run, &r[1]);
+  if (a.p.gate != nullptr) load_any(a.p.elem, a.p.gate, gate_row * a.p.ldg, run, &r[2]);
+}
+
+// Rows of up to 16 * kMaxThreads columns in the registers.
+template <int X, int Y, int A>
+__global__ __launch_bounds__(kMaxThreads) void echo_block_norm_stats_k(const BlockNormBwdArgs a, int64_t row0) {
+  constexpr int kRuns = 2;
   __shared__ Slots<3> lds;
   int turn = 0;
-  const int64_t C = a.p.C, runs = (C + 8 * kMaxThreads - 1) / (8 * kMaxThreads);
-  const float cols = static_cast<float>(C);
-  int64_t lo, hi;
-  rows_of(a, sp, &lo, &hi);
-  for (int64_t row = lo; row < hi; ++row) {
-    const int64_t gate_row = row / a.p.rows_per_gate;
+  const int64_t C = a.p.C, row = row0 + blockIdx.x;
+  RawRow<X, Y, A> raw[kRuns];
+  RawParam r[kRuns][3];
+#pragma unroll
+  for (int k = 0; k < kRuns; ++k) {
+    const Run run = run_of(k, C);
+    raw[k].load(a, row, run.at);
+    if (a.p.w_pre != nullptr) load_raw(a.p.elem, a.p.w_pre, 0, run.at, &r[k][0]);
+  }
+  float m[3] = {0.0f, 0.0f, 0.0f};
+#pragma unroll
+  for (int k = 0; k < kRuns; ++k) add_squares<X, Y, A>(a, raw[k], r[k][0], run_of(k, C).lo, m);
+  block_sums(m, &lds, &turn);
+  float4 st = stats_of(a, m);
+  if (a.y != nullptr && a.p.post) {
+    float q[1] = {0.0f};
+#pragma unroll
+    for (int k = 0; k < kRuns; ++k) {
+      const Run run = run_of(k, C);
+      load_params(a, row / a.p.rows_per_gate, run.at, r[k]);
+      q[0] = q[0] + post_product<X, Y, A>(a, raw[k], r[k], run.lo, st);
+    }
+    block_sums(q, &lds, &turn);
+    st.w = st.z * st.z * (q[0] / static_cast<float>(C));
+  }
+  if (threadIdx.x == 0) a.stats[row] = st;
+}
+
+// Rows of any length: the inputs are read again for the second statistic.
+template <int X, int Y, int A>
+__global__ __launch_bounds__(kMaxThreads) void echo_block_norm_stats_long_k(const BlockNormBwdArgs a) {
+  __shared__ Slots<3> lds;
+  int turn = 0;
+  const int64_t C = a.p.C;
+  const int runs = static_cast<int>((C + 8 * kMaxThreads - 1) / (8 * kMaxThreads));
+  for (int64_t row = blockIdx.x; row < a.p.R; row += gridDim.x) {
     float m[3] = {0.0f, 0.0f, 0.0f};
-    for (int64_t j = 0; j < runs; ++j) {
-      const int64_t at = run_at(j);
-      const int n = run_length(at, C);
-      float s[8], v[8], w[8];
-      load_run<X>(a.out, row * a.ldo + at, n, s);
-      if (a.da != nullptr) {
-        load_run<A>(a.da, row * a.ldda + at, n, v);
-        load_weight(a.p, a.p.w_pre, at, n, w);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = v[i] * w[i] * s[i];
-        m[1] = m[1] + sum8(v);
-      }
-#pragma unroll
-      for (int i = 0; i < 8; ++i) s[i] = s[i] * s[i];
-      m[0] = m[0] + sum8(s);
-      if (a.y != nullptr) {
-        load_run<Y>(a.y, row * a.ldy + at, n, v);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = v[i] * v[i];
-        m[2] = m[2] + sum8(v);
-      }
+    RawRow<X, Y, A> raw;
+    RawParam r[3];
+    for (int k = 0; k < runs; ++k) {
+      const Run run = any_run_of(k, C);
+      raw.load_any(a, row, run);
+      if (a.p.w_pre != nullptr) load_any(a.p.elem, a.p.w_pre, 0, run, &r[0]);
+      add_squares<X, Y, A>(a, raw, r[0], run.lo, m);
     }
     block_sums(m, &lds, &turn);
-    const float rs = reciprocal_rms(m[0], a.p), k = rs * rs * (m[1] / cols);
-    const float ry = a.p.post ? reciprocal_rms(m[2], a.p) : 1.0f;
-    float ky = 0.0f;
-    // two rounds: the statistic of the post-norm's gradient, then the gradients
-    for (int round = a.y != nullptr && a.p.post ? 0 : 1; round < 2; ++round) {
+    float4 st = stats_of(a, m);
+    if (a.y != nullptr && a.p.post) {
       float q[1] = {0.0f};
-      for (int64_t j = 0; j < runs; ++j) {
-        const int64_t at = run_at(j);
-        const int n = run_length(at, C);
-        float t[8], s[8], v[8], w[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) t[i] = 0.0f;
-        if (a.dout != nullptr) load_run<X>(a.dout, row * a.lddo + at, n, t);
-        if (a.da != nullptr) {
-          load_run<X>(a.out, row * a.ldo + at, n, s);
-          load_run<A>(a.da, row * a.ldda + at, n, v);
-          load_weight(a.p, a.p.w_pre, at, n, w);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            t[i] = t[i] + rs * (v[i] * w[i] - s[i] * k);
-            v[i] = v[i] * (s[i] * rs);
-          }
-          if (round == 1 && a.dw_pre != nullptr) add_to(part_at(a, blockIdx.x, kSumPre), at, n, row == lo, v);
-        }
-        if (a.y != nullptr) {
-          float y[8], gate[8];
-          load_run<Y>(a.y, row * a.ldy + at, n, y);
-          if (a.p.gate != nullptr) {
-            load_run(a.p.elem, a.p.gate, gate_row * a.p.ldg + at, n, gate);
-          } else {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) gate[i] = 1.0f;
-          }
-          load_weight(a.p, a.p.post ? a.p.w_post : nullptr, at, n, w);
-          if (round == 0) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = gate[i] * t[i] * w[i] * y[i];
-            q[0] = q[0] + sum8(v);
-          } else {
-            float dy[8], dw[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const float dn = gate[i] * t[i], yh = y[i] * ry;
-              dy[i] = ry * (dn * w[i] - y[i] * ky);
-              dw[i] = dn * yh;
-              v[i] = t[i] * (yh * w[i]);
-            }
-            if (a.dy != nullptr) store_run<Y>(a.dy, row * a.lddy + at, n, dy);
-            if (a.dw_post != nullptr) add_to(part_at(a, blockIdx.x, kSumPost), at, n, row == lo, dw);
-            if (a.dgate != nullptr) {
-              float* p = part_at(a, blockIdx.x, kSumGate);
-              add_to(p, at, n, row == lo || (sp.chunks == 0 && row % a.p.rows_per_gate == 0), v);
-              if (sp.chunks == 0 && (row + 1) % a.p.rows_per_gate == 0) {
-                load_run<kElemF32>(p, at, n, v);
-                store_run(a.p.elem, a.dgate, gate_row * a.lddg + at, n, v);
-              }
-            }
-          }
-        }
-        if (round == 1 && a.dx != nullptr) {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) t[i] = a.p.alpha * t[i];
-          store_run<X>(a.dx, row * a.lddx + at, n, t);
-        }
+      for (int k = 0; k < runs; ++k) {
+        const Run run = any_run_of(k, C);
+        raw.load_any(a, row, run);
+        load_any_params(a, row / a.p.rows_per_gate, run, r);
+        q[0] = q[0] + post_product<X, Y, A>(a, raw, r, run.lo, st);
       }
-      if (round == 0) {
-        block_sums(q, &lds, &turn);
-        ky = ry * ry * (q[0] / cols);
-      }
+      block_sums(q, &lds, &turn);
+      st.w = st.z * st.z * (q[0] / static_cast<float>(C));
     }
+    if (threadIdx.x == 0) a.stats[row] = st;
   }
 }
 
-// The workgroups' column sums added in order: 64 columns to a workgroup, whose four
-// wavefronts take a quarter of the sums each.  blockIdx.y: w_pre, w_post, then the gates.
-__global__ __launch_bounds__(256) void echo_block_norm_join_k(const BlockNormBwdArgs a, const BlockSplit sp, int64_t n_gates) {
-  __shared__ float lds[4][64];
+// The gradients of kColumnTile columns of a workgroup's rows, whose statistics are known: no
+// sums over a row are left, so rows pass without a barrier.
+template <int X, int Y, int A>
+__global__ __launch_bounds__(kColumnTile / 8) void echo_block_norm_cols_k(const BlockNormBwdArgs a, const BlockSplit sp) {
+  const int64_t C = a.p.C;
+  const Run run = any_run_of(blockIdx.y, C);
+  const int e = a.p.elem;
+  const Rows rows = rows_of(a, sp);
+  RawRow<X, Y, A> next;
+  next.load_any(a, rows.lo, run);
+  float4 next_st = a.stats[rows.lo];
+  RawParam r[3];
+  load_any_params(a, rows.lo / a.p.rows_per_gate, run, r);
+  float pre[8], post[8], gate[8], acc[kSums][8];
+  factor_of(e, a.p.w_pre != nullptr, a.p.offset, r[0], run.lo, pre);
+  factor_of(e, a.p.w_post != nullptr, a.p.offset, r[1], run.lo, post);
+  factor_of(e, a.p.gate != nullptr, 0.0f, r[2], run.lo, gate);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) acc[kSumPre][i] = acc[kSumPost][i] = acc[kSumGate][i] = 0.0f;
+  for (int64_t row = rows.lo; row < rows.hi; row += rows.step) {
+    const RawRow<X, Y, A> raw = next;
+    const float4 st = next_st;
+    if (row + rows.step < rows.hi) {
+      next.load_any(a, row + rows.step, run);
+      next_st = a.stats[row + rows.step];
+    }
+    float t[8], w[8];
+    stream_gradient<X, Y, A>(a, raw, pre, run.lo, st, t, w);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) acc[kSumPre][i] = acc[kSumPre][i] + w[i];
+    if (a.dx != nullptr) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) w[i] = a.p.alpha * t[i];
+      store_from<X>(a.dx, row * a.lddx, run, w);
+    }
+    if (a.y == nullptr) continue;
+    if (sp.chunks == 0 && a.p.gate != nullptr && row % a.p.rows_per_gate == 0 && row != rows.lo) {
+      load_any(e, a.p.gate, row / a.p.rows_per_gate * a.p.ldg, run, &r[2]);
+      factor_of(e, true, 0.0f, r[2], run.lo, gate);
+    }
+    float y[8];
+    widen<Y>(raw.y, y);
+    clear_below(run.lo, y);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float yh = y[i] * st.z, dn = gate[i] * t[i];
+      acc[kSumGate][i] = acc[kSumGate][i] + t[i] * (yh * post[i]);
+      acc[kSumPost][i] = acc[kSumPost][i] + dn * yh;
+      w[i] = st.z * (dn * post[i] - y[i] * st.w);
+    }
+    if (a.dy != nullptr) store_from<Y>(a.dy, row * a.lddy, run, w);
+    if (sp.chunks == 0 && a.dgate != nullptr && (row + 1) % a.p.rows_per_gate == 0) {
+      // the last row of a gate that is this workgroup's alone
+      store_from(e, a.dgate, row / a.p.rows_per_gate * a.lddg, run, acc[kSumGate]);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) acc[kSumGate][i] = 0.0f;
+    }
+  }
+  if (a.dw_pre != nullptr) store_from<kElemF32>(part_at(a, blockIdx.x, kSumPre), 0, run, acc[kSumPre]);
+  if (a.dw_post != nullptr) store_from<kElemF32>(part_at(a, blockIdx.x, kSumPost), 0, run, acc[kSumPost]);
+  if (a.dgate != nullptr && sp.chunks != 0)
+    store_from<kElemF32>(part_at(a, blockIdx.x, kSumGate), 0, run, acc[kSumGate]);
+}
+
+// The workgroups' column sums added in an order of their own: 64 columns to a workgroup,
+// whose 16 wavefronts take every 16th sum each, four loads at a time.  blockIdx.y: w_pre,
+// w_post, then the gates.
+__global__ __launch_bounds__(kMaxThreads) void echo_block_norm_join_k(const BlockNormBwdArgs a, const BlockSplit sp,
+                                                                      int64_t n_gates) {
+  __shared__ float lds[kMaxWaves][64];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int64_t col = static_cast<int64_t>(blockIdx.x) * 64 + lane;
   for (int64_t job = blockIdx.y; job < 2 + n_gates; job += gridDim.y) {
@@ -276,16 +445,25 @@ __global__ __launch_bounds__(256) void echo_block_norm_join_k(const BlockNormBwd
     void* to = sum == kSumPre ? a.dw_pre : sum == kSumPost ? a.dw_post : a.dgate;
     if (to == nullptr) continue;
     const int64_t first = sum == kSumGate ? (job - kSumGate) * sp.chunks : 0;
-    const int64_t count = sum == kSumGate ? sp.chunks : sp.groups;
-    const int64_t lo = first + count * wave / 4, hi = first + count * (wave + 1) / 4;
+    const int count = static_cast<int>(sum == kSumGate ? sp.chunks : sp.groups);
+    const int64_t step = kMaxWaves * kSums * a.p.C;
     float v = 0.0f;
-    if (col < a.p.C)
-      for (int64_t g = lo; g < hi; ++g) v = v + part_at(a, g, sum)[col];
+    if (col < a.p.C) {
+      const float* p = part_at(a, first + wave, sum) + col;
+      int g = wave;
+      for (; g + 3 * kMaxWaves < count; g += 4 * kMaxWaves, p += 4 * step) {
+        const float v0 = p[0], v1 = p[step], v2 = p[2 * step], v3 = p[3 * step];
+        v = v + ((v0 + v1) + (v2 + v3));
+      }
+      for (; g < count; g += kMaxWaves, p += step) v = v + p[0];
+    }
     __syncthreads();
     lds[wave][lane] = v;
     __syncthreads();
     if (wave == 0 && col < a.p.C) {
-      v = (lds[0][lane] + lds[1][lane]) + (lds[2][lane] + lds[3][lane]);
+      v = 0.0f;
+#pragma unroll
+      for (int i = 0; i < kMaxWaves; ++i) v = v + lds[i][lane];
       const int64_t at = (sum == kSumGate ? (job - kSumGate) * a.lddg : 0) + col;
       if (a.p.elem == kElemF32) store1<kElemF32>(to, at, v);
       else if (a.p.elem == kElemBf16) store1<kElemBf16>(to, at, v);
@@ -297,21 +475,41 @@ __global__ __launch_bounds__(256) void echo_block_norm_join_k(const BlockNormBwd
 }  // namespace
 
 hipError_t launch_block_norm_bwd(const BlockNormBwdArgs& a, Elem x, Elem y, Elem out_a, hipStream_t s) {
-  const BlockSplit sp = block_split(a.p.R, a.p.n_gates);
-  const dim3 grid(static_cast<unsigned>(sp.groups));
+  const BlockSplit sp = block_split(a.p.R, a.p.n_gates, a.p.C);
+  const unsigned groups = static_cast<unsigned>(sp.groups);
   // without rows only the sums are written: zeros
-  const hipError_t e = a.p.R == 0 ? hipSuccess : with_types(x, y, out_a, [&](auto X, auto Y, auto A) {
-    if (a.p.C <= 8 * kMaxThreads)
-      hipLaunchKernelGGL((echo_block_norm_bwd_k<X(), Y(), A()>), grid, dim3(row_threads(a.p.C, 1)), 0, s, a, sp);
-    else
-      hipLaunchKernelGGL((echo_block_norm_bwd_long_k<X(), Y(), A()>), grid, dim3(kMaxThreads), 0, s, a, sp);
+  const hipError_t e = a.p.R == 0 ? hipSuccess : with_types(x, y, out_a, [&](auto X, auto Y, auto A) -> hipError_t {
+    if (block_fits(a.p.C)) {
+      const int threads = row_threads(a.p.C, 1);
+      hipLaunchKernelGGL((echo_block_norm_bwd_k<X(), Y(), A()>), dim3(groups), dim3(threads), threads * 6 * sizeof(float4), s,
+                         a, sp);
+      return hipGetLastError();
+    }
+    if (a.p.C > 8 * kMaxThreads && a.p.C <= 16 * kMaxThreads) {
+      const int threads = row_threads(a.p.C, 2);
+      const int64_t most = ((int64_t{1} << 32) - 1) / threads;  // a launch numbers its threads in 32 bits
+      for (int64_t row = 0; row < a.p.R; row += most) {
+        const int64_t rows = a.p.R - row < most ? a.p.R - row : most;
+        hipLaunchKernelGGL((echo_block_norm_stats_k<X(), Y(), A()>), dim3(static_cast<unsigned>(rows)), dim3(threads), 0, s, a,
+                           row);
+        const hipError_t r = hipGetLastError();
+        if (r != hipSuccess) return r;
+      }
+    } else {
+      const unsigned rows = static_cast<unsigned>(a.p.R < (1 << 20) ? a.p.R : (1 << 20));
+      hipLaunchKernelGGL((echo_block_norm_stats_long_k<X(), Y(), A()>), dim3(rows), dim3(kMaxThreads), 0, s, a);
+      const hipError_t r = hipGetLastError();
+      if (r != hipSuccess) return r;
+    }
+    const unsigned tiles = static_cast<unsigned>((a.p.C + kColumnTile - 1) / kColumnTile);
+    hipLaunchKernelGGL((echo_block_norm_cols_k<X(), Y(), A()>), dim3(groups, tiles), dim3(kColumnTile / 8), 0, s, a, sp);
     return hipGetLastError();
   });
   if (e != hipSuccess) return e;
   const int64_t gates = a.dgate != nullptr && (sp.chunks != 0 || a.p.R == 0) ? a.p.n_gates : 0;
   if (a.dw_pre == nullptr && a.dw_post == nullptr && gates == 0) return hipSuccess;
   hipLaunchKernelGGL(echo_block_norm_join_k, dim3(static_cast<unsigned>((a.p.C + 63) / 64), static_cast<unsigned>(2 + (gates < 1024 ? gates : 1024))),
-                     dim3(256), 0, s, a, sp, gates);
+                     dim3(kMaxThreads), 0, s, a, sp, gates);
   return hipGetLastError();
 }
 

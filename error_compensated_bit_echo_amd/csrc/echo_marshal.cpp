@@ -473,8 +473,7 @@ PyObject* block_norm_backward(PyObject*, PyObject* const* args, Py_ssize_t n) {
     const OnDevice on(dev.index);
     at::Tensor owned;
     size_t bytes = 0;
-    const bool sums = dgate != nullptr || dw_post != nullptr || dw_pre != nullptr;
-    const size_t need = sums ? echo_block_norm_workspace(b.rows, b.cols, b.c.gate != nullptr ? b.c.gate_rows : 0) : 0;
+    const size_t need = echo_block_norm_workspace(b.rows, b.cols, b.c.gate != nullptr ? b.c.gate_rows : 0);
     void* ws = workspace_of(args[16], args[17], need, dev, &owned, &bytes);
     return answer(echo_block_norm_backward(&b.c, mo.p, mo.ld, my.p, my.ld, mdo.p, mdo.ld, mda.p, mda.ld, mdx.p, mdx.ld,
                                            mdy.p, mdy.ld, dgate, ldg, dw_post, dw_pre, ws, bytes,

@@ -10,7 +10,6 @@
 namespace echo {
 namespace {
 
-constexpr int kMaxThreads = 1024;
 constexpr int kMaxWaves = kMaxThreads / 64;
 
 template <int CTRL>
@@ -119,6 +118,127 @@ __device__ __forceinline__ int run_length(int64_t at, int64_t C) {
   return n >= 8 ? 8 : n > 0 ? static_cast<int>(n) : 0;
 }
 
+// A run of 8 columns as the register kernels take it.  All of a kernel's loads are issued
+// before the first is used, so they may not hang on branches: a run that would reach past
+// the row starts at the row's last 8 columns instead, and its elements below `lo` are other
+// threads' (all 8 where the whole run lies behind the row).  Rows have 8 columns at least.
+struct Run {
+  uint32_t at;  // 32 bits beside a row's uniform start: one register, not two, for an address
+  int lo;
+};
+
+__device__ __forceinline__ Run run_of(int k, int64_t C) {
+  const uint32_t at = (k * blockDim.x + threadIdx.x) * 8, last = static_cast<uint32_t>(C) - 8;
+  return at <= last ? Run{at, 0} : Run{last, at - last < 8 ? static_cast<int>(at - last) : 8};
+}
+
+// Elements as they are loaded.
+template <int E>
+struct Raw {
+  typename ElemOf<E>::T v __attribute__((ext_vector_type(8)));
+};
+
+template <int E>
+__device__ __forceinline__ void load_raw(const void* base, int64_t row, uint32_t at, Raw<E>* r) {
+  const typename ElemOf<E>::T* p = static_cast<const typename ElemOf<E>::T*>(base) + row;
+  __builtin_memcpy(&r->v, p + at, sizeof(r->v));
+}
+
+template <int E>
+__device__ __forceinline__ void widen(const Raw<E>& r, float v[8]) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = static_cast<float>(r.v[i]);
+}
+
+// Parameters, whose type is an argument of the launch.
+struct RawParam {
+  uint32_t w[8];
+};
+
+__device__ __forceinline__ void load_raw(int elem, const void* base, int64_t row, uint32_t at, RawParam* r) {
+  if (elem == kElemF32) {
+    const float* p = static_cast<const float*>(base) + row;
+    __builtin_memcpy(r->w, p + at, 32);
+  } else {
+    const uint16_t* p = static_cast<const uint16_t*>(base) + row;
+    __builtin_memcpy(r->w, p + at, 16);
+  }
+}
+
+__device__ __forceinline__ void widen(int elem, const RawParam& r, float v[8]) {
+  if (elem == kElemF32) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r.w[i]);
+  } else if (elem == kElemBf16) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(i & 1 ? r.w[i >> 1] & 0xFFFF0000u : r.w[i >> 1] << 16);
+  } else {
+    Raw<kElemF16> h;
+    __builtin_memcpy(&h.v, r.w, 16);
+    widen<kElemF16>(h, v);
+  }
+}
+
+// The same for rows of fewer than 8 columns too: the first run starts before the row then
+// (`at` wraps), and its elements from `lo` on are the row's.
+__device__ __forceinline__ Run any_run_of(int k, int64_t C) {
+  if (C >= 8) return run_of(k, C);
+  const uint32_t at = static_cast<uint32_t>(C) - 8;
+  return Run{at, k == 0 && threadIdx.x == 0 ? 8 - static_cast<int>(C) : 8};
+}
+
+template <int E>
+__device__ __forceinline__ void load_any(const void* base, int64_t row, Run run, Raw<E>* r) {
+  if (static_cast<int>(run.at) >= 0) {
+    load_raw<E>(base, row, run.at, r);
+  } else {
+    const typename ElemOf<E>::T* p = static_cast<const typename ElemOf<E>::T*>(base) + row;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int j = static_cast<int>(run.at) + i;
+      r->v[i] = p[j > 0 ? j : 0];
+    }
+  }
+}
+
+__device__ __forceinline__ void load_any(int elem, const void* base, int64_t row, Run run, RawParam* r) {
+  if (elem == kElemF32) {
+    Raw<kElemF32> f;
+    load_any<kElemF32>(base, row, run, &f);
+    __builtin_memcpy(r->w, &f.v, 32);
+  } else {  // either 16-bit type: its bits
+    Raw<kElemF16> h;
+    load_any<kElemF16>(base, row, run, &h);
+    __builtin_memcpy(r->w, &h.v, 16);
+  }
+}
+
+// Zeros in place of the elements that are other threads'.
+__device__ __forceinline__ void clear_below(int lo, float v[8]) {
+  if (lo > 0) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = i < lo ? 0.0f : v[i];
+  }
+}
+
+template <int E>
+__device__ __forceinline__ void store_from(void* base, int64_t row, Run run, const float v[8]) {
+  typename ElemOf<E>::T* p = static_cast<typename ElemOf<E>::T*>(base) + row;
+  if (run.lo == 0) {
+    store8<E>(p, run.at, v);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i >= run.lo) store1<E>(p, run.at + i, v[i]);
+  }
+}
+
+__device__ __forceinline__ void store_from(int elem, void* base, int64_t row, Run run, const float v[8]) {
+  if (elem == kElemF32) store_from<kElemF32>(base, row, run, v);
+  else if (elem == kElemBf16) store_from<kElemBf16>(base, row, run, v);
+  else store_from<kElemF16>(base, row, run, v);
+}
+
 // The factor of a norm's weight: offset + w, 1 without a weight.
 __device__ __forceinline__ void load_weight(const BlockParams& p, const void* w, int64_t at, int n, float v[8]) {
   if (w == nullptr) {
@@ -137,12 +257,6 @@ __device__ __forceinline__ float reciprocal_rms(float squares, const BlockParams
 }
 
 }  // namespace
-
-// Threads for rows of C columns, 8 * `runs` of them to a thread.
-inline int row_threads(int64_t C, int runs) {
-  const int64_t t = (C + 8 * runs - 1) / (8 * runs);
-  return static_cast<int>(t >= kMaxThreads ? kMaxThreads : (t + 63) / 64 * 64);
-}
 
 // Calls f with the three types as constants; bfloat16 and fp16 do not come together.
 template <typename F>

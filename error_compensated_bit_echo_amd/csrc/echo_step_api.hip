@@ -273,21 +273,24 @@ echo_status echo_block_norm_backward(const echo_block* b, const void* out, int64
   Mat ins[] = {{dout, b->rows, lddo, b->x_dtype}, {out, b->rows, ldo, b->x_dtype}, {y, b->rows, ldy, b->y_dtype},
                {da, b->rows, ldda, b->a_dtype}, gate, {b->w_post, 1, C, b->param_dtype}, {b->w_pre, 1, C, b->param_dtype}};
   Mat outs[] = {{dx, b->rows, lddx, b->x_dtype}, {dy, b->rows, lddy, b->y_dtype}, {dgate, n_gates, ld_dgate, b->param_dtype},
-                {dw_post, 1, C, b->param_dtype}, {dw_pre, 1, C, b->param_dtype}, {nullptr, 0, 0, ECHO_F32}};
+                {dw_post, 1, C, b->param_dtype}, {dw_pre, 1, C, b->param_dtype}};
   for (Mat& m : ins)
     if ((e = check_mat(&m, C)) != ECHO_OK) return e;
   for (Mat& m : outs)
     if ((e = check_mat(&m, C)) != ECHO_OK) return e;
   const size_t need = echo_block_norm_workspace(b->rows, C, n_gates);
   const bool sums = dgate != nullptr || dw_post != nullptr || dw_pre != nullptr;
-  if (sums && need > 0) {
+  if (need > 0) {
     if (workspace == nullptr || workspace_bytes < need) return ECHO_ERR_WORKSPACE;
     if (!aligned(workspace, 16)) return ECHO_ERR_ARG;
-    // rows of fp32 as wide as the others
-    outs[5] = Mat{workspace, static_cast<int64_t>(need / (static_cast<size_t>(C) * sizeof(float))), C, ECHO_F32};
+    const Area w = area(workspace, 1, static_cast<int64_t>(need), 0);
+    for (const Mat& m : ins)
+      if (m.p != nullptr && m.rows != 0 && overlap(w, area_of(m, C))) return ECHO_ERR_ARG;
+    for (const Mat& m : outs)
+      if (m.p != nullptr && m.rows != 0 && overlap(w, area_of(m, C))) return ECHO_ERR_ARG;
   }
   // dx may be dout itself: a thread reads an element before it writes it
-  if (!apart(outs, 6, ins, 7, C, 0, 0)) return ECHO_ERR_ARG;
+  if (!apart(outs, 5, ins, 7, C, 0, 0)) return ECHO_ERR_ARG;
   if (b->rows == 0 && !sums) return ECHO_OK;
   echo::BlockNormBwdArgs n{};
   n.p = params_of(*b, ins[4]);
@@ -308,6 +311,8 @@ echo_status echo_block_norm_backward(const echo_block* b, const void* out, int64
   n.lddy = outs[1].ld;
   n.lddg = outs[2].ld;
   n.part = static_cast<float*>(workspace);
+  n.stats = reinterpret_cast<float4*>(static_cast<char*>(workspace) +
+                                      (echo::block_norm_part(b->rows, C, n.p.n_gates) + 15) / 16 * 16);
   const int32_t yt = y != nullptr ? b->y_dtype : b->x_dtype, at = da != nullptr ? b->a_dtype : b->x_dtype;
   return status_of(echo::launch_block_norm_bwd(n, elem(b->x_dtype), elem(yt), elem(at), static_cast<hipStream_t>(stream)));
 }

@@ -46,16 +46,62 @@ struct BlockNormBwdArgs {
   void* dw_post;
   void* dw_pre;
   int64_t ldo, ldy, lddo, ldda, lddx, lddy, lddg;
-  float* part;  // workspace: column sums of the workgroups
+  float* part;   // workspace: column sums of the workgroups
+  float4* stats;  // and the rows' statistics
 };
-// The split of the rows over workgroups: `chunks` workgroups to a gate's rows, or, where
-// chunks is 0, `gates` whole gates to a workgroup.
+constexpr int kMaxThreads = 1024;
+
+// Threads for rows of C columns, 8 * `runs` of them to a thread.
+inline int row_threads(int64_t C, int runs) {
+  const int64_t t = (C + 8 * runs - 1) / (8 * runs);
+  return static_cast<int>(t >= kMaxThreads ? kMaxThreads : (t + 63) / 64 * 64);
+}
+
+// Whether one workgroup holds a row's inputs and column sums in its registers; other rows
+// take a pass for their statistics and one by columns.
+inline bool block_fits(int64_t C) { return C >= 8 && C <= 8 * kMaxThreads; }
+
+constexpr int64_t kColumnTile = 2048;  // columns of a workgroup of the pass by columns
+
+// The split of the rows over workgroups that sum columns: `chunks` workgroups to a gate's
+// rows, each taking every chunks-th of them (rows next to each other are worked on at the
+// same time, so that their addresses spread over the memory channels: 16384 x 8192 bfloat16
+// 344 us, with consecutive rows to a workgroup 354); or, where chunks is 0, `gates` whole
+// gates of `rows` rows in all to a workgroup.
 struct BlockSplit {
-  int64_t groups, chunks, gates, rows;  // workgroups; rows to a workgroup (of one gate)
+  int64_t groups, chunks, gates, rows;
 };
-BlockSplit block_split(int64_t R, int64_t n_gates);
+
+inline BlockSplit block_split(int64_t R, int64_t n_gates, int64_t C) {
+  BlockSplit s{};
+  if (R == 0) return s;
+  const int64_t per_gate = R / n_gates;
+  // as many workgroups as 256 CUs hold at a time, 16 wavefronts to a CU
+  const int64_t tiles = (C + kColumnTile - 1) / kColumnTile;
+  int64_t most = block_fits(C) ? 256 * (kMaxThreads / row_threads(C, 1)) : tiles < 1024 ? 1024 / tiles : 1;
+  // a workgroup's column sums cost two rows of fp32 each: at least 4 rows for them, where
+  // that leaves a workgroup to every CU
+  const int64_t few = R / 4 > 256 ? R / 4 : 256;
+  if (most > few) most = few;
+  if (n_gates < most) {
+    const int64_t chunks = most / n_gates;
+    s.chunks = per_gate < chunks ? per_gate : chunks;
+    s.groups = n_gates * s.chunks;
+  } else {
+    s.gates = (n_gates + most - 1) / most;
+    s.groups = (n_gates + s.gates - 1) / s.gates;
+    s.rows = s.gates * per_gate;
+  }
+  return s;
+}
+
+// The workspace: every workgroup's three column sums, and, for rows that do not fit the
+// registers, four statistics of each.
+inline size_t block_norm_part(int64_t R, int64_t C, int64_t n_gates) {
+  return static_cast<size_t>(block_split(R, n_gates, C).groups) * 3 * static_cast<size_t>(C) * sizeof(float);
+}
 inline size_t block_norm_workspace(int64_t R, int64_t C, int64_t n_gates) {
-  return static_cast<size_t>(block_split(R, n_gates).groups) * 3 * static_cast<size_t>(C) * sizeof(float);
+  return (block_norm_part(R, C, n_gates) + 15) / 16 * 16 + (block_fits(C) ? 0 : static_cast<size_t>(R) * 16);
 }
 hipError_t launch_block_norm_bwd(const BlockNormBwdArgs& a, Elem x, Elem y, Elem out_a, hipStream_t s);
 

@@ -473,8 +473,8 @@ echo_status echo_block_norm(const echo_block* b, const void* x, int64_t ldx, con
                             int64_t ldo, void* a, int64_t lda, echo_stream_t stream);
 
 /* Source: none on the pages (host bookkeeping).
- * Bytes of workspace of echo_block_norm_backward where it gives gradients of
- * parameters; gate_rows 0 without a gate.  0 for sizes that it refuses. */
+ * Bytes of workspace of echo_block_norm_backward; gate_rows 0 without a gate.  0
+ * for sizes that it refuses. */
 size_t echo_block_norm_workspace(int64_t rows, int64_t cols, int64_t gate_rows);
 
 /* Source: none on the pages (the backward pass of echo_block_norm).
@@ -488,9 +488,8 @@ size_t echo_block_norm_workspace(int64_t rows, int64_t cols, int64_t gate_rows);
  *   dw_post = sum of dn y ry,  dw_pre = sum of da out rs over the rows.
  * Sums over rows are fp32, in an order that the sizes fix; every output is
  * rounded once.  dx may be dout itself.  With no rows, gradients of parameters
- * are zeros.  workspace: echo_block_norm_workspace bytes, 16-byte aligned, NULL
- * where only dx and dy are wanted.  At most two launches.  Errors as above, and
- * ECHO_ERR_WORKSPACE. */
+ * are zeros.  workspace: echo_block_norm_workspace bytes, 16-byte aligned.  One to
+ * three launches.  Errors as above, and ECHO_ERR_WORKSPACE. */
 echo_status echo_block_norm_backward(const echo_block* b, const void* out, int64_t ldo, const void* y, int64_t ldy,
                                      const void* dout, int64_t lddo, const void* da, int64_t ldda, void* dx, int64_t lddx,
                                      void* dy, int64_t lddy, void* dgate, int64_t ld_dgate, void* dw_post, void* dw_pre,
