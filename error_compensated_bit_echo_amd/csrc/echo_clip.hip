@@ -1,6 +1,6 @@
 // The norm of many tensors together, and the tensors scaled by min(1, max_norm / (norm +
-// 1e-6)).  Two launches for up to kClipTensors tensors: the first adds squares, a partial
-// sum per workgroup; in the second every workgroup adds the partial sums, in the same
+// 1e-6)).  Two launches for up to 176 tensors (280 in place): the first adds squares, a
+// partial sum per workgroup; in the second every workgroup adds the partial sums, in the same
 // order, and scales its chunks.  Tensors come in the launch's arguments, so nothing is kept
 // between calls and a captured call needs no table in device memory.
 //
@@ -12,8 +12,8 @@ namespace echo {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kRuns = 8;                            // runs of 8 elements to a thread and chunk
-constexpr int64_t kChunk = kThreads * kRuns * 8;    // elements
+constexpr int kUnits = static_cast<int>(kClipChunk) / 16 / kThreads;  // 16-byte units of a chunk to a thread
+constexpr int kHalf = kUnits / 2;
 
 __device__ __forceinline__ double wave_sum64(double v) {
 #pragma unroll
@@ -30,54 +30,124 @@ __device__ __forceinline__ double block_sum64(double v, double* lds) {
   return (lds[0] + lds[1]) + (lds[2] + lds[3]);
 }
 
-// The tensor that holds a chunk: the last one whose first chunk is not behind it.
+// A launch's chunks: where each lies.  Every lane keeps a few of the tensors' first chunks, so
+// that finding a chunk's tensor is a count of those not behind it, with no chain of loads.
 template <typename Args>
-__device__ __forceinline__ int tensor_of(const Args* a, uint32_t chunk) {
-  int lo = 0, hi = a->tensors;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (a->first[mid] <= chunk) lo = mid;
-    else hi = mid;
+struct Tensors {
+  static constexpr int kEach = (Args::kTensors + 63) / 64;
+  uint32_t first[kEach];
+
+  template <typename A>
+  __device__ __forceinline__ void load(const A* a) {
+    const int lane = threadIdx.x & 63, n = a->tensors;
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+      const int t = i * 64 + lane;
+      first[i] = t < n ? a->first[t] : ~0u;
+    }
   }
-  return lo;
+  __device__ __forceinline__ int tensor_of(uint32_t chunk) const {
+    int t = -1;
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) t += __popcll(__ballot(first[i] <= chunk));
+    return t;
+  }
+};
+
+struct Chunk {
+  int64_t at;      // its first byte in the tensor
+  int tensor, elem;
+  int bytes;       // of it
+};
+
+template <typename Args, typename A>
+__device__ __forceinline__ Chunk chunk_of(const A* a, const Tensors<Args>& ts, uint32_t c) {
+  const int t = ts.tensor_of(c);
+  const uint32_t tail = a->tail[t], first = a->first[t];
+  return Chunk{static_cast<int64_t>(c - first) * kClipChunk, t, static_cast<int>(tail >> 14),
+               c + 1 == a->first[t + 1] ? static_cast<int>(((tail & 0x3FFF) + 1) * 2) : static_cast<int>(kClipChunk)};
+}
+
+// 16 bytes of a chunk.  One that would reach past the tensor's end starts 16 bytes before it
+// instead, and its first `lo` bytes are another thread's (16: all of them).  All of a
+// chunk's loads are issued before the first is used.
+struct Unit {
+  uint32_t w[4];
+};
+
+struct Spot {
+  int64_t at;
+  int lo;
+};
+
+__device__ __forceinline__ Spot spot_of(const Chunk& c, int k) {
+  const int at = (k * kThreads + static_cast<int>(threadIdx.x)) * 16, last = c.bytes - 16;
+  return at <= last ? Spot{c.at + at, 0} : Spot{c.at + last, at - last < 16 ? at - last : 16};
+}
+
+template <int N>
+__device__ __forceinline__ void load_units(const Chunk& c, const char* p, Unit (&u)[N]) {
+  if (c.at + c.bytes >= 16) {
+#pragma unroll
+    for (int k = 0; k < N; ++k) __builtin_memcpy(u[k].w, p + spot_of(c, k).at, 16);
+  } else {
+    // a tensor of fewer than 16 bytes: its elements are the unit's last ones
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int64_t at = static_cast<int64_t>(c.bytes) - 16 + i * 4;  // of a dword of the unit
+      const uint32_t low = at >= 0 ? *reinterpret_cast<const uint16_t*>(p + at) : 0;
+      const uint32_t high = at + 2 >= 0 ? *reinterpret_cast<const uint16_t*>(p + at + 2) : 0;
+      u[0].w[i] = low | high << 16;
+    }
+#pragma unroll
+    for (int k = 1; k < N; ++k) u[k] = u[0];
+  }
 }
 
 template <int E>
-__device__ __forceinline__ double chunk_squares(const void* p, int64_t at, int64_t n) {
+__device__ __forceinline__ double unit_squares(const Unit& u, int lo) {
+  typedef typename ElemOf<E>::T T;
+  constexpr int kN = 16 / sizeof(T);
+  T x[kN];
+  __builtin_memcpy(x, u.w, 16);
   double s = 0.0;
-  if (at + kChunk <= n) {
-    float v[kRuns][8];
 #pragma unroll
-    for (int k = 0; k < kRuns; ++k) load8<E>(p, at + (k * kThreads + threadIdx.x) * 8, v[k]);
-#pragma unroll
-    for (int k = 0; k < kRuns; ++k)
-#pragma unroll
-      for (int i = 0; i < 8; ++i) s = s + static_cast<double>(v[k][i]) * static_cast<double>(v[k][i]);
-  } else {
-    for (int k = 0; k < kRuns; ++k) {
-      const int64_t j = at + (k * kThreads + threadIdx.x) * 8;
-      float v[8];
-      load_run<E>(p, j, run_length(j, n), v);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) s = s + static_cast<double>(v[i]) * static_cast<double>(v[i]);
-    }
+  for (int i = 0; i < kN; ++i) {
+    const double v = static_cast<double>(i * static_cast<int>(sizeof(T)) >= lo ? static_cast<float>(x[i]) : 0.0f);
+    s = __builtin_fma(v, v, s);
   }
   return s;
 }
 
-__global__ __launch_bounds__(kThreads) void echo_clip_sum_k(const ClipArgs given, double* part) {
+template <int E, int N>
+__device__ __forceinline__ double squares_of(const Chunk& c, const char* p) {
+  Unit u[N];
+  load_units(c, p, u);
+  double s = 0.0;
+#pragma unroll
+  for (int k = 0; k < N; ++k) s = s + unit_squares<E>(u[k], spot_of(c, k).lo);
+  return s;
+}
+
+// A chunk that half the units cover, and so a short tensor, is loaded by halves.
+template <int E>
+__device__ __forceinline__ double squares(const Chunk& c, const char* p) {
+  return c.bytes <= kHalf * kThreads * 16 ? squares_of<E, kHalf>(c, p) : squares_of<E, kUnits>(c, p);
+}
+
+__global__ __launch_bounds__(kThreads) void echo_clip_sum_k(const ClipInPlace given, double* part) {
   __shared__ double lds[4];
-  const auto* a = kernel_args<ClipArgs>();
+  const auto* a = kernel_args<ClipInPlace>();
+  Tensors<ClipInPlace> ts;
+  ts.load(a);
   const uint32_t chunks = a->first[a->tensors];
   double s = 0.0;
-  for (uint32_t c = blockIdx.x; c < chunks; c += gridDim.x) {
-    const int t = tensor_of(a, c);
-    const int64_t at = static_cast<int64_t>(c - a->first[t]) * kChunk, n = a->n[t];
-    const void* p = a->src[t];
-    const int e = a->elem[t];
-    if (e == kElemF32) s = s + chunk_squares<kElemF32>(p, at, n);
-    else if (e == kElemBf16) s = s + chunk_squares<kElemBf16>(p, at, n);
-    else s = s + chunk_squares<kElemF16>(p, at, n);
+  for (uint32_t i = blockIdx.x; i < chunks; i += gridDim.x) {
+    const Chunk c = chunk_of(a, ts, i);
+    const char* p = static_cast<const char*>(a->src[c.tensor]);
+    if (c.elem == kElemF32) s = s + squares<kElemF32>(c, p);
+    else if (c.elem == kElemBf16) s = s + squares<kElemBf16>(c, p);
+    else s = s + squares<kElemF16>(c, p);
   }
   s = block_sum64(s, lds);
   if (threadIdx.x == 0) part[blockIdx.x] = s;
@@ -89,53 +159,68 @@ __device__ __forceinline__ double norm_of(const double* part, int64_t n_part, do
   return sqrt(block_sum64(s, lds));
 }
 
-template <int E>
-__device__ __forceinline__ void scale_chunk(const void* p, void* o, int64_t at, int64_t n, float f) {
-  if (at + kChunk <= n) {
-    float v[kRuns][8];
+// STREAM: past the caches, so that what the first launch read and the cache still holds is not
+// replaced by the results.
+template <int E, bool STREAM>
+__device__ __forceinline__ void scale_unit(const Unit& u, char* o, Spot at, float f) {
+  typedef typename ElemOf<E>::T T;
+  constexpr int kN = 16 / sizeof(T);
+  T x[kN];
+  __builtin_memcpy(x, u.w, 16);
 #pragma unroll
-    for (int k = 0; k < kRuns; ++k) load8<E>(p, at + (k * kThreads + threadIdx.x) * 8, v[k]);
-#pragma unroll
-    for (int k = 0; k < kRuns; ++k) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) v[k][i] = v[k][i] * f;
-      store8<E>(o, at + (k * kThreads + threadIdx.x) * 8, v[k]);
-    }
+  for (int i = 0; i < kN; ++i) x[i] = narrow<E>(static_cast<float>(x[i]) * f);
+  if (at.lo == 0) {
+    typedef uint32_t u4 __attribute__((ext_vector_type(4), aligned(2)));
+    u4 w;
+    __builtin_memcpy(&w, x, 16);
+    u4* to = reinterpret_cast<u4*>(o + at.at);
+    if constexpr (STREAM) __builtin_nontemporal_store(w, to);
+    else *to = w;
   } else {
-    for (int k = 0; k < kRuns; ++k) {
-      const int64_t j = at + (k * kThreads + threadIdx.x) * 8;
-      const int m = run_length(j, n);
-      float v[8];
-      load_run<E>(p, j, m, v);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = v[i] * f;
-      store_run<E>(o, j, m, v);
-    }
+    for (int i = 0; i < kN; ++i)
+      if (i * static_cast<int>(sizeof(T)) >= at.lo) reinterpret_cast<T*>(o + at.at)[i] = x[i];
   }
 }
 
-__global__ __launch_bounds__(kThreads) void echo_clip_scale_k(const ClipArgs given, const double* part, int64_t n_part,
+template <int E, bool STREAM, int N>
+__device__ __forceinline__ void scale_units(const Chunk& c, const char* p, char* o, float f) {
+  Unit u[N];
+  load_units(c, p, u);
+#pragma unroll
+  for (int k = 0; k < N; ++k) scale_unit<E, STREAM>(u[k], o, spot_of(c, k), f);
+}
+
+template <int E, bool STREAM>
+__device__ __forceinline__ void scale(const Chunk& c, const char* p, char* o, float f) {
+  if (c.bytes <= kHalf * kThreads * 16) scale_units<E, STREAM, kHalf>(c, p, o, f);
+  else scale_units<E, STREAM, kUnits>(c, p, o, f);
+}
+
+template <typename Args, bool STREAM>
+__global__ __launch_bounds__(kThreads) void echo_clip_scale_k(const Args given, const double* part, int64_t n_part,
                                                               double max_norm, float* norm) {
   __shared__ double lds[4];
-  const auto* a = kernel_args<ClipArgs>();
+  const auto* a = kernel_args<Args>();
+  Tensors<Args> ts;
+  ts.load(a);
   const double total = norm_of(part, n_part, lds);
   if (norm != nullptr && blockIdx.x == 0 && threadIdx.x == 0) *norm = static_cast<float>(total);
   // a norm that is not a number makes every element one; an infinite norm gives 0
   const double f64 = max_norm / (total + 1e-6);
   const float f = f64 >= 1.0 ? 1.0f : static_cast<float>(f64);
+  constexpr bool kApart = sizeof(a->dst) > sizeof(void*);
+  if (!kApart && f == 1.0f) return;
   const uint32_t chunks = a->first[a->tensors];
   // from the last chunk on: the first launch read it last, so it is likeliest to be cached
-  for (uint32_t c = blockIdx.x; c < chunks; c += gridDim.x) {
-    const uint32_t chunk = chunks - 1 - c;
-    const int t = tensor_of(a, chunk);
-    const int64_t at = static_cast<int64_t>(chunk - a->first[t]) * kChunk, n = a->n[t];
-    const void* p = a->src[t];
-    void* o = a->dst[t];
+  for (uint32_t i = blockIdx.x; i < chunks; i += gridDim.x) {
+    const Chunk c = chunk_of(a, ts, chunks - 1 - i);
+    const char* p = static_cast<const char*>(a->src[c.tensor]);
+    char* o = kApart ? static_cast<char*>(a->dst[c.tensor]) : const_cast<char*>(p);
     if (f == 1.0f && p == o) continue;
-    const int e = a->elem[t];
-    if (e == kElemF32) scale_chunk<kElemF32>(p, o, at, n, f);
-    else if (e == kElemBf16) scale_chunk<kElemBf16>(p, o, at, n, f);
-    else scale_chunk<kElemF16>(p, o, at, n, f);
+    if (c.elem == kElemF32) scale<kElemF32, STREAM>(c, p, o, f);
+    else if (c.elem == kElemBf16) scale<kElemBf16, STREAM>(c, p, o, f);
+    else scale<kElemF16, STREAM>(c, p, o, f);
   }
 }
 
@@ -145,26 +230,31 @@ __global__ __launch_bounds__(kThreads) void echo_clip_norm_k(const double* part,
   if (threadIdx.x == 0) *norm = static_cast<float>(total);
 }
 
-unsigned clip_grid(uint32_t chunks) {
-  return chunks < static_cast<uint32_t>(kClipGroups) ? chunks : static_cast<unsigned>(kClipGroups);
+template <typename Args>
+hipError_t launch_scale(const Args& a, const double* part, int64_t n_part, double max_norm, float* norm, bool stream, hipStream_t s) {
+  const dim3 grid(clip_grid(a.first[a.tensors]));
+  if (stream)
+    hipLaunchKernelGGL((echo_clip_scale_k<Args, true>), grid, dim3(kThreads), 0, s, a, part, n_part, max_norm, norm);
+  else
+    hipLaunchKernelGGL((echo_clip_scale_k<Args, false>), grid, dim3(kThreads), 0, s, a, part, n_part, max_norm, norm);
+  return hipGetLastError();
 }
 
 }  // namespace
 
-int64_t clip_chunks(int64_t n) { return (n + kChunk - 1) / kChunk; }
-
-hipError_t launch_clip_sum(const ClipArgs& a, double* part, int64_t at, int64_t* used, hipStream_t s) {
-  const unsigned grid = clip_grid(a.first[a.tensors]);
-  *used = grid;
-  hipLaunchKernelGGL(echo_clip_sum_k, dim3(grid), dim3(kThreads), 0, s, a, part + at);
+hipError_t launch_clip_sum(const ClipInPlace& a, double* part, hipStream_t s) {
+  hipLaunchKernelGGL(echo_clip_sum_k, dim3(clip_grid(a.first[a.tensors])), dim3(kThreads), 0, s, a, part);
   return hipGetLastError();
 }
 
-hipError_t launch_clip_scale(const ClipArgs& a, const double* part, int64_t n_part, double max_norm, float* norm,
-                             hipStream_t s) {
-  hipLaunchKernelGGL(echo_clip_scale_k, dim3(clip_grid(a.first[a.tensors])), dim3(kThreads), 0, s, a, part, n_part,
-                     max_norm, norm);
-  return hipGetLastError();
+hipError_t launch_clip_scale(const ClipInPlace& a, const double* part, int64_t n_part, double max_norm, float* norm,
+                             bool stream, hipStream_t s) {
+  return launch_scale(a, part, n_part, max_norm, norm, stream, s);
+}
+
+hipError_t launch_clip_scale(const ClipApart& a, const double* part, int64_t n_part, double max_norm, float* norm,
+                             bool stream, hipStream_t s) {
+  return launch_scale(a, part, n_part, max_norm, norm, stream, s);
 }
 
 hipError_t launch_clip_norm(const double* part, int64_t n_part, float* norm, hipStream_t s) {

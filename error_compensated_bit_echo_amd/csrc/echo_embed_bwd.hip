@@ -2,10 +2,11 @@
 // row r V + v, in rising order of t), zeros for rows without a token.
 //
 // The tokens are sorted by row (stable, so equal tokens stay in order), then runs of equal
-// tokens are summed: no atomics, so the result is the same from call to call, and a row is
-// written once.  The sort is a radix sort of 8-bit digits.  Up to kSmall tokens one
-// workgroup holds them all in LDS, while the launch's other workgroups clear the tables.
-// More tokens take three launches a digit: counts per tile, their prefix sums, placement.
+// tokens are summed: no atomics on sums, so the result is the same from call to call.  The
+// sort is a radix sort of 9-bit digits: two for vocabularies of up to 2^18 - 1 rows.  Up to
+// kSmall tokens one workgroup holds them all in LDS; more take three launches a digit: counts
+// per tile, their prefix sums, placement.  Either way the launches' other workgroups clear the
+// tables meanwhile, which takes longer than the sort where tables are large.
 //
 // The sorted tokens are cut into chunks of equal length, whatever the runs: a chunk writes
 // the rows of runs that lie inside it, and puts the sum of a run that crosses its start or
@@ -18,12 +19,13 @@ namespace {
 
 constexpr int kSortThreads = 1024;
 constexpr int kWaves = kSortThreads / 64;
-constexpr int kDigits = 256;
+constexpr int kDigitBits = 9;
+constexpr int kDigits = 1 << kDigitBits;
 constexpr int kSmallRounds = 16;
 constexpr int64_t kSmall = kSortThreads * kSmallRounds;  // tokens that one workgroup sorts: 128 KB of LDS
 constexpr int kTileRounds = 4;
-constexpr int64_t kTile = kSortThreads * kTileRounds;
-constexpr int kThreads = 256;
+constexpr int kThreads = 256;  // of the join
+constexpr unsigned kClearGroups = 512;  // of kSortThreads: two to a CU
 
 struct SortLds {
   uint32_t count[kWaves][kDigits];
@@ -50,7 +52,7 @@ __device__ __forceinline__ void places(const uint32_t (&key)[ROUNDS], int digit_
     const uint32_t d = (key[r] >> digit_shift) & (kDigits - 1);
     uint64_t same = ~uint64_t{0};  // the lanes with this digit
 #pragma unroll
-    for (int b = 0; b < 8; ++b) {
+    for (int b = 0; b < kDigitBits; ++b) {
       const uint64_t set = __ballot((d >> b) & 1);
       same &= (d >> b) & 1 ? set : ~set;
     }
@@ -61,11 +63,12 @@ __device__ __forceinline__ void places(const uint32_t (&key)[ROUNDS], int digit_
   }
   __syncthreads();
   // exclusive prefix sums of the counts, digit by digit and within a digit by wavefront:
-  // four counters to a thread
-  const int d = threadIdx.x >> 2, w0 = (threadIdx.x & 3) * 4;
-  uint32_t c[4], sum = 0;
+  // eight counters to a thread
+  static_assert(kWaves * kDigits == kSortThreads * 8, "counters");
+  const int d = threadIdx.x >> 1, w0 = (threadIdx.x & 1) * 8;
+  uint32_t c[8], sum = 0;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
+  for (int i = 0; i < 8; ++i) {
     c[i] = sum;
     sum += lds->count[w0 + i][d];
   }
@@ -80,63 +83,150 @@ __device__ __forceinline__ void places(const uint32_t (&key)[ROUNDS], int digit_
   uint32_t base = upto - sum;
   for (int w = 0; w < wave; ++w) base += lds->wave_total[w];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) lds->count[w0 + i][d] = base + c[i];
+  for (int i = 0; i < 8; ++i) lds->count[w0 + i][d] = base + c[i];
   __syncthreads();
 #pragma unroll
   for (int r = 0; r < ROUNDS; ++r) place[r] += lds->count[wave][(key[r] >> digit_shift) & (kDigits - 1)];
 }
 
-// Clears the tables, workgroup `id` of `of`.
-template <int E, typename Args>
-__device__ __forceinline__ void clear_tables(const Args* a, int64_t id, int64_t of) {
-  const int64_t C = a->C, rows = a->P * a->V;
-  const float zero[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
-  for (int64_t row = id; row < rows; row += of) {
-    const int64_t r = row / a->V, v = row - r * a->V;
-    void* table = a->dtable[r];
-    for (int64_t at = static_cast<int64_t>(threadIdx.x) * 8; at < C; at += kSortThreads * 8)
-      store_run<E>(table, v * a->ldt + at, run_length(at, C), zero);
+// Zeros to a row's columns from `at` on, 16 bytes at most: neighbouring threads write
+// neighbouring 16 bytes, where 8 columns of fp32 to each would leave half of every line to a
+// second store.
+template <int E>
+constexpr int kZeros = 16 / sizeof(typename ElemOf<E>::T);
+
+// STREAM: past the caches, which the sums' reads and writes would otherwise have to empty of
+// zeros first (4 tables of 16384 x 4096 fp32: 285 us, 299 without); tables that the last-level
+// cache holds stay there (50000 x 1024 fp32: 42 us, 52 past it).
+template <int E, bool STREAM>
+__device__ __forceinline__ void clear_run(void* table, int64_t at, int64_t left) {
+  typedef typename ElemOf<E>::T T;
+  T* p = static_cast<T*>(table) + at;
+  if (left >= kZeros<E>) {
+    typedef uint32_t u4 __attribute__((ext_vector_type(4), aligned(2)));
+    if constexpr (STREAM) __builtin_nontemporal_store(u4{0, 0, 0, 0}, reinterpret_cast<u4*>(p));
+    else *reinterpret_cast<u4*>(p) = u4{0, 0, 0, 0};
+  } else {
+    for (int i = 0; i < left; ++i) p[i] = static_cast<T>(0.0f);
   }
 }
 
-// Workgroup 0 sorts up to kSmall tokens; the others clear the tables.
-template <int E>
+// Part `part` of `parts` of clearing the tables, by workgroup `id` of `of`.  Tables whose
+// rows follow each other without a gap are one row each.
+template <int E, bool STREAM, typename Args>
+__device__ __forceinline__ void clear_tables_as(const Args* a, int part, int parts, uint32_t id, uint32_t of) {
+  const bool whole = a->ldt == a->C || a->V == 1;
+  const int64_t C = whole ? a->V * a->C : a->C, V = whole ? 1 : a->V;
+  constexpr int kZ = kZeros<E>;
+  int shift = 0;  // 2^shift threads to a row
+  while ((1 << shift) < kSortThreads && (int64_t{kZ} << shift) < C) ++shift;
+  const int64_t width = int64_t{kZ} << shift, cuts = (C + width - 1) / width, per = kSortThreads >> shift;
+  const int64_t blocks = (V + per - 1) / per, jobs = blocks * cuts * a->P;  // blocks of rows, cut into columns
+  const int64_t lo = jobs * part / parts, hi = jobs * (part + 1) / parts;
+  for (int64_t job = lo + id; job < hi; job += of) {
+    const int64_t cut = job % cuts, block = job / cuts;
+    const int64_t r = block / blocks, v = (block - r * blocks) * per + (threadIdx.x >> shift);
+    const int64_t at = cut * width + (threadIdx.x & ((1 << shift) - 1)) * kZ;
+    if (v < V) clear_run<E, STREAM>(a->dtable[r], v * a->ldt + at, C - at);
+  }
+}
+
+// The two are apart as a whole: the compiler would make one of two stores that differ in
+// their cache policy alone.
+template <int E, typename Args>
+__device__ __forceinline__ void clear_tables(const Args* a, int part, int parts, uint32_t id, uint32_t of) {
+  if (a->stream) clear_tables_as<E, true>(a, part, parts, id, of);
+  else clear_tables_as<E, false>(a, part, parts, id, of);
+}
+
+// Clears the rows that no token has, workgroup `id` of `of`: it takes every `of`-th block of
+// rows, 2^shift threads to a row (64 at most: a row to 1024 threads costs a look at its mark
+// for every store, 323 us in place of 285 in the case below), and marks those of its rows that
+// a token has in LDS, kMarked rows at a time.  Rows that the sums will write are not written
+// twice: at 16384 tokens, 65536 rows of 4096 fp32, a tenth of them.
+constexpr int kMarked = 32 * kSortThreads;
+
+template <int E, bool STREAM, typename Args>
+__device__ __forceinline__ void clear_untouched_as(const Args* a, uint32_t id, uint32_t of, uint32_t* marks) {
+  constexpr int kZ = kZeros<E>;
+  const int64_t C = a->C;
+  const uint32_t V = static_cast<uint32_t>(a->V), rows = static_cast<uint32_t>(a->P) * V;
+  const int shift = embed_shift(C);
+  const int bits = 10 - shift;  // 2^bits rows to a block
+  static_assert(kSortThreads == 1 << 10, "rows of a block");
+  const uint32_t blocks = ((rows - 1) >> bits) + 1, window = kMarked >> bits;
+  for (uint64_t j0 = 0; id + j0 * of < blocks; j0 += window) {
+    marks[threadIdx.x] = 0;
+    __syncthreads();
+    for (int64_t t = threadIdx.x; t < a->T; t += kSortThreads) {
+      const uint32_t k = key_of(a, t), block = k >> bits;
+      if (k >= rows || block % of != id) continue;
+      const uint64_t j = block / of;
+      if (j < j0 || j >= j0 + window) continue;
+      const uint32_t m = static_cast<uint32_t>((j - j0) << bits) + (k & ((1u << bits) - 1));
+      atomicOr(&marks[m >> 5], 1u << (m & 31));
+    }
+    __syncthreads();
+    for (uint32_t j = 0; j < window; ++j) {
+      const uint64_t block = id + (j0 + j) * of;
+      if (block >= blocks) break;
+      const uint32_t in = threadIdx.x >> shift, row = (static_cast<uint32_t>(block) << bits) + in, m = (j << bits) + in;
+      if (row >= rows || (marks[m >> 5] >> (m & 31) & 1)) continue;
+      const uint32_t r = row / V;
+      void* table = a->dtable[r];
+      const int64_t v = (row - r * V) * a->ldt;
+      for (int64_t at = (threadIdx.x & ((1 << shift) - 1)) * kZ; at < C; at += int64_t{kZ} << shift)
+        clear_run<E, STREAM>(table, v + at, C - at);
+    }
+    __syncthreads();
+  }
+}
+
+template <int E, typename Args>
+__device__ __forceinline__ void clear_untouched(const Args* a, uint32_t id, uint32_t of, uint32_t* marks) {
+  if (a->stream) clear_untouched_as<E, true>(a, id, of, marks);
+  else clear_untouched_as<E, false>(a, id, of, marks);
+}
+
+// Workgroup 0 sorts up to 1024 * ROUNDS tokens; the others clear the rows without one.
+template <int E, int ROUNDS>
 __global__ __launch_bounds__(kSortThreads) void echo_embed_sort_k(const EmbedBwdArgs given, int digits, uint32_t* keys,
                                                                   uint32_t* order) {
   __shared__ SortLds lds;
-  __shared__ uint32_t sk[kSmall], so[kSmall];
+  __shared__ uint32_t sk[kSortThreads * ROUNDS];
+  __shared__ uint16_t so[kSortThreads * ROUNDS];
   const auto* a = kernel_args<EmbedBwdArgs>();
   if (blockIdx.x != 0) {
-    clear_tables<E>(a, blockIdx.x - 1, gridDim.x - 1);
+    clear_untouched<E>(a, blockIdx.x - 1, gridDim.x - 1, sk);
     return;
   }
   const int T = static_cast<int>(a->T);
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
-  uint32_t key[kSmallRounds], at[kSmallRounds], place[kSmallRounds];
+  uint32_t key[ROUNDS], at[ROUNDS], place[ROUNDS];
 #pragma unroll
-  for (int r = 0; r < kSmallRounds; ++r) {
-    const int i = (wave * kSmallRounds + r) * 64 + lane;
+  for (int r = 0; r < ROUNDS; ++r) {
+    const int i = (wave * ROUNDS + r) * 64 + lane;
     key[r] = i < T ? key_of(a, i) : ~0u;  // behind every key in every digit
     at[r] = static_cast<uint32_t>(i);
   }
   for (int d = 0; d < digits; ++d) {
-    places(key, 8 * d, &lds, place);
+    places(key, kDigitBits * d, &lds, place);
 #pragma unroll
-    for (int r = 0; r < kSmallRounds; ++r) {
+    for (int r = 0; r < ROUNDS; ++r) {
       sk[place[r]] = key[r];
-      so[place[r]] = at[r];
+      so[place[r]] = static_cast<uint16_t>(at[r]);
     }
     __syncthreads();
 #pragma unroll
-    for (int r = 0; r < kSmallRounds; ++r) {
-      const int i = (wave * kSmallRounds + r) * 64 + lane;
+    for (int r = 0; r < ROUNDS; ++r) {
+      const int i = (wave * ROUNDS + r) * 64 + lane;
       key[r] = sk[i];
       at[r] = so[i];
     }
   }
 #pragma unroll
-  for (int r = 0; r < kSmallRounds; ++r) {
-    const int i = (wave * kSmallRounds + r) * 64 + lane;
+  for (int r = 0; r < ROUNDS; ++r) {
+    const int i = (wave * ROUNDS + r) * 64 + lane;
     if (i < T) {
       keys[i] = key[r];
       order[i] = at[r];
@@ -146,7 +236,7 @@ __global__ __launch_bounds__(kSortThreads) void echo_embed_sort_k(const EmbedBwd
 
 template <int E>
 __global__ __launch_bounds__(kSortThreads) void echo_embed_clear_k(const EmbedBwdArgs given) {
-  clear_tables<E>(kernel_args<EmbedBwdArgs>(), blockIdx.x, gridDim.x);
+  clear_tables<E>(kernel_args<EmbedBwdArgs>(), 0, 1, blockIdx.x, gridDim.x);
 }
 
 // ---- more than kSmall tokens -------------------------------------------------------------
@@ -158,7 +248,7 @@ __device__ __forceinline__ void load_tile(const Args* a, const uint32_t* keys, c
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
 #pragma unroll
   for (int r = 0; r < kTileRounds; ++r) {
-    const int64_t i = blockIdx.x * kTile + (wave * kTileRounds + r) * 64 + lane;
+    const int64_t i = blockIdx.x * kEmbedTile + (wave * kTileRounds + r) * 64 + lane;
     key[r] = ~0u;
     at[r] = static_cast<uint32_t>(i);
     if (i < a->T) {
@@ -168,11 +258,22 @@ __device__ __forceinline__ void load_tile(const Args* a, const uint32_t* keys, c
   }
 }
 
+// Workgroups behind the `work` ones of a launch clear their part of the tables.
+struct Share {
+  uint32_t work;
+  int part, parts;
+};
+
 // counts[digit * tiles + tile]
-__global__ __launch_bounds__(kSortThreads) void echo_embed_count_k(const EmbedBwdArgs given, int shift, const uint32_t* keys,
-                                                                   uint32_t* counts) {
+template <int E>
+__global__ __launch_bounds__(kSortThreads) void echo_embed_count_k(const EmbedBwdArgs given, const Share sh, int shift,
+                                                                   const uint32_t* keys, uint32_t* counts) {
   __shared__ uint32_t n[kDigits];
   const auto* a = kernel_args<EmbedBwdArgs>();
+  if (blockIdx.x >= sh.work) {
+    clear_tables<E>(a, sh.part, sh.parts, blockIdx.x - sh.work, gridDim.x - sh.work);
+    return;
+  }
   if (threadIdx.x < kDigits) n[threadIdx.x] = 0;
   __syncthreads();
   uint32_t key[kTileRounds], at[kTileRounds];
@@ -181,12 +282,18 @@ __global__ __launch_bounds__(kSortThreads) void echo_embed_count_k(const EmbedBw
   for (int r = 0; r < kTileRounds; ++r)
     if (static_cast<int64_t>(at[r]) < a->T) atomicAdd(&n[(key[r] >> shift) & (kDigits - 1)], 1u);
   __syncthreads();
-  if (threadIdx.x < kDigits) counts[threadIdx.x * static_cast<int64_t>(gridDim.x) + blockIdx.x] = n[threadIdx.x];
+  if (threadIdx.x < kDigits) counts[threadIdx.x * static_cast<int64_t>(sh.work) + blockIdx.x] = n[threadIdx.x];
 }
 
 // Exclusive prefix sums in place, one workgroup.
-__global__ __launch_bounds__(kSortThreads) void echo_embed_scan_k(uint32_t* counts, int64_t n) {
+template <int E>
+__global__ __launch_bounds__(kSortThreads) void echo_embed_scan_k(const EmbedBwdArgs given, const Share sh, uint32_t* counts,
+                                                                  int64_t n) {
   __shared__ uint32_t total[kWaves];
+  if (blockIdx.x >= sh.work) {
+    clear_tables<E>(kernel_args<EmbedBwdArgs>(), sh.part, sh.parts, blockIdx.x - sh.work, gridDim.x - sh.work);
+    return;
+  }
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   uint32_t carry = 0;
   for (int64_t lo = 0; lo < n; lo += kSortThreads * 4) {
@@ -217,12 +324,18 @@ __global__ __launch_bounds__(kSortThreads) void echo_embed_scan_k(uint32_t* coun
   }
 }
 
-__global__ __launch_bounds__(kSortThreads) void echo_embed_place_k(const EmbedBwdArgs given, int shift, const uint32_t* keys,
-                                                                   const uint32_t* order, const uint32_t* counts,
-                                                                   uint32_t* keys_to, uint32_t* order_to) {
+template <int E>
+__global__ __launch_bounds__(kSortThreads) void echo_embed_place_k(const EmbedBwdArgs given, const Share sh, int shift,
+                                                                   const uint32_t* keys, const uint32_t* order,
+                                                                   const uint32_t* counts, uint32_t* keys_to,
+                                                                   uint32_t* order_to) {
   __shared__ SortLds lds;
   __shared__ uint32_t start[kDigits];  // the digit's first place in the tile
   const auto* a = kernel_args<EmbedBwdArgs>();
+  if (blockIdx.x >= sh.work) {
+    clear_tables<E>(a, sh.part, sh.parts, blockIdx.x - sh.work, gridDim.x - sh.work);
+    return;
+  }
   uint32_t key[kTileRounds], at[kTileRounds], place[kTileRounds];
   load_tile(a, keys, order, key, at);
   places(key, shift, &lds, place);
@@ -232,10 +345,10 @@ __global__ __launch_bounds__(kSortThreads) void echo_embed_place_k(const EmbedBw
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
 #pragma unroll
   for (int r = 0; r < kTileRounds; ++r) {
-    const int64_t i = blockIdx.x * kTile + (wave * kTileRounds + r) * 64 + lane;
+    const int64_t i = blockIdx.x * kEmbedTile + (wave * kTileRounds + r) * 64 + lane;
     if (i < a->T) {
       const uint32_t d = (key[r] >> shift) & (kDigits - 1);
-      const uint32_t to = counts[d * static_cast<int64_t>(gridDim.x) + blockIdx.x] + place[r] - start[d];
+      const uint32_t to = counts[d * static_cast<int64_t>(sh.work) + blockIdx.x] + place[r] - start[d];
       keys_to[to] = key[r];
       order_to[to] = at[r];
     }
@@ -244,64 +357,136 @@ __global__ __launch_bounds__(kSortThreads) void echo_embed_place_k(const EmbedBw
 
 // ---- sums over runs ----------------------------------------------------------------------
 
-// Tokens to a chunk.
-constexpr int64_t kRun = 32;
+// The columns that thread `lane` of 2^shift has in tile blockIdx.y; all 8 below `lo` where it
+// has none.
+__device__ __forceinline__ Run columns_of(uint32_t lane, int shift, int64_t C) {
+  const uint32_t at = ((blockIdx.y << shift) + lane) * 8;
+  if (static_cast<int64_t>(at) + 8 <= C) return Run{at, 0};
+  return Run{static_cast<uint32_t>(C) - 8, static_cast<int64_t>(at) < C ? static_cast<int>(at + 8 - static_cast<uint32_t>(C)) : 8};
+}
 
 template <int E, typename Args>
-__device__ __forceinline__ void write_row(const Args* a, uint32_t key, int64_t at, int n, const float acc[8]) {
-  const int64_t r = key / a->V, v = key - r * a->V;
+__device__ __forceinline__ void write_row(const Args* a, uint32_t key, Run run, const float acc[8]) {
+  const uint32_t V = static_cast<uint32_t>(a->V), r = key / V, v = key - r * V;
   float o[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) o[i] = acc[i] * a->scale;
-  store_run<E>(a->dtable[r], v * a->ldt + at, n, o);
+  store_from<E>(a->dtable[r], v * a->ldt, run, o);
 }
 
-// 2^shift threads to a chunk's columns.  part: two rows of C to a chunk, for the run that
-// crosses its start and for the one that crosses its end only.
-template <int O, int E>
-__global__ __launch_bounds__(kThreads) void echo_embed_sum_k(const EmbedBwdArgs given, int shift, const uint32_t* keys,
-                                                             const uint32_t* order, float* part) {
+constexpr int kBatch = 8;  // rows in flight to a thread
+constexpr int kSumThreads = 512;
+
+// A workgroup takes the tokens of kSumThreads >> shift consecutive chunks, 2^shift threads (64
+// at most) to a chunk, and 8 << shift columns.  A chunk writes the rows of runs inside it and
+// leaves the sums of its first and last run in LDS; a thread a column then adds those along
+// the chunks.  part: two rows of C to a workgroup, for the run that crosses its start and for
+// the one that crosses its end only.  WAVE: a chunk to a wavefront (shift 6), whose tokens
+// come through scalar loads.
+template <int O, int E, bool WAVE>
+__global__ __launch_bounds__(kSumThreads) void echo_embed_sum_k(const EmbedBwdArgs given, int shift, int length,
+                                                                const uint32_t* __restrict__ keys,
+                                                                const uint32_t* __restrict__ order,
+                                                                float* __restrict__ part) {
+  __shared__ float head[kSumThreads * 8], tail[kSumThreads * 8];
+  __shared__ uint32_t first[kSumThreads], last[kSumThreads];
   const auto* a = kernel_args<EmbedBwdArgs>();
-  const int64_t chunk = (static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x) >> shift, C = a->C, T = a->T;
-  const int64_t at = ((static_cast<int64_t>(blockIdx.y) << shift) + (threadIdx.x & ((1 << shift) - 1))) * 8;
-  const int64_t lo = chunk * kRun, hi = lo + kRun < T ? lo + kRun : T;
-  if (lo >= T || at >= C) return;
+  const int64_t C = a->C, T = a->T;
   const uint32_t none = static_cast<uint32_t>(a->P * a->V);
-  const int n = run_length(at, C);
-  const uint32_t before = lo > 0 ? keys[lo - 1] : ~0u, behind = hi < T ? keys[hi] : ~0u, first = keys[lo];
-  float acc[8];
-  uint32_t cur = first;
+  const int subs = kSumThreads >> shift, width = 8 << shift;
+  uint32_t sub = threadIdx.x >> shift;
+  if constexpr (WAVE) sub = __builtin_amdgcn_readfirstlane(sub);
+  const uint32_t lane = threadIdx.x & ((1u << shift) - 1);
+  const Run run = columns_of(lane, shift, C);
+  const int64_t block = static_cast<int64_t>(blockIdx.x) * subs * length;  // the workgroup's first token
+  const int64_t lo = block + static_cast<int64_t>(sub) * length, hi = lo + length < T ? lo + length : T;
+  if (lo < T) {
+    float acc[8];
+    uint32_t cur = keys[lo];
+    const uint32_t start = cur;
+    if (lane == 0) first[sub] = start;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) acc[i] = 0.0f;
-  for (int64_t i = lo; i < hi; ++i) {
-    const uint32_t k = keys[i];
-    if (k != cur) {
-      if (cur == before) store_run<kElemF32>(part, (2 * chunk) * C + at, n, acc);
-      else write_row<E>(a, cur, at, n, acc);
+    for (int i = 0; i < 8; ++i) acc[i] = 0.0f;
+    const auto leave = [&](float* to) {  // this thread's columns of the tile
 #pragma unroll
-      for (int j = 0; j < 8; ++j) acc[j] = 0.0f;
-      cur = k;
+      for (int i = 0; i < 8; ++i)
+        if (i >= run.lo) to[sub * width + lane * 8 + i - run.lo] = acc[i];
+    };
+    for (int64_t i = lo; i < hi; i += kBatch) {
+      uint32_t k[kBatch];
+      Raw<O> v[kBatch];
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j) {
+        const int64_t t = i + j < hi ? i + j : hi - 1;
+        k[j] = keys[t];
+        load_any<O>(a->dout, order[t] * a->lddo, run, &v[j]);
+      }
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j) {
+        if (i + j >= hi) break;
+        if (k[j] != cur) {
+          if (cur == start) leave(head);
+          else if (run.lo < 8) write_row<E>(a, cur, run, acc);
+#pragma unroll
+          for (int n = 0; n < 8; ++n) acc[n] = 0.0f;
+          cur = k[j];
+        }
+        float w[8];
+        widen<O>(v[j], w);
+#pragma unroll
+        for (int n = 0; n < 8; ++n) acc[n] = acc[n] + w[n];
+      }
     }
-    if (k == none) return;  // nothing but tokens without a row from here on
-    float v[8];
-    load_run<O>(a->dout, order[i] * a->lddo + at, n, v);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) acc[j] = acc[j] + v[j];
+    leave(cur == start ? head : tail);
+    if (lane == 0) last[sub] = cur;
   }
-  if (cur == before) store_run<kElemF32>(part, (2 * chunk) * C + at, n, acc);
-  else if (cur == behind) store_run<kElemF32>(part, (2 * chunk + 1) * C + at, n, acc);
-  else write_row<E>(a, cur, at, n, acc);
+  __syncthreads();
+  const int64_t col = static_cast<int64_t>(blockIdx.y) * width + threadIdx.x;
+  if (static_cast<int>(threadIdx.x) >= width || col >= C) return;
+  const int64_t end = block + static_cast<int64_t>(subs) * length;
+  const uint32_t before = block > 0 ? keys[block - 1] : ~0u, behind = end < T ? keys[end] : ~0u;
+  const auto put = [&](uint32_t key, float sum, bool at_end) {
+    if (key == none) return;  // tokens without a row
+    if (key == before) {
+      part[2 * blockIdx.x * C + col] = sum;
+    } else if (at_end && key == behind) {
+      part[(2 * blockIdx.x + 1) * C + col] = sum;
+    } else {
+      const uint32_t V = static_cast<uint32_t>(a->V), r = key / V, v = key - r * V;
+      store1<E>(a->dtable[r], v * a->ldt + col, sum * a->scale);
+    }
+  };
+  uint32_t cur = first[0];
+  float sum = 0.0f;
+  for (int s = 0; s < subs && block + static_cast<int64_t>(s) * length < T; ++s) {
+    const uint32_t f = first[s], l = last[s];
+    if (f != cur) {
+      put(cur, sum, false);
+      cur = f;
+      sum = 0.0f;
+    }
+    sum = sum + head[s * width + threadIdx.x];
+    if (l != f) {
+      put(cur, sum, false);
+      cur = l;
+      sum = tail[s * width + threadIdx.x];
+    }
+  }
+  put(cur, sum, true);
 }
 
-// The runs that cross chunks: the chunk where one starts adds up its parts.
+// The runs that cross workgroups of the sums, `length` tokens to each: the one where a run
+// starts adds up its parts.  2^shift threads to its columns.
 template <int E>
-__global__ __launch_bounds__(kThreads) void echo_embed_join_k(const EmbedBwdArgs given, int shift, const uint32_t* keys,
-                                                              const float* part) {
+__global__ __launch_bounds__(kThreads) void echo_embed_join_k(const EmbedBwdArgs given, int shift, int64_t length,
+                                                              const uint32_t* __restrict__ keys,
+                                                              const float* __restrict__ part) {
   const auto* a = kernel_args<EmbedBwdArgs>();
-  const int64_t chunk = (static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x) >> shift, C = a->C, T = a->T;
-  const int64_t at = ((static_cast<int64_t>(blockIdx.y) << shift) + (threadIdx.x & ((1 << shift) - 1))) * 8;
-  const int64_t lo = chunk * kRun, hi = lo + kRun;
-  if (hi >= T || at >= C) return;
+  const int64_t C = a->C, T = a->T;
+  const int64_t group = static_cast<int64_t>(blockIdx.x) * (kThreads >> shift) + (threadIdx.x >> shift);
+  const Run run = columns_of(threadIdx.x & ((1u << shift) - 1), shift, C);
+  const int64_t lo = group * length, hi = lo + length;
+  if (hi >= T || run.lo == 8) return;
   const uint32_t k = keys[hi - 1];
   if (k == static_cast<uint32_t>(a->P * a->V) || keys[hi] != k) return;
   if (keys[lo] == k && lo > 0 && keys[lo - 1] == k) return;  // it starts further up
@@ -312,80 +497,104 @@ __global__ __launch_bounds__(kThreads) void echo_embed_join_k(const EmbedBwdArgs
     if (keys[m] == k) b = m + 1;
     else e = m;
   }
-  const int n = run_length(at, C);
+  const int64_t last = (b - 1) / length;
+  Raw<kElemF32> v[kBatch];
   float acc[8];
-  load_run<kElemF32>(part, (2 * chunk + 1) * C + at, n, acc);
-  const int64_t last = (b - 1) / kRun;
-  for (int64_t c = chunk + 1; c <= last; ++c) {
-    float v[8];
-    load_run<kElemF32>(part, (2 * c) * C + at, n, v);
+  load_any<kElemF32>(part, (2 * group + 1) * C, run, &v[0]);
+  widen<kElemF32>(v[0], acc);
+  for (int64_t c = group + 1; c <= last; c += kBatch) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) acc[i] = acc[i] + v[i];
+    for (int j = 0; j < kBatch; ++j) load_any<kElemF32>(part, 2 * (c + j < last ? c + j : last) * C, run, &v[j]);
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) {
+      if (c + j > last) break;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) acc[i] = acc[i] + v[j].v[i];
+    }
   }
-  write_row<E>(a, k, at, n, acc);
+  write_row<E>(a, k, run, acc);
 }
 
-size_t align256(size_t n) { return (n + 255) & ~size_t{255}; }
+template <bool WAVE, int O, int E>
+hipError_t launch_sums(const EmbedBwdArgs& a, int shift, const uint32_t* keys, const uint32_t* order, float* part,
+                       hipStream_t s) {
+  const int64_t runs = (a.C + 7) / 8, length = embed_chunk(a.T), group = length * (kSumThreads >> shift);
+  const int64_t groups = (a.T + group - 1) / group;
+  hipLaunchKernelGGL((echo_embed_sum_k<O, E, WAVE>),
+                     dim3(static_cast<unsigned>(groups), static_cast<unsigned>((runs + (1 << shift) - 1) >> shift)),
+                     dim3(kSumThreads), 0, s, a, shift, static_cast<int>(length), keys, order, part);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess || groups == 1) return e;
+  int js = shift;
+  while (js < 8 && (int64_t{1} << js) < runs) ++js;
+  const int64_t per = kThreads >> js;
+  hipLaunchKernelGGL((echo_embed_join_k<E>),
+                     dim3(static_cast<unsigned>((groups + per - 1) / per), static_cast<unsigned>((runs + (1 << js) - 1) >> js)),
+                     dim3(kThreads), 0, s, a, js, group, keys, part);
+  return hipGetLastError();
+}
 
-int64_t tiles_of(int64_t T) { return (T + kTile - 1) / kTile; }
+// More than kSmall tokens.  *in: which of the two buffers they end in.
+template <int E>
+hipError_t launch_sort(const EmbedBwdArgs& a, int digits, uint32_t* const keys[2], uint32_t* const order[2], uint32_t* counts,
+                       int* in, hipStream_t s) {
+  const unsigned tiles = static_cast<unsigned>(embed_tiles(a.T));
+  hipError_t e;
+  Share sh{tiles, 0, 3 * digits};
+  for (int d = 0; d < digits; ++d, *in ^= 1) {
+    const uint32_t *k = d == 0 ? nullptr : keys[*in], *o = d == 0 ? nullptr : order[*in];
+    const int shift = kDigitBits * d;
+    hipLaunchKernelGGL(echo_embed_count_k<E>, dim3(tiles + kClearGroups), dim3(kSortThreads), 0, s, a, sh, shift, k, counts);
+    if ((e = hipGetLastError()) != hipSuccess) return e;
+    ++sh.part;
+    sh.work = 1;
+    hipLaunchKernelGGL(echo_embed_scan_k<E>, dim3(1 + kClearGroups), dim3(kSortThreads), 0, s, a, sh, counts,
+                       tiles * int64_t{kDigits});
+    if ((e = hipGetLastError()) != hipSuccess) return e;
+    ++sh.part;
+    sh.work = tiles;
+    hipLaunchKernelGGL(echo_embed_place_k<E>, dim3(tiles + kClearGroups), dim3(kSortThreads), 0, s, a, sh, shift, k, o, counts,
+                       keys[*in ^ 1], order[*in ^ 1]);
+    if ((e = hipGetLastError()) != hipSuccess) return e;
+    ++sh.part;
+  }
+  return hipSuccess;
+}
 
 }  // namespace
 
-// Two pairs of keys and places, the tiles' counts, the parts of the chunks.
-size_t embed_workspace(int64_t T, int64_t C) {
-  if (T == 0) return 0;
-  return 4 * align256(static_cast<size_t>(T) * 4) + align256(static_cast<size_t>(tiles_of(T)) * kDigits * 4) +
-         static_cast<size_t>((T + kRun - 1) / kRun) * 2 * static_cast<size_t>(C) * sizeof(float);
-}
-
-hipError_t launch_embed_bwd(const EmbedBwdArgs& a, Elem dout, Elem table, hipStream_t s) {
-  const int64_t T = a.T, n_rows = a.P * a.V;
-  const unsigned fill = static_cast<unsigned>(n_rows < 2048 ? n_rows : 2048);
-  char* w = static_cast<char*>(a.workspace);
-  uint32_t *keys[2], *order[2];
-  for (int i = 0; i < 2; ++i) {
-    keys[i] = reinterpret_cast<uint32_t*>(w);
-    w += align256(static_cast<size_t>(T) * 4);
-    order[i] = reinterpret_cast<uint32_t*>(w);
-    w += align256(static_cast<size_t>(T) * 4);
-  }
-  uint32_t* counts = reinterpret_cast<uint32_t*>(w);
-  float* part = reinterpret_cast<float*>(w + align256(static_cast<size_t>(tiles_of(T)) * kDigits * 4));
-  int digits = 1;  // of keys 0 .. n_rows
-  while (digits < 4 && (n_rows >> (8 * digits)) != 0) ++digits;
+hipError_t launch_embed_bwd(const EmbedBwdArgs& given, Elem dout, Elem table, hipStream_t s) {
+  EmbedBwdArgs a = given;
+  a.stream = a.P * a.V * a.C * (table == kElemF32 ? 4 : 2) >= int64_t{256} << 20;
+  const int64_t T = a.T;
+  const EmbedLayout w = embed_layout(T, a.C);
+  char* base = static_cast<char*>(a.workspace);
+  uint32_t* const keys[2] = {reinterpret_cast<uint32_t*>(base + w.keys[0]), reinterpret_cast<uint32_t*>(base + w.keys[1])};
+  uint32_t* const order[2] = {reinterpret_cast<uint32_t*>(base + w.order[0]), reinterpret_cast<uint32_t*>(base + w.order[1])};
+  int digits = 1;  // of keys 0 .. P V
+  while (((a.P * a.V) >> (kDigitBits * digits)) != 0) ++digits;
   int in = 0;
+  const int64_t elems = a.P * a.V * a.C, want = (elems + kSortThreads * 8 - 1) / (kSortThreads * 8);
+  const unsigned clear = static_cast<unsigned>(want < kClearGroups - 1 ? want : kClearGroups - 1);
   return with_types(dout, dout, table, [&](auto O, auto, auto E) -> hipError_t {
-    hipError_t e;
-    if (T == 0 || T > kSmall) {
-      hipLaunchKernelGGL((echo_embed_clear_k<E()>), dim3(fill), dim3(kSortThreads), 0, s, a);
-      if ((e = hipGetLastError()) != hipSuccess || T == 0) return e;
-      const unsigned tiles = static_cast<unsigned>(tiles_of(T));
-      for (int d = 0; d < digits; ++d, in ^= 1) {
-        const uint32_t *k = d == 0 ? nullptr : keys[in], *o = d == 0 ? nullptr : order[in];
-        hipLaunchKernelGGL(echo_embed_count_k, dim3(tiles), dim3(kSortThreads), 0, s, a, 8 * d, k, counts);
-        if ((e = hipGetLastError()) != hipSuccess) return e;
-        hipLaunchKernelGGL(echo_embed_scan_k, dim3(1), dim3(kSortThreads), 0, s, counts, tiles * int64_t{kDigits});
-        if ((e = hipGetLastError()) != hipSuccess) return e;
-        hipLaunchKernelGGL(echo_embed_place_k, dim3(tiles), dim3(kSortThreads), 0, s, a, 8 * d, k, o, counts, keys[in ^ 1],
-                           order[in ^ 1]);
-        if ((e = hipGetLastError()) != hipSuccess) return e;
-      }
-    } else {
-      hipLaunchKernelGGL((echo_embed_sort_k<E()>), dim3(1 + fill), dim3(kSortThreads), 0, s, a, digits, keys[0], order[0]);
-      if ((e = hipGetLastError()) != hipSuccess) return e;
-    }
-    const int64_t runs = (a.C + 7) / 8, chunks = (T + kRun - 1) / kRun;
-    int shift = 0;
-    while (shift < 8 && (int64_t{1} << shift) < runs) ++shift;
-    const int64_t per = kThreads >> shift;
-    const dim3 grid(static_cast<unsigned>((chunks + per - 1) / per), static_cast<unsigned>((runs + (1 << shift) - 1) >> shift));
-    hipLaunchKernelGGL((echo_embed_sum_k<O(), E()>), grid, dim3(kThreads), 0, s, a, shift, keys[in], order[in], part);
-    if ((e = hipGetLastError()) != hipSuccess) return e;
-    if (chunks > 1) {
-      hipLaunchKernelGGL((echo_embed_join_k<E()>), grid, dim3(kThreads), 0, s, a, shift, keys[in], part);
-      e = hipGetLastError();
-    }
-    return e;
+    hipError_t e = hipSuccess;
+    if (T == 0)
+      hipLaunchKernelGGL((echo_embed_clear_k<E()>), dim3(clear), dim3(kSortThreads), 0, s, a);
+    else if (T <= kSortThreads)
+      hipLaunchKernelGGL((echo_embed_sort_k<E(), 1>), dim3(1 + clear), dim3(kSortThreads), 0, s, a, digits, keys[0], order[0]);
+    else if (T <= 4 * kSortThreads)
+      hipLaunchKernelGGL((echo_embed_sort_k<E(), 4>), dim3(1 + clear), dim3(kSortThreads), 0, s, a, digits, keys[0], order[0]);
+    else if (T <= kSmall)
+      hipLaunchKernelGGL((echo_embed_sort_k<E(), kSmallRounds>), dim3(1 + (clear < 255 ? clear : 255)), dim3(kSortThreads), 0, s, a, digits, keys[0],
+                         order[0]);
+    else
+      e = launch_sort<E()>(a, digits, keys, order, reinterpret_cast<uint32_t*>(base + w.counts), &in, s);
+    if (e == hipSuccess) e = hipGetLastError();
+    if (e != hipSuccess || T == 0) return e;
+    const int shift = embed_shift(a.C);
+    float* part = reinterpret_cast<float*>(base + w.part);
+    return shift == 6 ? launch_sums<true, O(), E()>(a, shift, keys[in], order[in], part, s)
+                      : launch_sums<false, O(), E()>(a, shift, keys[in], order[in], part, s);
   });
 }
 

@@ -118,7 +118,7 @@ echo_status check_tensors(const void* const* src, void* const* dst, const int64_
   for (int64_t i = 0; i < count; ++i) {
     if (!known(dtypes[i])) return ECHO_ERR_DTYPE;
     if (n[i] < 0 || n[i] > kMaxElems) return ECHO_ERR_SHAPE;
-    chunks += echo::clip_chunks(n[i]);
+    chunks += echo::clip_chunks(n[i] * bytes_of(dtypes[i]));
     if (chunks >= int64_t{1} << 31) return ECHO_ERR_SHAPE;
     if (n[i] == 0) continue;
     const uintptr_t es = static_cast<uintptr_t>(bytes_of(dtypes[i]));
@@ -164,30 +164,53 @@ echo_status tensors_apart(const void* const* src, void* const* dst, const int64_
   return ok ? ECHO_OK : ECHO_ERR_ARG;
 }
 
-// Fills the launches' arguments, kClipTensors tensors at a time, and hands each to f.
-template <typename F>
+// Fills the arguments of one launch after the other and hands each to f.
+template <typename Args, typename F>
 echo_status for_launches(const void* const* src, void* const* dst, const int64_t* n, const int32_t* dtypes, int64_t count,
                          F f) {
-  echo::ClipArgs a;
+  Args a;
   a.tensors = 0;
   uint32_t chunks = 0;
   for (int64_t i = 0; i <= count; ++i) {
-    if (a.tensors == echo::kClipTensors || (i == count && a.tensors > 0)) {
+    if (a.tensors == Args::kTensors || (i == count && a.tensors > 0)) {
       a.first[a.tensors] = chunks;
-      const hipError_t e = f(a);
-      if (e != hipSuccess) return ECHO_ERR_HIP;
+      if (f(a) != hipSuccess) return ECHO_ERR_HIP;
       a.tensors = 0;
       chunks = 0;
     }
     if (i == count || n[i] == 0) continue;
+    const int64_t bytes = n[i] * bytes_of(dtypes[i]);
     a.src[a.tensors] = src[i];
-    a.dst[a.tensors] = dst != nullptr ? dst[i] : nullptr;
-    a.n[a.tensors] = n[i];
-    a.elem[a.tensors] = static_cast<uint8_t>(dtypes[i]);
+    if (sizeof(a.dst) > sizeof(void*)) a.dst[a.tensors] = dst[i];
+    a.tail[a.tensors] = echo::clip_tail(bytes, dtypes[i]);
     a.first[a.tensors++] = chunks;
-    chunks += static_cast<uint32_t>(echo::clip_chunks(n[i]));
+    chunks += static_cast<uint32_t>(echo::clip_chunks(bytes));
   }
   return ECHO_OK;
+}
+
+// The tensors' squares, as *n_part partial sums.
+echo_status launch_sums(const void* const* src, const int64_t* n, const int32_t* dtypes, int64_t count, double* part,
+                        int64_t* n_part, hipStream_t s) {
+  *n_part = 0;
+  return for_launches<echo::ClipInPlace>(src, nullptr, n, dtypes, count, [&](const echo::ClipInPlace& a) {
+    const hipError_t e = echo::launch_clip_sum(a, part + *n_part, s);
+    *n_part += echo::clip_grid(a.first[a.tensors]);
+    return e;
+  });
+}
+
+template <typename Args>
+echo_status launch_scales(const void* const* src, void* const* dst, const int64_t* n, const int32_t* dtypes, int64_t count,
+                          const double* part, int64_t n_part, double max_norm, float* norm, hipStream_t s) {
+  int64_t bytes = 0;
+  for (int64_t i = 0; i < count; ++i) bytes += n[i] * bytes_of(dtypes[i]);
+  const bool stream = bytes >= echo::kClipStream;
+  return for_launches<Args>(src, dst, n, dtypes, count, [&](const Args& a) {
+    const hipError_t e = echo::launch_clip_scale(a, part, n_part, max_norm, norm, stream, s);
+    norm = nullptr;  // the first launch writes it
+    return e;
+  });
 }
 
 echo_status check_clip_workspace(int64_t count, const void* workspace, size_t bytes) {
@@ -319,7 +342,7 @@ echo_status echo_block_norm_backward(const echo_block* b, const void* out, int64
 
 size_t echo_clip_workspace(int64_t n_tensors) {
   if (n_tensors < 1 || n_tensors > (int64_t{1} << 24)) return 0;
-  const int64_t launches = (n_tensors + echo::kClipTensors - 1) / echo::kClipTensors;
+  const int64_t launches = (n_tensors + echo::ClipInPlace::kTensors - 1) / echo::ClipInPlace::kTensors;
   return static_cast<size_t>(launches) * echo::kClipGroups * sizeof(double);
 }
 
@@ -332,14 +355,8 @@ echo_status echo_grad_norm(const void* const* grads, const int64_t* numel, const
   if ((e = tensors_apart(grads, nullptr, numel, dtypes, n_tensors, norm)) != ECHO_OK) return e;
   const hipStream_t s = static_cast<hipStream_t>(stream);
   double* part = static_cast<double*>(workspace);
-  int64_t n_part = 0;
-  e = for_launches(grads, nullptr, numel, dtypes, n_tensors, [&](const echo::ClipArgs& a) {
-    int64_t used = 0;
-    const hipError_t r = echo::launch_clip_sum(a, part, n_part, &used, s);
-    n_part += used;
-    return r;
-  });
-  if (e != ECHO_OK) return e;
+  int64_t n_part;
+  if ((e = launch_sums(grads, numel, dtypes, n_tensors, part, &n_part, s)) != ECHO_OK) return e;
   return status_of(echo::launch_clip_norm(part, n_part, norm, s));
 }
 
@@ -355,21 +372,13 @@ echo_status echo_clip_grads(const void* const* grads, void* const* out, const in
   if ((e = tensors_apart(grads, out, numel, dtypes, n_tensors, norm)) != ECHO_OK) return e;
   const hipStream_t s = static_cast<hipStream_t>(stream);
   double* part = static_cast<double*>(workspace);
-  int64_t n_part = 0;
-  e = for_launches(grads, out, numel, dtypes, n_tensors, [&](const echo::ClipArgs& a) {
-    int64_t used = 0;
-    const hipError_t r = echo::launch_clip_sum(a, part, n_part, &used, s);
-    n_part += used;
-    return r;
-  });
-  if (e != ECHO_OK) return e;
+  int64_t n_part;
+  if ((e = launch_sums(grads, numel, dtypes, n_tensors, part, &n_part, s)) != ECHO_OK) return e;
   if (n_part == 0) return status_of(echo::launch_clip_norm(part, 0, norm, s));
-  float* to = norm;
-  return for_launches(grads, out, numel, dtypes, n_tensors, [&](const echo::ClipArgs& a) {
-    const hipError_t r = echo::launch_clip_scale(a, part, n_part, max_norm, to, s);
-    to = nullptr;
-    return r;
-  });
+  bool in_place = true;
+  for (int64_t i = 0; i < n_tensors && in_place; ++i) in_place = numel[i] == 0 || grads[i] == out[i];
+  return in_place ? launch_scales<echo::ClipInPlace>(grads, out, numel, dtypes, n_tensors, part, n_part, max_norm, norm, s)
+                  : launch_scales<echo::ClipApart>(grads, out, numel, dtypes, n_tensors, part, n_part, max_norm, norm, s);
 }
 
 echo_status echo_embed(const void* const* tables, const void* tokens, void* const* out, int32_t P, int64_t rows,
@@ -409,7 +418,7 @@ echo_status echo_embed(const void* const* tables, const void* tokens, void* cons
 
 size_t echo_embed_workspace(int64_t n_tokens, int64_t cols) {
   if (n_tokens < 1 || cols < 1 || n_tokens > (int64_t{1} << 27) || cols > echo::kStepMaxCols) return 0;
-  return echo::embed_workspace(n_tokens, cols);
+  return echo::embed_layout(n_tokens, cols).bytes;
 }
 
 echo_status echo_embed_backward(const void* dout, const void* tokens, void* const* dtables, int32_t P, int64_t rows,

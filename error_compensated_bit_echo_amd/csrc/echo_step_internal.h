@@ -105,24 +105,41 @@ inline size_t block_norm_workspace(int64_t R, int64_t C, int64_t n_gates) {
 }
 hipError_t launch_block_norm_bwd(const BlockNormBwdArgs& a, Elem x, Elem y, Elem out_a, hipStream_t s);
 
-// Gradient clipping: a launch takes up to kClipTensors tensors in its arguments.
-constexpr int kClipTensors = 120;
+// Gradient clipping: a launch takes its tensors in its arguments, cut into chunks of kClipChunk
+// bytes (the last of each may be shorter), so a tensor is a pointer, its first chunk, and 16
+// bits of its last chunk's length and its type; where the result goes elsewhere, a second
+// pointer.  4 KB of arguments hold 176 tensors, or 280 where there is one pointer each.
+constexpr int64_t kClipChunk = 32768;
 constexpr int kClipGroups = 2048;  // workgroups, and partial sums, of a launch at most
+template <int N, bool APART>
 struct ClipArgs {
-  const void* src[kClipTensors];
-  void* dst[kClipTensors];
-  int64_t n[kClipTensors];
-  uint32_t first[kClipTensors + 1];  // the tensor's first chunk
-  uint8_t elem[kClipTensors];
+  static constexpr int kTensors = N;
+  const void* src[N];
+  void* dst[APART ? N : 1];  // APART false: src itself
+  uint32_t first[N + 1];     // the tensor's first chunk
+  uint16_t tail[N];          // last chunk: bytes / 2 - 1, and Elem in the upper two bits
   int32_t tensors;
 };
-// chunks of a tensor of n elements
-int64_t clip_chunks(int64_t n);
-// part: kClipGroups doubles a launch, filled from `at` on; *used: how many it wrote
-hipError_t launch_clip_sum(const ClipArgs& a, double* part, int64_t at, int64_t* used, hipStream_t s);
-// norm: written (by the first of several launches) if not nullptr
-hipError_t launch_clip_scale(const ClipArgs& a, const double* part, int64_t n_part, double max_norm, float* norm,
-                             hipStream_t s);
+typedef ClipArgs<280, false> ClipInPlace;
+typedef ClipArgs<176, true> ClipApart;
+inline int64_t clip_chunks(int64_t bytes) { return (bytes + kClipChunk - 1) / kClipChunk; }
+inline uint16_t clip_tail(int64_t bytes, int32_t elem) {
+  const int64_t last = bytes - (clip_chunks(bytes) - 1) * kClipChunk;
+  return static_cast<uint16_t>((last / 2 - 1) | elem << 14);
+}
+inline unsigned clip_grid(uint32_t chunks) {
+  return chunks < static_cast<uint32_t>(kClipGroups) ? chunks : static_cast<unsigned>(kClipGroups);
+}
+// part: a partial sum for each of clip_grid(chunks) workgroups
+hipError_t launch_clip_sum(const ClipInPlace& a, double* part, hipStream_t s);
+// Results go past the caches where the tensors and they do not fit the last-level cache
+// together (64 MB of fp32 in 16 tensors; 256 MB: 153 us, 123 past them).
+constexpr int64_t kClipStream = int64_t{128} << 20;
+// norm: written if not nullptr
+hipError_t launch_clip_scale(const ClipInPlace& a, const double* part, int64_t n_part, double max_norm, float* norm,
+                             bool stream, hipStream_t s);
+hipError_t launch_clip_scale(const ClipApart& a, const double* part, int64_t n_part, double max_norm, float* norm,
+                             bool stream, hipStream_t s);
 hipError_t launch_clip_norm(const double* part, int64_t n_part, float* norm, hipStream_t s);
 
 struct EmbedArgs {
@@ -142,9 +159,52 @@ struct EmbedBwdArgs {
   int64_t V, C, ldt, T, lddo, first;
   float scale;
   int32_t P, wide;
-  void* workspace;  // embed_workspace(...) bytes, 256-byte aligned
+  int32_t stream;   // set by the launcher: zeros go past the caches
+  void* workspace;  // embed_layout(...).bytes, 256-byte aligned
 };
-size_t embed_workspace(int64_t T, int64_t C);
+
+constexpr int64_t kEmbedTile = 4096;  // tokens of a tile of the sort
+inline int64_t embed_tiles(int64_t T) { return (T + kEmbedTile - 1) / kEmbedTile; }
+
+// 2^embed_shift threads, 64 at most, take the columns of a row, 8 each and as often as needed.
+__host__ __device__ inline int embed_shift(int64_t C) {
+  int shift = 0;
+  while (shift < 6 && (int64_t{8} << shift) < C) ++shift;
+  return shift;
+}
+
+// Sorted tokens to a chunk: 8 for few tokens, so that none waits for another; more for many,
+// since runs over many chunks are added up chunk by chunk.
+inline int64_t embed_chunk(int64_t T) {
+  if (T <= 4096) return 8;
+  int64_t n = 16;
+  while (T > n * 8192) n *= 2;
+  return n;
+}
+
+// Where the workspace's parts lie: two pairs of keys and places, the tiles' counts of 512
+// digits, two rows of fp32 for every 512 threads' worth of chunks.
+struct EmbedLayout {
+  size_t keys[2], order[2], counts, part, bytes;
+};
+inline EmbedLayout embed_layout(int64_t T, int64_t C) {
+  EmbedLayout w{};
+  const auto take = [&w](size_t n) {
+    const size_t at = w.bytes;
+    w.bytes += (n + 255) & ~size_t{255};
+    return at;
+  };
+  if (T == 0) return w;
+  const int buffers = T > 4 * kEmbedTile ? 2 : 1;  // one workgroup sorts 16384 tokens in place
+  for (int i = 0; i < buffers; ++i) {
+    w.keys[i] = take(static_cast<size_t>(T) * 4);
+    w.order[i] = take(static_cast<size_t>(T) * 4);
+  }
+  if (buffers == 2) w.counts = take(static_cast<size_t>(embed_tiles(T)) * 512 * 4);
+  const int64_t group = embed_chunk(T) * (512 >> embed_shift(C)), groups = (T + group - 1) / group;
+  w.part = take(static_cast<size_t>(groups) * 2 * static_cast<size_t>(C) * sizeof(float));
+  return w;
+}
 hipError_t launch_embed_bwd(const EmbedBwdArgs& a, Elem dout, Elem table, hipStream_t s);
 
 }  // namespace echo

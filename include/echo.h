@@ -506,8 +506,8 @@ size_t echo_clip_workspace(int64_t n_tensors);
  * any mix, any alignment of the element type, lengths of 0 allowed).  Squares and
  * sums are held in 64 bits, in an order that the lengths fix.  norm lies in none
  * of the tensors; tensors may overlap each other.
- * n_tensors: at most 2^24; numel: 2^40; below 2^31 chunks of 16384 elements in
- * all.  workspace: 8-byte aligned.  A launch for every 120 tensors, and one more.
+ * n_tensors: at most 2^24; numel: 2^40; below 2^31 chunks of 32 KiB in all.
+ * workspace: 8-byte aligned.  A launch for every 280 tensors, and one more.
  * Errors: ECHO_ERR_ARG, ECHO_ERR_SHAPE, ECHO_ERR_DTYPE, ECHO_ERR_WORKSPACE (also
  * where the host has no memory for the check of overlaps), ECHO_ERR_HIP. */
 echo_status echo_grad_norm(const void* const* grads, const int64_t* numel, const int32_t* dtypes, int64_t n_tensors,
@@ -519,8 +519,9 @@ echo_status echo_grad_norm(const void* const* grads, const int64_t* numel, const
  * an fp32 operation, rounded once to the tensor's type.  An infinite norm gives f
  * = 0 (and NaN where the element is infinite), a NaN makes every element NaN.
  * out_i may be g_i itself (it is not touched then where f is 1) and overlaps no
- * other tensor.  max_norm: finite, at least 0.  Two launches for every 120
- * tensors.  Limits, workspace and errors as above. */
+ * other tensor.  max_norm: finite, at least 0.  A launch for every 280 tensors,
+ * and one for every 176 (280 where all are scaled in place).  Limits, workspace
+ * and errors as above. */
 echo_status echo_clip_grads(const void* const* grads, void* const* out, const int64_t* numel, const int32_t* dtypes,
                             int64_t n_tensors, double max_norm, float* norm, void* workspace, size_t workspace_bytes,
                             echo_stream_t stream);

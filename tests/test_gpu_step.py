@@ -289,8 +289,8 @@ def test_clip_many_tensors_of_mixed_types_at_any_element(E):
     """More tensors than a launch takes, lying next to each other in one buffer."""
     import torch
     g, rng = gen(2), np.random.default_rng(3)
-    for count in (119, 120, 121, 240, 500):
-        bufs = {t: torch.randn(1 << 18, generator=g, device="cuda").to(dt(t)) for t in ("f32", "bf16", "f16")}
+    for count in (175, 176, 177, 280, 281, 700):
+        bufs = {t: torch.randn(1 << 19, generator=g, device="cuda").to(dt(t)) for t in ("f32", "bf16", "f16")}
         at, grads = dict.fromkeys(bufs, 0), []
         for _ in range(count):
             t, n = ("f32", "bf16", "f16")[rng.integers(3)], int(rng.integers(0, 900))

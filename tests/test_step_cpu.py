@@ -153,7 +153,7 @@ def test_clip_refusals(want, kw):
 def test_clip_workspace():
     size = B.echo_clip_workspace
     assert size(0) == 0 and size(-1) == 0 and size((1 << 24) + 1) == 0
-    assert size(1) == size(120) > 0 and size(121) == 2 * size(1)
+    assert size(1) == size(280) > 0 and size(281) == 2 * size(1)
 
 
 TOK = 21 * G
