@@ -34,9 +34,16 @@ weight gradients, runs in 8-bit floating point with a scale per 128 elements
 bfloat16 and reduced by Echo as before, and weight gradients come in fp32.
 ``dropout`` puts a dropout on each reduced output before it joins the residual
 stream, with a mask that both passes draw from a counter-based generator.
+
+Around the blocks, a stack can have learned norms before and after each block
+with a gate and a scaled residual (``block_norms``; the end of a block and the
+start of the next are one kernel), an embedding whose vocabulary is split over
+the ranks and whose partials go through the same all-reduce (``vocab``), and
+train_step can clip the gradients of all its shards by their common norm.
 """
 from __future__ import annotations
 
+import math
 from typing import List, Optional
 
 from . import binding as B
@@ -310,9 +317,9 @@ def _fns():
         def forward(ctx, x, residual, p: float, rng, offset: int, first: int):
             ctx.save_for_backward(rng)
             ctx.args, ctx.x_dtype = (p, offset, first), x.dtype
-            out = torch.empty_like(residual, memory_format=torch.contiguous_format)
-            return B.echo_dropout_add(x.contiguous(), out, p, rng, residual=residual.contiguous(), offset=offset,
-                                      first=first)
+            out = torch.empty_like(x if residual is None else residual, memory_format=torch.contiguous_format)
+            return B.echo_dropout_add(x.contiguous(), out, p, rng, residual=None if residual is None else
+                                      residual.contiguous(), offset=offset, first=first)
 
         @staticmethod
         @once
@@ -326,7 +333,68 @@ def _fns():
                 B.echo_dropout_add(grad, dx, p, rng, offset=offset, first=first)
             return dx, grad if ctx.needs_input_grad[1] else None, None, None, None, None
 
-    return ReduceForward, ReduceBackward, RowParallelEcho, ColumnParallelEcho, RowParallelFp8, ColumnParallelFp8, DropoutAdd
+    def gradient(ctx, i, like):
+        """An empty gradient of input i, None where it is not wanted."""
+        return torch.empty_like(like, memory_format=torch.contiguous_format) if ctx.needs_input_grad[i] else None
+
+    class BlockNorm(torch.autograd.Function):
+        """The end of a block and the start of the next (see echo_block_norm): (out, a), out
+        alone without ``a_dtype``, a alone without ``y``.  The stored out is all that is kept
+        beside the inputs."""
+
+        @staticmethod
+        def forward(ctx, x, y, gate, w_post, w_pre, options, a_dtype):
+            x, y = x.contiguous(), None if y is None else y.contiguous()
+            out = None if y is None else torch.empty_like(x)
+            a = None if a_dtype is None else torch.empty_like(x, dtype=a_dtype)
+            B.echo_block_norm(x, out, a, y=y, gate=gate, w_post=w_post, w_pre=w_pre, **options)
+            ctx.save_for_backward(x if out is None else out, y, gate, w_post, w_pre)
+            ctx.options = options
+            ctx.set_materialize_grads(False)
+            return a if out is None else out if a is None else (out, a)
+
+        @staticmethod
+        @once
+        def backward(ctx, *grads):
+            out, y, gate, w_post, w_pre = ctx.saved_tensors
+            grads = [None if g is None else g.contiguous() for g in grads]
+            dout, da = grads if len(grads) == 2 else (None, grads[0]) if y is None else (grads[0], None)
+            if dout is None and da is None:
+                return (None,) * 7
+            dx = gradient(ctx, 0, out)
+            dy, dgate, dw_post, dw_pre = (None if t is None else gradient(ctx, i, t)
+                                          for i, t in ((1, y), (2, gate), (3, w_post), (4, w_pre)))
+            if da is None:  # the next block's input was not used
+                dw_pre = None if dw_pre is None else dw_pre.zero_()
+            B.echo_block_norm_backward(out, dout=dout, da=da, dx=dx, y=y, dy=dy, gate=gate, dgate=dgate, w_post=w_post,
+                                       dw_post=dw_post, w_pre=None if da is None else w_pre,
+                                       dw_pre=None if da is None else dw_pre, **ctx.options)
+            return dx, dy, dgate, dw_post, dw_pre, None, None
+
+    class VocabEmbed(torch.autograd.Function):
+        """The all-reduce, on the forward state, of every rank's bfloat16 partial embedding
+        (see echo_embed); the rounding passes gradients straight through."""
+
+        @staticmethod
+        def forward(ctx, group: "EchoGroup", tokens, scale: float, *tables):
+            tokens = tokens.contiguous()
+            shape = (tokens.numel(), tables[0].shape[1])
+            parts = [torch.empty(shape, dtype=torch.bfloat16, device=t.device) for t in tables]
+            B.echo_embed(tables, tokens, parts, scale=scale)
+            ctx.save_for_backward(tokens)
+            ctx.scale, ctx.like = scale, [(t.shape, t.dtype) for t in tables]
+            return group.allreduce([p.view(-1) for p in parts], B.ECHO_FWD).view(tokens.shape + shape[1:])
+
+        @staticmethod
+        @once
+        def backward(ctx, grad):
+            (tokens,) = ctx.saved_tensors
+            d = [torch.empty(shape, dtype=dtype, device=grad.device) for shape, dtype in ctx.like]
+            B.echo_embed_backward(grad.contiguous().view(tokens.numel(), -1), tokens, d, scale=ctx.scale)
+            return (None, None, None) + tuple(d)
+
+    return (ReduceForward, ReduceBackward, RowParallelEcho, ColumnParallelEcho, RowParallelFp8, ColumnParallelFp8, DropoutAdd,
+            BlockNorm, VocabEmbed)
 
 
 _FNS = None
@@ -372,13 +440,50 @@ def column_parallel_fp8(group: "EchoGroup", a, ws, w8):
 
 
 def dropout_add(x, residual, p: float, rng, offset: int = 0, first: int = 0):
-    """residual + dropout(x), differentiable in both; the mask is drawn from ``rng``
-    (int64 device tensor: key, step), ``offset`` and ``first`` in both passes
-    (see echo_dropout_add)."""
+    """residual + dropout(x), differentiable in both (``residual`` None: dropout(x));
+    the mask is drawn from ``rng`` (int64 device tensor: key, step), ``offset`` and
+    ``first`` in both passes (see echo_dropout_add)."""
     global _FNS
     if _FNS is None:
         _FNS = _fns()
     return _FNS[6].apply(x, residual, p, rng, offset, first)
+
+
+def block_norm(x, y=None, gate=None, w_post=None, w_pre=None, *, post_norm: bool = False, residual_scale: float = 1.0,
+               weight_offset: float = 0.0, eps: float = 1e-6, a: bool = True, a_dtype=None):
+    """(out, a): out = residual_scale * x + gate * n, n = rmsnorm(y) * (weight_offset + w_post)
+    or y, and a = rmsnorm(out) * (weight_offset + w_pre) of ``a_dtype`` (x's by default),
+    differentiable in x, y, gate and the weights (see echo_block_norm).  Without ``y`` out is
+    x; ``a`` false: a is None."""
+    global _FNS
+    if _FNS is None:
+        _FNS = _fns()
+    if y is None and not a:
+        raise ValueError("neither a block's output nor a norm")
+    options = dict(post_norm=post_norm, residual_scale=residual_scale, weight_offset=weight_offset, eps=eps)
+    got = _FNS[7].apply(x, y, gate, w_post, w_pre, options, (a_dtype or x.dtype) if a else None)
+    return (x, got) if y is None else got if a else (got, None)
+
+
+def vocab_embed(group: "EchoGroup", tables, tokens, scale: float = 1.0):
+    """The embedding [.., H] of ``tokens`` from P tables [rows, H] that hold consecutive
+    stretches of the vocabulary: their partials through Echo's forward state (fp32),
+    differentiable in the tables.  Tokens outside the vocabulary give zeros."""
+    global _FNS
+    if _FNS is None:
+        _FNS = _fns()
+    return _FNS[8].apply(group, tokens, scale, *tables)
+
+
+def clip_grads(grads, max_norm: float):
+    """Scales ``grads`` in place so that the norm of all of them together is at most
+    ``max_norm``; returns the norm before (one float32 element, see echo_clip_grads)."""
+    import torch
+
+    grads = [g.detach() for g in grads]
+    if not grads:
+        raise ValueError("no gradients")
+    return B.echo_clip_grads(grads, max_norm, torch.empty(1, dtype=torch.float32, device=grads[0].device))
 
 
 def quantize_weights_fp8(ws, backward: bool = True):
@@ -423,10 +528,16 @@ class TPMLPStack:
     point (any sizes).  ``dropout``: probability with which an element of a reduced
     output is dropped before the residual add while ``training`` is set; the masks
     come from ``rng`` (key ``seed``, step), layer l's from step + l, and train_step
-    moves the step on by the number of layers."""
+    moves the step on by the number of layers.
+
+    ``block_norms``: x <- residual_scale * x + gate * rmsnorm(y) * w_post, a = rmsnorm(x) *
+    w_pre, with a gate and two weights [H] per layer that start at 1; a dropout then
+    applies to y.  ``vocab``: an embedding of that many rows (rounded up to a multiple of
+    P) in P stretches, times sqrt(H); forward then takes tokens too."""
 
     def __init__(self, layers: int, hidden: int, ffn: int, P: int, seed: int = 0, device=None,
-                 product: str = "f32", dropout: float = 0.0):
+                 product: str = "f32", dropout: float = 0.0, block_norms: bool = False, residual_scale: float = 1.0,
+                 vocab: int = 0):
         import torch
 
         if ffn % P:
@@ -435,7 +546,12 @@ class TPMLPStack:
             raise ValueError(f"product {product!r}")
         if not 0.0 <= dropout <= 1.0 - 2.0 ** -16:  # what echo_dropout_add takes
             raise ValueError(f"dropout {dropout!r}")
+        if not math.isfinite(residual_scale) or (residual_scale != 1.0 and not block_norms):
+            raise ValueError(f"residual_scale {residual_scale!r} (block_norms {block_norms!r})")
+        if vocab < 0:
+            raise ValueError(f"vocab {vocab!r}")
         self.L, self.H, self.F, self.P, self.product = layers, hidden, ffn, P, product
+        self.block_norms, self.residual_scale = block_norms, residual_scale
         dev = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
         self.dropout, self.training = dropout, True
         self.rng = torch.tensor([seed, 0], dtype=torch.int64, device=dev) if dropout > 0 else None
@@ -449,52 +565,78 @@ class TPMLPStack:
                             for r in range(P)])
             self.w2.append([w2[r * ffn // P:(r + 1) * ffn // P, :].contiguous().requires_grad_()
                             for r in range(P)])
+        ones = lambda: [torch.ones(hidden, device=dev).requires_grad_() for _ in range(layers)] if block_norms else []
+        self.w_pre, self.w_post, self.gate = ones(), ones(), ones()
+        self.tables = [(torch.randn(-(-vocab // P), hidden, generator=g, device=dev) / hidden ** 0.5).requires_grad_()
+                       for _ in range(P)] if vocab else []
 
     def parameters(self):
-        return [w for layer in self.w1 + self.w2 for w in layer]
+        return [w for layer in self.w1 + self.w2 for w in layer] + self.w_pre + self.w_post + self.gate + self.tables
 
     def quantize_weights(self):
         """The weights of every layer in 8 bits, for ``forward(..., weights8=...)`` as long
         as they do not change; without it a forward pass quantizes them itself."""
         return [(quantize_weights_fp8(w1), quantize_weights_fp8(w2)) for w1, w2 in zip(self.w1, self.w2)]
 
+    def _block(self, l: int, a, shape, group: EchoGroup, weights8):
+        """The reduced output of layer l's block for its normalised input."""
+        import torch
+
+        gelu = torch.nn.functional.gelu
+        if self.product == "fp8":
+            w8 = weights8[l] if weights8 is not None else [quantize_weights_fp8(w, torch.is_grad_enabled())
+                                                           for w in (self.w1[l], self.w2[l])]
+            pres = column_parallel_fp8(group, a, self.w1[l], w8[0])
+            # gelu in fp32 of the bfloat16 pre-activations
+            return row_parallel_fp8(group, [gelu(p.float()) for p in pres], self.w2[l], shape, w8[1])
+        if self.product == "f32":
+            xs = replicate(group, a)
+            hs = [gelu(xs[r] @ self.w1[l][r]) for r in range(self.P)]
+            partials = [(hs[r] @ self.w2[l][r]).to(torch.bfloat16) for r in range(self.P)]
+            return reduce_forward(group, [p.reshape(-1) for p in partials], shape)
+        pres = column_parallel_echo(group, a, self.w1[l], self.product == "bf16_fused")
+        return row_parallel_echo(group, [gelu(p) for p in pres], self.w2[l], shape, self.product == "bf16_fused")
+
     def forward(self, x, group: EchoGroup, weights8=None):
+        """``x``: the residual stream [T, H], or tokens [T] where there is a vocabulary."""
         import torch
 
         if weights8 is not None and self.product != "fp8":
             raise ValueError("weights8 goes with product 'fp8'")
-        gelu = torch.nn.functional.gelu
+        if not x.is_floating_point():
+            if not self.tables:
+                raise ValueError("tokens need a vocabulary")
+            x = vocab_embed(group, self.tables, x, self.H ** 0.5)
+        drop = self.dropout > 0 and self.training
+        if self.block_norms:
+            a = block_norm(x, w_pre=self.w_pre[0])[1] if self.L else None
+            for l in range(self.L):
+                y = self._block(l, a, x.shape, group, weights8)
+                if drop:
+                    y = dropout_add(y, None, self.dropout, self.rng, offset=l)
+                more = l + 1 < self.L
+                x, a = block_norm(x, y, self.gate[l], self.w_post[l], self.w_pre[l + 1] if more else None, post_norm=True,
+                                  residual_scale=self.residual_scale, a=more)
+            return x
         for l in range(self.L):
             a = x * torch.rsqrt(x.pow(2).mean(dim=-1, keepdim=True) + 1e-6)
-            if self.product == "fp8":
-                w8 = weights8[l] if weights8 is not None else [quantize_weights_fp8(w, torch.is_grad_enabled())
-                                                               for w in (self.w1[l], self.w2[l])]
-                pres = column_parallel_fp8(group, a, self.w1[l], w8[0])
-                # gelu in fp32 of the bfloat16 pre-activations
-                y = row_parallel_fp8(group, [gelu(p.float()) for p in pres], self.w2[l], x.shape, w8[1])
-            elif self.product == "f32":
-                xs = replicate(group, a)
-                hs = [gelu(xs[r] @ self.w1[l][r]) for r in range(self.P)]
-                partials = [(hs[r] @ self.w2[l][r]).to(torch.bfloat16) for r in range(self.P)]
-                y = reduce_forward(group, [p.reshape(-1) for p in partials], x.shape)
-            else:
-                pres = column_parallel_echo(group, a, self.w1[l], self.product == "bf16_fused")
-                hs = [gelu(p) for p in pres]
-                y = row_parallel_echo(group, hs, self.w2[l], x.shape, self.product == "bf16_fused")
-            if self.dropout > 0 and self.training:
-                x = dropout_add(y, x, self.dropout, self.rng, offset=l)
-            else:
-                x = x + y
+            y = self._block(l, a, x.shape, group, weights8)
+            x = dropout_add(y, x, self.dropout, self.rng, offset=l) if drop else x + y
         return x
 
 
-def train_step(model: TPMLPStack, group: EchoGroup, x0, target, weights8=None):
-    """One forward + backward; returns (loss, dL/dx0, [dL/dW...]).  ``weights8``: the
-    weights in 8 bits (quantize_weights), for several steps before they change."""
+def train_step(model: TPMLPStack, group: EchoGroup, x0, target, weights8=None, max_norm=None):
+    """One forward + backward; returns (loss, dL/dx0, [dL/dW...]).  ``x0``: the residual
+    stream, or tokens (dL/dx0 is None).  ``weights8``: the weights in 8 bits
+    (quantize_weights), for several steps before they change.  ``max_norm``: the gradients
+    of the parameters are clipped to that norm together, and the norm before is returned too,
+    as a fourth value."""
     import torch
 
     group.reset()
-    x = x0.detach().clone().requires_grad_()
+    x = x0.detach().clone()
+    if x.is_floating_point():
+        x.requires_grad_()
     for p in model.parameters():
         p.grad = None
     y = model.forward(x, group, weights8=weights8)
@@ -502,4 +644,6 @@ def train_step(model: TPMLPStack, group: EchoGroup, x0, target, weights8=None):
     loss.backward()
     if model.rng is not None and model.training:
         model.rng[1] += model.L  # the next step draws other masks
-    return loss.detach(), x.grad.detach(), [p.grad.detach() for p in model.parameters()]
+    grads = [p.grad.detach() for p in model.parameters()]
+    result = loss.detach(), None if x.grad is None else x.grad.detach(), grads
+    return result if max_norm is None else result + (clip_grads(grads, max_norm),)
