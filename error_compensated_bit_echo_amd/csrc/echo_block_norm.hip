@@ -51,8 +51,7 @@ __global__ __launch_bounds__(MAXT) void echo_block_norm_k(const BlockNormArgs a,
           float y[8];
           widen<Y>(ry[k], y);
           clear_below(run[k].lo, y);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) s[0] = s[0] + y[i] * y[i];
+          s[0] = dot8(y, y, s[0]);
         }
         block_sums(s, &lds, &turn);
         rs = reciprocal_rms(s[0], a.p);
@@ -91,8 +90,7 @@ __global__ __launch_bounds__(MAXT) void echo_block_norm_k(const BlockNormArgs a,
 #pragma unroll
     for (int k = 0; k < RUNS; ++k) {
       clear_below(run[k].lo, v[k]);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) s[0] = s[0] + v[k][i] * v[k][i];
+      s[0] = dot8(v[k], v[k], s[0]);
     }
     block_sums(s, &lds, &turn);
     const float rs = reciprocal_rms(s[0], a.p);

@@ -90,7 +90,6 @@ __global__ __launch_bounds__(kMaxThreads) void echo_block_norm_bwd_k(const Block
   const int64_t C = a.p.C;
   const Run run = run_of(0, C);
   const uint32_t at = run.at;
-  const float cols = static_cast<float>(C);
   const int e = a.p.elem;
   const Rows rows = rows_of(a, sp);
   RawRow<X, Y, A> next;
@@ -123,21 +122,19 @@ __global__ __launch_bounds__(kMaxThreads) void echo_block_norm_bwd_k(const Block
     widen<X>(raw.s, s);
     clear_below(run.lo, s);
     float m[3] = {0.0f, 0.0f, 0.0f};
-#pragma unroll
-    for (int i = 0; i < 8; ++i) m[0] = m[0] + s[i] * s[i];
+    m[0] = dot8(s, s, 0.0f);
     if (a.da != nullptr) {
       float da[8];
       widen<A>(raw.da, da);
       clear_below(run.lo, da);
       pre.get(w);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) m[1] = m[1] + da[i] * w[i] * s[i];
+      for (int i = 0; i < 8; ++i) m[1] = __builtin_fmaf(da[i] * w[i], s[i], m[1]);
     }
     if (a.y != nullptr) {
       widen<Y>(raw.y, y);
       clear_below(run.lo, y);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) m[2] = m[2] + y[i] * y[i];
+      m[2] = dot8(y, y, 0.0f);
     }
     block_sums(m, &lds, &turn);
 #pragma unroll
@@ -151,11 +148,11 @@ __global__ __launch_bounds__(kMaxThreads) void echo_block_norm_bwd_k(const Block
       widen<A>(raw.da, da);
       clear_below(run.lo, da);
       pre.get(w);
-      const float rs = reciprocal_rms(m[0], a.p), k = rs * rs * (m[1] / cols);
+      const float rs = reciprocal_rms(m[0], a.p), k = rs * rs * (m[1] * a.p.inv_cols);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        t[i] = t[i] + rs * (da[i] * w[i] - s[i] * k);
-        acc[kSumPre][i] = acc[kSumPre][i] + da[i] * (s[i] * rs);
+        t[i] = __builtin_fmaf(rs, __builtin_fmaf(da[i], w[i], -(s[i] * k)), t[i]);
+        acc[kSumPre][i] = __builtin_fmaf(da[i], s[i] * rs, acc[kSumPre][i]);
       }
     }
     if (a.dx != nullptr) {
@@ -178,19 +175,19 @@ __global__ __launch_bounds__(kMaxThreads) void echo_block_norm_bwd_k(const Block
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const float yh = y[i] * ry, dn = gate[i] * t[i];
-        acc[kSumGate][i] = acc[kSumGate][i] + t[i] * (yh * w[i]);
-        acc[kSumPost][i] = acc[kSumPost][i] + dn * yh;
+        acc[kSumGate][i] = __builtin_fmaf(t[i], yh * w[i], acc[kSumGate][i]);
+        acc[kSumPost][i] = __builtin_fmaf(dn, yh, acc[kSumPost][i]);
         t[i] = dn * w[i];
-        q[0] = q[0] + t[i] * y[i];
+        q[0] = __builtin_fmaf(t[i], y[i], q[0]);
       }
       block_sums(q, &lds, &turn);
-      const float k = ry * ry * (q[0] / cols);
+      const float k = ry * ry * (q[0] * a.p.inv_cols);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) t[i] = ry * (t[i] - y[i] * k);
+      for (int i = 0; i < 8; ++i) t[i] = ry * __builtin_fmaf(-y[i], k, t[i]);
     } else {
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        acc[kSumGate][i] = acc[kSumGate][i] + t[i] * y[i];
+        acc[kSumGate][i] = __builtin_fmaf(t[i], y[i], acc[kSumGate][i]);
         t[i] = gate[i] * t[i];
       }
     }
@@ -213,7 +210,7 @@ __global__ __launch_bounds__(kMaxThreads) void echo_block_norm_bwd_k(const Block
 // rs(out), its square times mean(u out), rs(y), its square times mean(v y)
 __device__ __forceinline__ float4 stats_of(const BlockNormBwdArgs& a, const float m[3]) {
   const float rs = reciprocal_rms(m[0], a.p), ry = a.p.post ? reciprocal_rms(m[2], a.p) : 1.0f;
-  return make_float4(rs, rs * rs * (m[1] / static_cast<float>(a.p.C)), ry, 0.0f);
+  return make_float4(rs, rs * rs * (m[1] * a.p.inv_cols), ry, 0.0f);
 }
 
 // A thread's share of the three sums, from its 8 columns.
@@ -261,7 +258,7 @@ __device__ __forceinline__ void stream_gradient(const BlockNormBwdArgs& a, const
     clear_below(lo, da);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      t[i] = t[i] + st.x * (da[i] * pre[i] - s[i] * st.y);
+      t[i] = __builtin_fmaf(st.x, __builtin_fmaf(da[i], pre[i], -(s[i] * st.y)), t[i]);
       dw[i] = da[i] * (s[i] * st.x);
     }
   }
@@ -329,7 +326,7 @@ __global__ __launch_bounds__(kMaxThreads) void echo_block_norm_stats_k(const Blo
       q[0] = q[0] + post_product<X, Y, A>(a, raw[k], r[k], run.lo, st);
     }
     block_sums(q, &lds, &turn);
-    st.w = st.z * st.z * (q[0] / static_cast<float>(C));
+    st.w = st.z * st.z * (q[0] * a.p.inv_cols);
   }
   if (threadIdx.x == 0) a.stats[row] = st;
 }
@@ -362,7 +359,7 @@ __global__ __launch_bounds__(kMaxThreads) void echo_block_norm_stats_long_k(cons
         q[0] = q[0] + post_product<X, Y, A>(a, raw, r, run.lo, st);
       }
       block_sums(q, &lds, &turn);
-      st.w = st.z * st.z * (q[0] / static_cast<float>(C));
+      st.w = st.z * st.z * (q[0] * a.p.inv_cols);
     }
     if (threadIdx.x == 0) a.stats[row] = st;
   }
@@ -414,9 +411,9 @@ __global__ __launch_bounds__(kColumnTile / 8) void echo_block_norm_cols_k(const 
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const float yh = y[i] * st.z, dn = gate[i] * t[i];
-      acc[kSumGate][i] = acc[kSumGate][i] + t[i] * (yh * post[i]);
-      acc[kSumPost][i] = acc[kSumPost][i] + dn * yh;
-      w[i] = st.z * (dn * post[i] - y[i] * st.w);
+      acc[kSumGate][i] = __builtin_fmaf(t[i], yh * post[i], acc[kSumGate][i]);
+      acc[kSumPost][i] = __builtin_fmaf(dn, yh, acc[kSumPost][i]);
+      w[i] = st.z * __builtin_fmaf(dn, post[i], -(y[i] * st.w));
     }
     if (a.dy != nullptr) store_from<Y>(a.dy, row * a.lddy, run, w);
     if (sp.chunks == 0 && a.dgate != nullptr && (row + 1) % a.p.rows_per_gate == 0) {

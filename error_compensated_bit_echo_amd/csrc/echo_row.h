@@ -12,21 +12,21 @@ namespace {
 
 constexpr int kMaxWaves = kMaxThreads / 64;
 
-template <int CTRL>
+// Another lane's value; 0 in the rows that ROWS leaves out.
+template <int CTRL, int ROWS = 0xF>
 __device__ __forceinline__ float dpp(float v) {
-  return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, 0xF, 0xF, true));
+  return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, ROWS, 0xF, ROWS == 0xF));
 }
 
-// The sum over the wavefront's 64 lanes, in every lane: four exchanges within rows of 16
-// lanes, then the four rows' sums through scalar registers.  All lanes are active.
+// The sum over the wavefront's 64 lanes, in lane 63: four exchanges within rows of 16 lanes,
+// then row to row.  All lanes are active.
 __device__ __forceinline__ float wave_sum(float v) {
   v = v + dpp<0xB1>(v);   // quad_perm [1, 0, 3, 2]
   v = v + dpp<0x4E>(v);   // quad_perm [2, 3, 0, 1]
   v = v + dpp<0x141>(v);  // row_half_mirror
   v = v + dpp<0x140>(v);  // row_mirror
-  const int b = __float_as_int(v);
-  return (__int_as_float(__builtin_amdgcn_readlane(b, 0)) + __int_as_float(__builtin_amdgcn_readlane(b, 16))) +
-         (__int_as_float(__builtin_amdgcn_readlane(b, 32)) + __int_as_float(__builtin_amdgcn_readlane(b, 48)));
+  v = v + dpp<0x142, 0xA>(v);  // row_bcast:15 into rows 1 and 3
+  return v + dpp<0x143, 0xC>(v);  // row_bcast:31 into rows 2 and 3
 }
 
 // Sums of N values over the workgroup, in every thread.  Consecutive calls alternate
@@ -43,11 +43,15 @@ __device__ __forceinline__ void block_sums(float (&v)[N], Slots<M>* lds, int* tu
   const int waves = static_cast<int>(blockDim.x) >> 6;
 #pragma unroll
   for (int i = 0; i < N; ++i) v[i] = wave_sum(v[i]);
-  if (waves == 1) return;
+  if (waves == 1) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v[i]), 63));
+    return;
+  }
   const int slot = *turn;
   *turn ^= 1;
   const int wave = static_cast<int>(threadIdx.x) >> 6, lane = static_cast<int>(threadIdx.x) & 63;
-  if (lane == 0) {
+  if (lane == 63) {
 #pragma unroll
     for (int i = 0; i < N; ++i) lds->v[slot][i][wave] = v[i];
   }
@@ -102,6 +106,13 @@ __device__ __forceinline__ void store_run(int elem, void* base, int64_t at, int 
 template <int E>
 __device__ __forceinline__ float stored(float v) {
   return static_cast<float>(narrow<E>(v));
+}
+
+// s plus the products of 8 pairs.
+__device__ __forceinline__ float dot8(const float a[8], const float b[8], float s) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) s = __builtin_fmaf(a[i], b[i], s);
+  return s;
 }
 
 __device__ __forceinline__ float sum8(const float v[8]) {
@@ -213,9 +224,10 @@ __device__ __forceinline__ void load_any(int elem, const void* base, int64_t row
   }
 }
 
-// Zeros in place of the elements that are other threads'.
+// Zeros in place of the elements that are other threads'.  The branch is the wavefront's, on
+// a scalar: most hold whole runs alone.
 __device__ __forceinline__ void clear_below(int lo, float v[8]) {
-  if (lo > 0) {
+  if (__ballot(lo > 0) != 0) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] = i < lo ? 0.0f : v[i];
   }
@@ -251,9 +263,15 @@ __device__ __forceinline__ void load_weight(const BlockParams& p, const void* w,
   for (int i = 0; i < 8; ++i) v[i] = v[i] + p.offset;
 }
 
-// 1 / sqrt(mean of the squares + eps)
+// 1 / sqrt(mean of the squares + eps), by the reciprocal root's instruction (1 ulp; what is
+// under the root is at least 2^-126): the exact division and root are 60 instructions, as
+// many as a row's 8 columns take.
 __device__ __forceinline__ float reciprocal_rms(float squares, const BlockParams& p) {
-  return 1.0f / sqrtf(squares / static_cast<float>(p.C) + p.eps);
+#if defined(__HIP_DEVICE_COMPILE__)
+  return __builtin_amdgcn_rsqf(__builtin_fmaf(squares, p.inv_cols, p.eps));
+#else
+  return 0.0f;
+#endif
 }
 
 }  // namespace

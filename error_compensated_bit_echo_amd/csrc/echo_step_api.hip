@@ -99,6 +99,7 @@ echo::BlockParams params_of(const echo_block& b, const Mat& gate) {
   p.alpha = static_cast<float>(b.residual_scale);
   p.offset = static_cast<float>(b.weight_offset);
   p.eps = static_cast<float>(b.eps);
+  p.inv_cols = static_cast<float>(1.0 / static_cast<double>(b.cols));
   p.elem = b.param_dtype;
   p.post = b.post_norm;
   return p;

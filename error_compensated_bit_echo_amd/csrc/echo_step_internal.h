@@ -19,7 +19,7 @@ struct BlockParams {
   const void* w_pre;   // nullptr: 1
   int64_t ldg, n_gates, rows_per_gate;  // n_gates 1 without a gate
   int64_t R, C;
-  float alpha, offset, eps;
+  float alpha, offset, eps, inv_cols;  // inv_cols: 1 / C
   int32_t elem;  // Elem of gate, w_post and w_pre
   int32_t post;  // y is normalised
 };

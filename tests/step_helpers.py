@@ -36,10 +36,10 @@ def depth(C):
 
 def rs_error(C):
     """Relative error of 1 / sqrt(mean of squares + eps): each square is rounded and passes `depth`
-    additions (all terms positive, so their errors are relative to the sum); the division and the
-    addition of eps make two more roundings; the root halves all that and rounds, the reciprocal
-    rounds."""
-    return ((depth(C) + 3) / 2 + 2) * U
+    additions (all terms positive, so their errors are relative to the sum); 1 / C, the product with
+    it and the addition of eps make three more roundings; the root halves all that, and its
+    instruction is off by one unit in the last place at most, two half steps."""
+    return ((depth(C) + 4) / 2 + 2) * U
 
 
 def rs(v, eps):
