@@ -24,7 +24,7 @@ __global__ __launch_bounds__(MAXT) void echo_block_norm_k(const BlockNormArgs a,
   const int e = a.p.elem;
   {
     const int64_t row = row0 + blockIdx.x;
-    const int64_t gate_row = a.p.gate != nullptr ? row / a.p.rows_per_gate * a.p.ldg : 0;
+    const int64_t gate_row = a.p.gate != nullptr ? gate_of(a.p, row) * a.p.ldg : 0;
     Run run[RUNS];
     Raw<X> rx[RUNS];
     Raw<Y> ry[RUNS];
@@ -147,7 +147,7 @@ __global__ __launch_bounds__(kMaxThreads) void echo_block_norm_long_k(const Bloc
           for (int i = 0; i < 8; ++i) y[i] = y[i] * rs * w[i];
         }
         if (a.p.gate != nullptr) {
-          load_run(a.p.elem, a.p.gate, row / a.p.rows_per_gate * a.p.ldg + at, n, w);
+          load_run(a.p.elem, a.p.gate, gate_of(a.p, row) * a.p.ldg + at, n, w);
 #pragma unroll
           for (int i = 0; i < 8; ++i) y[i] = y[i] * w[i];
         }

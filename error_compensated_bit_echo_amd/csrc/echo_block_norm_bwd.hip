@@ -22,17 +22,18 @@ __device__ __forceinline__ float* part_at(const BlockNormBwdArgs& a, int64_t gro
   return a.part + (group * kSums + sum) * a.p.C;
 }
 
-// The rows of workgroup blockIdx.x.
+// The rows of workgroup blockIdx.x, and the gate of the first.  Row numbers fit 32 bits, whose
+// divisions are a quarter of those in 64.
 struct Rows {
-  int64_t lo, hi, step;
+  int64_t lo, hi, step, gate;
 };
 __device__ __forceinline__ Rows rows_of(const BlockNormBwdArgs& a, const BlockSplit& sp) {
   if (sp.chunks != 0) {
-    const int64_t g = blockIdx.x / sp.chunks, c = blockIdx.x % sp.chunks;
-    return Rows{g * a.p.rows_per_gate + c, (g + 1) * a.p.rows_per_gate, sp.chunks};
+    const uint32_t chunks = static_cast<uint32_t>(sp.chunks), g = blockIdx.x / chunks;
+    return Rows{g * a.p.rows_per_gate + (blockIdx.x - g * chunks), (g + 1) * a.p.rows_per_gate, sp.chunks, g};
   }
   const int64_t lo = blockIdx.x * sp.rows, hi = lo + sp.rows;
-  return Rows{lo, hi < a.p.R ? hi : a.p.R, 1};
+  return Rows{lo, hi < a.p.R ? hi : a.p.R, 1, blockIdx.x * sp.gates};
 }
 
 // A row's inputs as they are loaded.
@@ -96,28 +97,24 @@ __global__ __launch_bounds__(kMaxThreads) void echo_block_norm_bwd_k(const Block
   next.load(a, rows.lo, at);
   float acc[kSums][8];
   {
-    RawParam r[2];
+    RawParam r[3];
     float w[8];
     if (a.p.w_pre != nullptr) load_raw(e, a.p.w_pre, 0, at, &r[0]);
     if (a.p.w_post != nullptr) load_raw(e, a.p.w_post, 0, at, &r[1]);
+    if (a.p.gate != nullptr) load_raw(e, a.p.gate, rows.gate * a.p.ldg, at, &r[2]);
     factor_of(e, a.p.w_pre != nullptr, a.p.offset, r[0], run.lo, w);
     pre.put(w);
     factor_of(e, a.p.w_post != nullptr, a.p.offset, r[1], run.lo, w);
     post.put(w);
+    factor_of(e, a.p.gate != nullptr, 0.0f, r[2], run.lo, w);
+    gates.put(w);
   }
+  int64_t gate_row = rows.gate, gate_left = a.p.rows_per_gate;  // of whole gates
 #pragma unroll
   for (int i = 0; i < 8; ++i) acc[kSumPre][i] = acc[kSumPost][i] = acc[kSumGate][i] = 0.0f;
   for (int64_t row = rows.lo; row < rows.hi; row += rows.step) {
     const RawRow<X, Y, A> raw = next;
     if (row + rows.step < rows.hi) next.load(a, row + rows.step, at);  // in flight while this row is worked on
-    if (a.p.gate != nullptr && (row == rows.lo || (sp.chunks == 0 && row % a.p.rows_per_gate == 0))) {
-      RawParam r;
-      float w[8];
-      load_raw(e, a.p.gate, row / a.p.rows_per_gate * a.p.ldg, at, &r);
-      widen(e, r, w);
-      clear_below(run.lo, w);
-      gates.put(w);
-    }
     float s[8], t[8], y[8], w[8];
     widen<X>(raw.s, s);
     clear_below(run.lo, s);
@@ -162,12 +159,7 @@ __global__ __launch_bounds__(kMaxThreads) void echo_block_norm_bwd_k(const Block
     }
     if (a.y == nullptr) continue;
     float gate[8];
-    if (a.p.gate != nullptr) {
-      gates.get(gate);
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) gate[i] = 1.0f;
-    }
+    gates.get(gate);
     if (a.p.post) {
       const float ry = reciprocal_rms(m[2], a.p);
       float q[1] = {0.0f};
@@ -192,11 +184,19 @@ __global__ __launch_bounds__(kMaxThreads) void echo_block_norm_bwd_k(const Block
       }
     }
     if (a.dy != nullptr) store_from<Y>(a.dy, row * a.lddy, run, t);
-    if (sp.chunks == 0 && a.dgate != nullptr && (row + 1) % a.p.rows_per_gate == 0) {
+    if (sp.chunks == 0 && --gate_left == 0) {
       // the last row of a gate that is this workgroup's alone
-      store_from(e, a.dgate, row / a.p.rows_per_gate * a.lddg, run, acc[kSumGate]);
+      if (a.dgate != nullptr) store_from(e, a.dgate, gate_row * a.lddg, run, acc[kSumGate]);
 #pragma unroll
       for (int i = 0; i < 8; ++i) acc[kSumGate][i] = 0.0f;
+      ++gate_row;
+      gate_left = a.p.rows_per_gate;
+      if (a.p.gate != nullptr && row + 1 < rows.hi) {
+        RawParam r;
+        load_raw(e, a.p.gate, gate_row * a.p.ldg, at, &r);
+        factor_of(e, true, 0.0f, r, run.lo, gate);
+        gates.put(gate);
+      }
     }
   }
   if (a.dw_pre != nullptr) store_from<kElemF32>(part_at(a, blockIdx.x, kSumPre), 0, run, acc[kSumPre]);
@@ -322,7 +322,7 @@ __global__ __launch_bounds__(kMaxThreads) void echo_block_norm_stats_k(const Blo
 #pragma unroll
     for (int k = 0; k < kRuns; ++k) {
       const Run run = run_of(k, C);
-      load_params(a, row / a.p.rows_per_gate, run.at, r[k]);
+      load_params(a, gate_of(a.p, row), run.at, r[k]);
       q[0] = q[0] + post_product<X, Y, A>(a, raw[k], r[k], run.lo, st);
     }
     block_sums(q, &lds, &turn);
@@ -355,7 +355,7 @@ __global__ __launch_bounds__(kMaxThreads) void echo_block_norm_stats_long_k(cons
       for (int k = 0; k < runs; ++k) {
         const Run run = any_run_of(k, C);
         raw.load_any(a, row, run);
-        load_any_params(a, row / a.p.rows_per_gate, run, r);
+        load_any_params(a, gate_of(a.p, row), run, r);
         q[0] = q[0] + post_product<X, Y, A>(a, raw, r, run.lo, st);
       }
       block_sums(q, &lds, &turn);
@@ -377,7 +377,8 @@ __global__ __launch_bounds__(kColumnTile / 8) void echo_block_norm_cols_k(const 
   next.load_any(a, rows.lo, run);
   float4 next_st = a.stats[rows.lo];
   RawParam r[3];
-  load_any_params(a, rows.lo / a.p.rows_per_gate, run, r);
+  load_any_params(a, rows.gate, run, r);
+  int64_t gate_row = rows.gate, gate_left = a.p.rows_per_gate;  // of whole gates
   float pre[8], post[8], gate[8], acc[kSums][8];
   factor_of(e, a.p.w_pre != nullptr, a.p.offset, r[0], run.lo, pre);
   factor_of(e, a.p.w_post != nullptr, a.p.offset, r[1], run.lo, post);
@@ -401,10 +402,6 @@ __global__ __launch_bounds__(kColumnTile / 8) void echo_block_norm_cols_k(const 
       store_from<X>(a.dx, row * a.lddx, run, w);
     }
     if (a.y == nullptr) continue;
-    if (sp.chunks == 0 && a.p.gate != nullptr && row % a.p.rows_per_gate == 0 && row != rows.lo) {
-      load_any(e, a.p.gate, row / a.p.rows_per_gate * a.p.ldg, run, &r[2]);
-      factor_of(e, true, 0.0f, r[2], run.lo, gate);
-    }
     float y[8];
     widen<Y>(raw.y, y);
     clear_below(run.lo, y);
@@ -416,11 +413,17 @@ __global__ __launch_bounds__(kColumnTile / 8) void echo_block_norm_cols_k(const 
       w[i] = st.z * __builtin_fmaf(dn, post[i], -(y[i] * st.w));
     }
     if (a.dy != nullptr) store_from<Y>(a.dy, row * a.lddy, run, w);
-    if (sp.chunks == 0 && a.dgate != nullptr && (row + 1) % a.p.rows_per_gate == 0) {
+    if (sp.chunks == 0 && --gate_left == 0) {
       // the last row of a gate that is this workgroup's alone
-      store_from(e, a.dgate, row / a.p.rows_per_gate * a.lddg, run, acc[kSumGate]);
+      if (a.dgate != nullptr) store_from(e, a.dgate, gate_row * a.lddg, run, acc[kSumGate]);
 #pragma unroll
       for (int i = 0; i < 8; ++i) acc[kSumGate][i] = 0.0f;
+      ++gate_row;
+      gate_left = a.p.rows_per_gate;
+      if (a.p.gate != nullptr && row + 1 < rows.hi) {
+        load_any(e, a.p.gate, gate_row * a.p.ldg, run, &r[2]);
+        factor_of(e, true, 0.0f, r[2], run.lo, gate);
+      }
     }
   }
   if (a.dw_pre != nullptr) store_from<kElemF32>(part_at(a, blockIdx.x, kSumPre), 0, run, acc[kSumPre]);

@@ -263,6 +263,12 @@ __device__ __forceinline__ void load_weight(const BlockParams& p, const void* w,
   for (int i = 0; i < 8; ++i) v[i] = v[i] + p.offset;
 }
 
+// The row of the gate for a row of the stream; both fit 32 bits, whose division is a quarter
+// of that in 64.
+__device__ __forceinline__ int64_t gate_of(const BlockParams& p, int64_t row) {
+  return static_cast<uint32_t>(row) / static_cast<uint32_t>(p.rows_per_gate);
+}
+
 // 1 / sqrt(mean of the squares + eps), by the reciprocal root's instruction (1 ulp; what is
 // under the root is at least 2^-126): the exact division and root are 60 instructions, as
 // many as a row's 8 columns take.
