@@ -50,16 +50,20 @@ __device__ __forceinline__ void places(const uint32_t (&key)[ROUNDS], int digit_
 #pragma unroll
   for (int r = 0; r < ROUNDS; ++r) {
     const uint32_t d = (key[r] >> digit_shift) & (kDigits - 1);
-    uint64_t same = ~uint64_t{0};  // the lanes with this digit
+    // the lanes with another digit, in two halves
+    uint32_t low = 0, high = 0;
 #pragma unroll
     for (int b = 0; b < kDigitBits; ++b) {
-      const uint64_t set = __ballot((d >> b) & 1);
-      same &= (d >> b) & 1 ? set : ~set;
+      const uint32_t bit = static_cast<uint32_t>(__builtin_amdgcn_sbfe(static_cast<int>(d), b, 1));  // 0 or all ones
+      const uint64_t set = __ballot(bit != 0);
+      low |= static_cast<uint32_t>(set) ^ bit;
+      high |= static_cast<uint32_t>(set >> 32) ^ bit;
     }
-    const int before = __popcll(same & ((uint64_t{1} << lane) - 1));
+    const uint64_t same = ~(static_cast<uint64_t>(high) << 32 | low);
+    const uint32_t before = __builtin_amdgcn_mbcnt_hi(~high, __builtin_amdgcn_mbcnt_lo(~low, 0));
     uint32_t old = 0;
     if (before == 0) old = atomicAdd(&lds->count[wave][d], static_cast<uint32_t>(__popcll(same)));
-    place[r] = __shfl(old, __ffsll(static_cast<unsigned long long>(same)) - 1) + static_cast<uint32_t>(before);
+    place[r] = __shfl(old, __ffsll(static_cast<unsigned long long>(same)) - 1) + before;
   }
   __syncthreads();
   // exclusive prefix sums of the counts, digit by digit and within a digit by wavefront:
@@ -400,6 +404,9 @@ __global__ __launch_bounds__(kSumThreads) void echo_embed_sum_k(const EmbedBwdAr
   const Run run = columns_of(lane, shift, C);
   const int64_t block = static_cast<int64_t>(blockIdx.x) * subs * length;  // the workgroup's first token
   const int64_t lo = block + static_cast<int64_t>(sub) * length, hi = lo + length < T ? lo + length : T;
+  // the tokens around the workgroup's
+  const int64_t end = block + static_cast<int64_t>(subs) * length;
+  const uint32_t before = block > 0 ? keys[block - 1] : ~0u, behind = end < T ? keys[end] : ~0u;
   if (lo < T) {
     float acc[8];
     uint32_t cur = keys[lo];
@@ -443,8 +450,6 @@ __global__ __launch_bounds__(kSumThreads) void echo_embed_sum_k(const EmbedBwdAr
   __syncthreads();
   const int64_t col = static_cast<int64_t>(blockIdx.y) * width + threadIdx.x;
   if (static_cast<int>(threadIdx.x) >= width || col >= C) return;
-  const int64_t end = block + static_cast<int64_t>(subs) * length;
-  const uint32_t before = block > 0 ? keys[block - 1] : ~0u, behind = end < T ? keys[end] : ~0u;
   const auto put = [&](uint32_t key, float sum, bool at_end) {
     if (key == none) return;  // tokens without a row
     if (key == before) {
@@ -584,6 +589,8 @@ hipError_t launch_embed_bwd(const EmbedBwdArgs& given, Elem dout, Elem table, hi
       hipLaunchKernelGGL((echo_embed_sort_k<E(), 1>), dim3(1 + clear), dim3(kSortThreads), 0, s, a, digits, keys[0], order[0]);
     else if (T <= 4 * kSortThreads)
       hipLaunchKernelGGL((echo_embed_sort_k<E(), 4>), dim3(1 + clear), dim3(kSortThreads), 0, s, a, digits, keys[0], order[0]);
+    else if (T <= 8 * kSortThreads)
+      hipLaunchKernelGGL((echo_embed_sort_k<E(), 8>), dim3(1 + clear), dim3(kSortThreads), 0, s, a, digits, keys[0], order[0]);
     else if (T <= kSmall)
       hipLaunchKernelGGL((echo_embed_sort_k<E(), kSmallRounds>), dim3(1 + (clear < 255 ? clear : 255)), dim3(kSortThreads), 0, s, a, digits, keys[0],
                          order[0]);
