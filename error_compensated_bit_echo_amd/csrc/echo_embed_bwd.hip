@@ -144,10 +144,11 @@ __device__ __forceinline__ void clear_tables(const Args* a, int part, int parts,
 }
 
 // Clears the rows that no token has, workgroup `id` of `of`: it takes every `of`-th block of
-// rows, 2^shift threads to a row (64 at most: a row to 1024 threads costs a look at its mark
-// for every store, 323 us in place of 285 in the case below), and marks those of its rows that
-// a token has in LDS, kMarked rows at a time.  Rows that the sums will write are not written
-// twice: at 16384 tokens, 65536 rows of 4096 fp32, a tenth of them.
+// rows, 2^shift threads (64 at most) to a row, and marks those of its rows that a token has in
+// LDS, kMarked rows at a time.  A wavefront writes rows behind one another, up to 32 KB of them
+// (1 GiB filled so: 6.4 TB/s, with 16 KB 6.0, 4 KB 5.3; the workgroup's wavefronts all on one
+// row: 5.4).  Rows that the sums will write are not written twice: at 16384 tokens, 65536 rows
+// of 4096 fp32, a tenth of them.
 constexpr int kMarked = 32 * kSortThreads;
 
 template <int E, bool STREAM, typename Args>
@@ -156,8 +157,12 @@ __device__ __forceinline__ void clear_untouched_as(const Args* a, uint32_t id, u
   const int64_t C = a->C;
   const uint32_t V = static_cast<uint32_t>(a->V), rows = static_cast<uint32_t>(a->P) * V;
   const int shift = embed_shift(C);
-  const int bits = 10 - shift;  // 2^bits rows to a block
   static_assert(kSortThreads == 1 << 10, "rows of a block");
+  int deep = 0;  // 2^deep rows behind one another
+  while (deep < 5 && (C * static_cast<int64_t>(sizeof(typename ElemOf<E>::T)) << (deep + 1)) <= 32768 &&
+         (rows >> (11 - shift + deep)) >= of)
+    ++deep;
+  const int bits = 10 - shift + deep;  // 2^bits rows to a block
   const uint32_t blocks = ((rows - 1) >> bits) + 1, window = kMarked >> bits;
   for (uint64_t j0 = 0; id + j0 * of < blocks; j0 += window) {
     marks[threadIdx.x] = 0;
@@ -174,13 +179,15 @@ __device__ __forceinline__ void clear_untouched_as(const Args* a, uint32_t id, u
     for (uint32_t j = 0; j < window; ++j) {
       const uint64_t block = id + (j0 + j) * of;
       if (block >= blocks) break;
-      const uint32_t in = threadIdx.x >> shift, row = (static_cast<uint32_t>(block) << bits) + in, m = (j << bits) + in;
-      if (row >= rows || (marks[m >> 5] >> (m & 31) & 1)) continue;
-      const uint32_t r = row / V;
-      void* table = a->dtable[r];
-      const int64_t v = (row - r * V) * a->ldt;
-      for (int64_t at = (threadIdx.x & ((1 << shift) - 1)) * kZ; at < C; at += int64_t{kZ} << shift)
-        clear_run<E, STREAM>(table, v + at, C - at);
+      for (uint32_t in = threadIdx.x >> shift << deep, end = in + (1u << deep); in < end; ++in) {
+        const uint32_t row = (static_cast<uint32_t>(block) << bits) + in, m = (j << bits) + in;
+        if (row >= rows || (marks[m >> 5] >> (m & 31) & 1)) continue;
+        const uint32_t r = row / V;
+        void* table = a->dtable[r];
+        const int64_t v = (row - r * V) * a->ldt;
+        for (int64_t at = (threadIdx.x & ((1 << shift) - 1)) * kZ; at < C; at += int64_t{kZ} << shift)
+          clear_run<E, STREAM>(table, v + at, C - at);
+      }
     }
     __syncthreads();
   }
