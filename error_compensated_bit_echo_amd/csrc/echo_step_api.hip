@@ -132,27 +132,28 @@ echo_status check_tensors(const void* const* src, void* const* dst, const int64_
 // One stretch of memory of a clipping call.
 struct Stretch {
   uintptr_t lo, hi;
-  int64_t tensor;
   bool written;
 };
 
-// Whether every written tensor lies apart from all others, its own input aside where that
+// Whether what is written (results, the norm, the workspace) lies apart from all else, a
+// result's own input aside where that
 // is the very same memory.  In order of their starts, a stretch meets an earlier one iff
 // it starts before the furthest end so far: of the written ones, and of any if it is written.
 echo_status tensors_apart(const void* const* src, void* const* dst, const int64_t* n, const int32_t* dtypes,
-                          int64_t count, const float* norm) {
-  Stretch* all = new (std::nothrow) Stretch[static_cast<size_t>(2 * count + 1)];
+                          int64_t count, const float* norm, const void* workspace) {
+  Stretch* all = new (std::nothrow) Stretch[static_cast<size_t>(2 * count + 2)];
   if (all == nullptr) return ECHO_ERR_WORKSPACE;
   int64_t m = 0;
   for (int64_t i = 0; i < count; ++i) {
     if (n[i] == 0) continue;
     const uintptr_t s = reinterpret_cast<uintptr_t>(src[i]), d = dst != nullptr ? reinterpret_cast<uintptr_t>(dst[i]) : 0;
     const uintptr_t bytes = static_cast<uintptr_t>(n[i] * bytes_of(dtypes[i]));
-    if (dst != nullptr) all[m++] = Stretch{d, d + bytes, i, true};
-    if (dst == nullptr || s != d) all[m++] = Stretch{s, s + bytes, i, false};
+    if (dst != nullptr) all[m++] = Stretch{d, d + bytes, true};
+    if (dst == nullptr || s != d) all[m++] = Stretch{s, s + bytes, false};
   }
-  const uintptr_t at = reinterpret_cast<uintptr_t>(norm);
-  all[m++] = Stretch{at, at + sizeof(float), -1, true};
+  const uintptr_t at = reinterpret_cast<uintptr_t>(norm), w = reinterpret_cast<uintptr_t>(workspace);
+  all[m++] = Stretch{at, at + sizeof(float), true};
+  if (count > 0) all[m++] = Stretch{w, w + echo_clip_workspace(count), true};
   std::sort(all, all + m, [](const Stretch& a, const Stretch& b) { return a.lo < b.lo; });
   uintptr_t end = 0, written_end = 0;
   bool ok = true;
@@ -353,7 +354,7 @@ echo_status echo_grad_norm(const void* const* grads, const int64_t* numel, const
   if (e != ECHO_OK) return e;
   if (norm == nullptr || !aligned(norm, 4)) return ECHO_ERR_ARG;
   if ((e = check_clip_workspace(n_tensors, workspace, workspace_bytes)) != ECHO_OK) return e;
-  if ((e = tensors_apart(grads, nullptr, numel, dtypes, n_tensors, norm)) != ECHO_OK) return e;
+  if ((e = tensors_apart(grads, nullptr, numel, dtypes, n_tensors, norm, workspace)) != ECHO_OK) return e;
   const hipStream_t s = static_cast<hipStream_t>(stream);
   double* part = static_cast<double*>(workspace);
   int64_t n_part;
@@ -370,7 +371,7 @@ echo_status echo_clip_grads(const void* const* grads, void* const* out, const in
   if (!(max_norm >= 0.0) || !is_finite(max_norm)) return ECHO_ERR_ARG;  // also refuses NaN
   if (norm == nullptr || !aligned(norm, 4)) return ECHO_ERR_ARG;
   if ((e = check_clip_workspace(n_tensors, workspace, workspace_bytes)) != ECHO_OK) return e;
-  if ((e = tensors_apart(grads, out, numel, dtypes, n_tensors, norm)) != ECHO_OK) return e;
+  if ((e = tensors_apart(grads, out, numel, dtypes, n_tensors, norm, workspace)) != ECHO_OK) return e;
   const hipStream_t s = static_cast<hipStream_t>(stream);
   double* part = static_cast<double*>(workspace);
   int64_t n_part;

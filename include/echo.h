@@ -460,8 +460,8 @@ typedef struct {
 /* Source: none on the pages (the norms and the residual add around the blocks
  * that «Почему обычное 4-битное суммирование портит модель» reduces).
  * out and a as echo_block says, in one pass.  y and out: both or neither; a NULL:
- * not wanted (w_pre is NULL then).  Sums and products are fp32 operations (a
- * row's mean square has to be below 2^128); out and a are rounded once each, and
+ * not wanted (w_pre is NULL then).  Sums and products are fp32 operations (the
+ * squares of a row have to add up to less than 2^128); out and a are rounded once each, and
  * a starts from out as it is stored, so that the norm of the stored stream gives
  * the same.  A NaN makes its row of out (where y has a post-norm) and of a NaN;
  * an infinity gives NaN in its own place and 0 in the others.
@@ -504,8 +504,8 @@ size_t echo_clip_workspace(int64_t n_tensors);
  * *norm (device, fp32) = sqrt of the sum of squares of all elements of n_tensors
  * contiguous tensors (numel and dtypes: host arrays; fp32, bfloat16 and fp16 in
  * any mix, any alignment of the element type, lengths of 0 allowed).  Squares and
- * sums are held in 64 bits, in an order that the lengths fix.  norm lies in none
- * of the tensors; tensors may overlap each other.
+ * sums are held in 64 bits, in an order that the lengths fix.  norm and workspace
+ * lie in none of the tensors; tensors may overlap each other.
  * n_tensors: at most 2^24; numel: 2^40; below 2^31 chunks of 32 KiB in all.
  * workspace: 8-byte aligned.  A launch for every 280 tensors, and one more.
  * Errors: ECHO_ERR_ARG, ECHO_ERR_SHAPE, ECHO_ERR_DTYPE, ECHO_ERR_WORKSPACE (also

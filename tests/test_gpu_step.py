@@ -480,6 +480,34 @@ def test_embed_backward_of_a_large_vocabulary(E):
     assert torch.equal(out, d[tokens])
 
 
+def test_more_threads_than_a_launch_numbers(E):
+    """Launches number their threads along an axis in 32 bits: 2^26 rows of 64 threads, 2^24 of 256."""
+    import torch
+    R, C = (1 << 26) + 5, 8
+    x = torch.randn(R, C, generator=gen(6), device="cuda").bfloat16()
+    w = torch.rand(C, generator=gen(7), device="cuda")
+    a, dx, dw = torch.zeros_like(x), torch.zeros_like(x), torch.empty_like(w)
+    E.echo_block_norm(x, a=a, w_pre=w)
+    E.echo_block_norm_backward(x, da=x, dx=dx, w_pre=w, dw_pre=dw)
+    some = torch.randint(0, R, (2000,), generator=gen(8), device="cuda")
+    some[:4] = torch.tensor([0, R - 1, R - 5, R - 6], device="cuda")
+    assert_close(a[some], *norm_ref(np64(x[some]), np64(w), 0.0, 1e-6), torch.bfloat16)
+    ref = block_norm_backward_ref(np64(x[some]), None, None, np64(x[some]), None, None, np64(w), False, 1.0, 0.0, 1e-6)
+    assert_close(dx[some], *ref["dx"], torch.bfloat16)
+    del a, dx
+    # sums of 2^26 terms, of about 0.5 each, in 4096 workgroups of 16384 rows: 16384 additions in a row and 70 more
+    total = sum((t.double() ** 2 / (t.double() ** 2).mean(1, keepdim=True).add(1e-6).sqrt()).sum(0) for t in x.split(1 << 22))
+    assert (np.abs(np64(dw) - total.cpu().numpy()) <= (16384 + 100) * U * total.abs().cpu().numpy()).all()
+    del x
+    T, C = (1 << 24) + 3, 2048
+    table = torch.randn(100, C, generator=gen(9), device="cuda").bfloat16()
+    tokens = torch.randint(0, 100, (T,), generator=gen(10), device="cuda")
+    out = torch.zeros(T, C, dtype=torch.bfloat16, device="cuda")
+    E.echo_embed([table], tokens, [out])
+    for lo in range(0, T, 1 << 20):
+        assert torch.equal(out[lo:lo + (1 << 20)], table[tokens[lo:lo + (1 << 20)]])
+
+
 # ---- streams, graphs ---------------------------------------------------------------------------
 
 

@@ -130,7 +130,7 @@ BAD_TENSORS = [
     (B.ECHO_ERR_ARG, dict(spec=((None, 1, F32),))), (B.ECHO_ERR_ARG, dict(spec=((X + 2, 1, F32),))),
     (B.ECHO_ERR_ARG, dict(spec=((X + 1, 1, BF16),))), (B.ECHO_ERR_ARG, dict(norm=None)), (B.ECHO_ERR_ARG, dict(norm=NORM + 2)),
     (B.ECHO_ERR_ARG, dict(norm=X + 396)), (B.ECHO_ERR_WORKSPACE, dict(ws=None)), (B.ECHO_ERR_WORKSPACE, dict(ws_bytes=100)),
-    (B.ECHO_ERR_ARG, dict(ws=WS + 4)),
+    (B.ECHO_ERR_ARG, dict(ws=WS + 4)), (B.ECHO_ERR_ARG, dict(ws=X + 8)), (B.ECHO_ERR_ARG, dict(ws=NORM - 64)),
 ]
 
 
