@@ -82,7 +82,7 @@ __device__ __forceinline__ void factor_of(int e, bool given, float offset, const
   clear_below(lo, w);
 }
 
-template <int X, int Y, int A>
+template <int X, int Y, int A, bool STREAM>
 __global__ __launch_bounds__(kMaxThreads) void echo_block_norm_bwd_k(const BlockNormBwdArgs a, const BlockSplit sp) {
   __shared__ Slots<3> lds;
   extern __shared__ float4 factors[];
@@ -155,7 +155,7 @@ __global__ __launch_bounds__(kMaxThreads) void echo_block_norm_bwd_k(const Block
     if (a.dx != nullptr) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) s[i] = a.p.alpha * t[i];
-      store_from<X>(a.dx, row * a.lddx, run, s);
+      store_from<X, STREAM>(a.dx, row * a.lddx, run, s);
     }
     if (a.y == nullptr) continue;
     float gate[8];
@@ -183,7 +183,7 @@ __global__ __launch_bounds__(kMaxThreads) void echo_block_norm_bwd_k(const Block
         t[i] = gate[i] * t[i];
       }
     }
-    if (a.dy != nullptr) store_from<Y>(a.dy, row * a.lddy, run, t);
+    if (a.dy != nullptr) store_from<Y, STREAM>(a.dy, row * a.lddy, run, t);
     if (sp.chunks == 0 && --gate_left == 0) {
       // the last row of a gate that is this workgroup's alone
       if (a.dgate != nullptr) store_from(e, a.dgate, gate_row * a.lddg, run, acc[kSumGate]);
@@ -367,7 +367,7 @@ __global__ __launch_bounds__(kMaxThreads) void echo_block_norm_stats_long_k(cons
 
 // The gradients of kColumnTile columns of a workgroup's rows, whose statistics are known: no
 // sums over a row are left, so rows pass without a barrier.
-template <int X, int Y, int A>
+template <int X, int Y, int A, bool STREAM>
 __global__ __launch_bounds__(kColumnTile / 8) void echo_block_norm_cols_k(const BlockNormBwdArgs a, const BlockSplit sp) {
   const int64_t C = a.p.C;
   const Run run = any_run_of(blockIdx.y, C);
@@ -399,7 +399,7 @@ __global__ __launch_bounds__(kColumnTile / 8) void echo_block_norm_cols_k(const 
     if (a.dx != nullptr) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) w[i] = a.p.alpha * t[i];
-      store_from<X>(a.dx, row * a.lddx, run, w);
+      store_from<X, STREAM>(a.dx, row * a.lddx, run, w);
     }
     if (a.y == nullptr) continue;
     float y[8];
@@ -412,7 +412,7 @@ __global__ __launch_bounds__(kColumnTile / 8) void echo_block_norm_cols_k(const 
       acc[kSumPost][i] = __builtin_fmaf(dn, yh, acc[kSumPost][i]);
       w[i] = st.z * __builtin_fmaf(dn, post[i], -(y[i] * st.w));
     }
-    if (a.dy != nullptr) store_from<Y>(a.dy, row * a.lddy, run, w);
+    if (a.dy != nullptr) store_from<Y, STREAM>(a.dy, row * a.lddy, run, w);
     if (sp.chunks == 0 && --gate_left == 0) {
       // the last row of a gate that is this workgroup's alone
       if (a.dgate != nullptr) store_from(e, a.dgate, gate_row * a.lddg, run, acc[kSumGate]);
@@ -479,11 +479,16 @@ hipError_t launch_block_norm_bwd(const BlockNormBwdArgs& a, Elem x, Elem y, Elem
   const unsigned groups = static_cast<unsigned>(sp.groups);
   // without rows only the sums are written: zeros
   const hipError_t e = a.p.R == 0 ? hipSuccess : with_types(x, y, out_a, [&](auto X, auto Y, auto A) -> hipError_t {
+    constexpr bool kAny = X() != kElemF32 || Y() != kElemF32;  // 16-bit results
+    const int64_t bytes = 3 * elem_size(X()) + elem_size(A()) + (a.y != nullptr ? 2 * elem_size(Y()) : 0);
+    const bool stream = kAny && block_streams(a.p.R, a.p.C, bytes);
     if (block_fits(a.p.C)) {
       const int threads = row_threads(a.p.C, 1);
-      hipLaunchKernelGGL((echo_block_norm_bwd_k<X(), Y(), A()>), dim3(groups), dim3(threads), threads * 6 * sizeof(float4), s,
-                         a, sp);
-      return hipGetLastError();
+      const auto launch = [&](auto kernel) {
+        hipLaunchKernelGGL(kernel, dim3(groups), dim3(threads), threads * 6 * sizeof(float4), s, a, sp);
+        return hipGetLastError();
+      };
+      return stream ? launch(echo_block_norm_bwd_k<X(), Y(), A(), kAny>) : launch(echo_block_norm_bwd_k<X(), Y(), A(), false>);
     }
     if (a.p.C > 8 * kMaxThreads && a.p.C <= 16 * kMaxThreads) {
       const int threads = row_threads(a.p.C, 2);
@@ -502,8 +507,11 @@ hipError_t launch_block_norm_bwd(const BlockNormBwdArgs& a, Elem x, Elem y, Elem
       if (r != hipSuccess) return r;
     }
     const unsigned tiles = static_cast<unsigned>((a.p.C + kColumnTile - 1) / kColumnTile);
-    hipLaunchKernelGGL((echo_block_norm_cols_k<X(), Y(), A()>), dim3(groups, tiles), dim3(kColumnTile / 8), 0, s, a, sp);
-    return hipGetLastError();
+    const auto launch = [&](auto kernel) {
+      hipLaunchKernelGGL(kernel, dim3(groups, tiles), dim3(kColumnTile / 8), 0, s, a, sp);
+      return hipGetLastError();
+    };
+    return stream ? launch(echo_block_norm_cols_k<X(), Y(), A(), kAny>) : launch(echo_block_norm_cols_k<X(), Y(), A(), false>);
   });
   if (e != hipSuccess) return e;
   const int64_t gates = a.dgate != nullptr && (sp.chunks != 0 || a.p.R == 0) ? a.p.n_gates : 0;

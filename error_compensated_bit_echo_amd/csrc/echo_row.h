@@ -67,6 +67,27 @@ __device__ __forceinline__ void block_sums(float (&v)[N], Slots<M>* lds, int* tu
   }
 }
 
+// The sum over the workgroup and a thread's RUNS runs, in the order in which a workgroup of
+// RUNS times as many threads with a run each adds them up: a row's sum does not depend on
+// which of the two works on it.  More than one wavefront, 16 of runs at most.
+template <int RUNS>
+__device__ __forceinline__ float block_sum_of_runs(float (&v)[RUNS], Slots<1>* lds, int* turn) {
+  const int waves = static_cast<int>(blockDim.x) >> 6, slot = *turn;
+  *turn ^= 1;
+  const int wave = static_cast<int>(threadIdx.x) >> 6, lane = static_cast<int>(threadIdx.x) & 63;
+#pragma unroll
+  for (int k = 0; k < RUNS; ++k) {
+    v[k] = wave_sum(v[k]);
+    if (lane == 63) lds->v[slot][0][k * waves + wave] = v[k];
+  }
+  __syncthreads();
+  float w = (lane & 15) < RUNS * waves ? lds->v[slot][0][lane & 15] : 0.0f;
+  w = w + dpp<0xB1>(w);
+  w = w + dpp<0x4E>(w);
+  w = w + dpp<0x141>(w);
+  return w + dpp<0x140>(w);
+}
+
 // A run of up to 8 columns: n of them lie in the row.
 template <int E>
 __device__ __forceinline__ void load_run(const void* base, int64_t at, int n, float v[8]) {
@@ -233,11 +254,24 @@ __device__ __forceinline__ void clear_below(int lo, float v[8]) {
   }
 }
 
-template <int E>
+// STREAM: 16-bit elements go past the caches (fp32 ones do not: a run of them is two stores,
+// which only a cache makes one line of).
+template <int E, bool STREAM = false>
 __device__ __forceinline__ void store_from(void* base, int64_t row, Run run, const float v[8]) {
-  typename ElemOf<E>::T* p = static_cast<typename ElemOf<E>::T*>(base) + row;
+  typedef typename ElemOf<E>::T T;
+  T* p = static_cast<T*>(base) + row;
   if (run.lo == 0) {
-    store8<E>(p, run.at, v);
+    if constexpr (STREAM && E != kElemF32) {
+      typedef uint32_t u4 __attribute__((ext_vector_type(4), aligned(2)));
+      Raw<E> x;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x.v[i] = narrow<E>(v[i]);
+      u4 w;
+      __builtin_memcpy(&w, &x.v, 16);
+      __builtin_nontemporal_store(w, reinterpret_cast<u4*>(p + run.at));
+    } else {
+      store8<E>(p, run.at, v);
+    }
   } else {
 #pragma unroll
     for (int i = 0; i < 8; ++i)

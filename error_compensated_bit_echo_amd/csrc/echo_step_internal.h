@@ -12,6 +12,8 @@ namespace echo {
 
 constexpr int64_t kStepMaxCols = int64_t{1} << 22;  // columns of a norm's or an embedding's row
 
+constexpr int64_t elem_size(int elem) { return elem == kElemF32 ? 4 : 2; }
+
 // The parameters of a block's norms and gate, as both directions read them.
 struct BlockParams {
   const void* gate;    // nullptr: 1
@@ -23,6 +25,11 @@ struct BlockParams {
   int32_t elem;  // Elem of gate, w_post and w_pre
   int32_t post;  // y is normalised
 };
+
+// Whether a call moves more than the last-level cache holds (256 MB): its 16-bit results then go
+// past the caches, where they would only replace inputs that later rows, or the next call, read.
+// Smaller results stay for the kernel that reads them next.
+inline bool block_streams(int64_t R, int64_t C, int64_t bytes) { return R * C >= (int64_t{256} << 20) / bytes; }
 
 struct BlockNormArgs {
   BlockParams p;

@@ -459,12 +459,13 @@ typedef struct {
 
 /* Source: none on the pages (the norms and the residual add around the blocks
  * that «Почему обычное 4-битное суммирование портит модель» reduces).
- * out and a as echo_block says, in one pass.  y and out: both or neither; a NULL:
- * not wanted (w_pre is NULL then).  Sums and products are fp32 operations (the
- * squares of a row have to add up to less than 2^128); out and a are rounded once each, and
- * a starts from out as it is stored, so that the norm of the stored stream gives
- * the same.  A NaN makes its row of out (where y has a post-norm) and of a NaN;
- * an infinity gives NaN in its own place and 0 in the others.
+ * out and a as echo_block says, in one pass; a row's depend on that row alone.
+ * y and out: both or neither; a NULL: not wanted (w_pre is NULL then).  Sums and
+ * products are fp32 operations (the squares of a row have to add up to less than
+ * 2^128); out and a are rounded once each, and a starts from out as it is stored,
+ * so that the norm of the stored stream gives the same.  A NaN makes its row of
+ * out (where y has a post-norm) and of a NaN; an infinity gives NaN in its own
+ * place and 0 in the others.
  * ld*: elements between rows, any alignment of the element type.  out may be x
  * itself (same pointer and pitch); outputs overlap nothing else.  One launch.
  * Errors: ECHO_ERR_ARG (null or misaligned pointer, parameters without y, an

@@ -158,6 +158,33 @@ def test_block_norm_parts_wanted(E):
         assert torch.equal(got, t), name
 
 
+@pytest.mark.parametrize("T,C,types", [(8200, 4100, ("bf16",) * 3), (5000, 7001, ("f32", "f16", "f16")), (4100, 9001, ("bf16",) * 3)])
+def test_block_norm_of_more_than_the_cache_holds(E, T, C, types):
+    """Calls that move more than 256 MB, whose 16-bit results go past the caches, give row by row
+    what small calls give; their column sums are the small calls' added up."""
+    import torch
+    c = BlockCase(T, C, types, "f32", pad=3)
+    out, a = c.forward(E)
+    got = c.gradients(E)
+    sums = {n: torch.zeros(1, C, dtype=torch.float64, device="cuda") for n in ("dgate", "dw_post", "dw_pre")}
+    for lo in range(0, T, 1000):
+        r = slice(lo, lo + 1000)
+        o, b = torch.empty_like(c.x[r]), torch.empty_like(a.t[r])
+        E.echo_block_norm(c.x[r], o, b, **dict(c.params, y=c.y[r]))
+        assert torch.equal(o, out.t[r]) and torch.equal(b, a.t[r])
+        dx, dy = torch.empty_like(o), torch.empty_like(c.y[r])
+        part = {n: torch.empty_like(got[n]) for n in sums}
+        E.echo_block_norm_backward(c.x[r], dout=c.dout[r], da=c.da[r], dx=dx, dy=dy, **part, **dict(c.params, y=c.y[r]))
+        assert torch.equal(dx, got["dx"].t[r]) and torch.equal(dy, got["dy"].t[r])
+        for n, p in part.items():
+            sums[n] += p.double()
+    for n, want in sums.items():
+        # both add T terms of random signs in fp32: a root of T of terms of at most 2 or so, and T roundings of them
+        off = T * U * T ** 0.5 * 2
+        assert float((got[n].double() - want).abs().max()) <= off, n
+    assert out.check() and a.check() and got["dx"].check() and got["dy"].check()
+
+
 def test_block_norm_in_place(E):
     import torch
     for C in (500, 20000):
