@@ -8,6 +8,13 @@
 // workgroup takes consecutive rows and sums its columns in registers; the workgroups' sums
 // go to the workspace and are added in order by a second kernel, so the result does not
 // depend on timing.
+//
+// As many workgroups as the CUs hold, each with its next row's inputs in flight while it works
+// on one; the parameters' factors wait in LDS, which leaves the registers (127 of 128) to the
+// sums and the inputs. 16384 x 8192 bfloat16 takes 297 us (5.4 TB/s of what it has to move), the
+// kernel 286 and the join 6; the vector units issue in 56 % of its cycles, so that every
+// instruction a row counts: with the exact root and division it took 345, with a 64-bit
+// division a row 309. 2048 x 4096 fp32: 57 us, 10 of them the column sums' way through memory.
 #include <type_traits>
 
 #include "echo_row.h"
@@ -206,6 +213,10 @@ __global__ __launch_bounds__(kMaxThreads) void echo_block_norm_bwd_k(const Block
 }
 
 // ---- rows that do not fit: statistics, then a pass by columns -------------------------------
+//
+// 8192 x 12288 bfloat16: 447 us, of which the statistics 214 (3.8 TB/s, a workgroup to a CU)
+// and the columns 223 (5.4 TB/s). One pass with two runs to a thread needs more registers than
+// there are: 920 us, spilled; three passes over each row from the caches took 860.
 
 // rs(out), its square times mean(u out), rs(y), its square times mean(v y)
 __device__ __forceinline__ float4 stats_of(const BlockNormBwdArgs& a, const float m[3]) {
