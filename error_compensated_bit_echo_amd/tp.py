@@ -366,6 +366,8 @@ def _fns():
                                           for i, t in ((1, y), (2, gate), (3, w_post), (4, w_pre)))
             if da is None:  # the next block's input was not used
                 dw_pre = None if dw_pre is None else dw_pre.zero_()
+                if not any(ctx.needs_input_grad[:4]):
+                    return None, None, None, None, dw_pre, None, None
             B.echo_block_norm_backward(out, dout=dout, da=da, dx=dx, y=y, dy=dy, gate=gate, dgate=dgate, w_post=w_post,
                                        dw_post=dw_post, w_pre=None if da is None else w_pre,
                                        dw_pre=None if da is None else dw_pre, **ctx.options)

@@ -91,6 +91,17 @@ def test_only_wanted_gradients_are_given(cuda, tp):
     assert_close(w_post.grad, *ref["dw_post"], y.dtype)
 
 
+def test_a_weight_whose_output_is_not_used(cuda, tp):
+    """The weight before the next block alone wants a gradient, and that block's input is dropped."""
+    import torch
+    leaves, dout, _ = block(torch.float32, 1)
+    for t in leaves[:4]:
+        t.requires_grad_(False)
+    out, _ = tp.block_norm(*leaves, post_norm=True)
+    (out * dout).sum().backward()
+    assert leaves[4].grad.shape == (H,) and not leaves[4].grad.any()
+
+
 def test_block_norm_gradient_against_differences(cuda, tp):
     """Along a direction, with a step of 2^-6: see the operator's own test for what a quotient may be off."""
     import torch
