@@ -421,7 +421,8 @@ __global__ __launch_bounds__(kColumnTile / 8) void echo_block_norm_cols_k(const 
       const float yh = y[i] * st.z, dn = gate[i] * t[i];
       acc[kSumGate][i] = __builtin_fmaf(t[i], yh * post[i], acc[kSumGate][i]);
       acc[kSumPost][i] = __builtin_fmaf(dn, yh, acc[kSumPost][i]);
-      w[i] = st.z * __builtin_fmaf(dn, post[i], -(y[i] * st.w));
+      // an infinite y times the 0 that stands for no post-norm would be no number
+      w[i] = a.p.post ? st.z * __builtin_fmaf(dn, post[i], -(y[i] * st.w)) : dn;
     }
     if (a.dy != nullptr) store_from<Y, STREAM>(a.dy, row * a.lddy, run, w);
     if (sp.chunks == 0 && --gate_left == 0) {

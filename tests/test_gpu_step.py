@@ -245,6 +245,19 @@ def test_block_norm_special_values(E, C):
         assert out[4].isnan().sum() == 1 and a[4].isnan().all()
 
 
+@pytest.mark.parametrize("C", [5, 300, 9000, 20000])
+def test_block_norm_gradient_beside_an_infinite_output(E, C):
+    """Without a post-norm y's gradient does not depend on y."""
+    import torch
+    for types in (("f32",) * 3, ("bf16",) * 3):
+        c = BlockCase(3, C, types, post=False, w_pre=False)
+        c.y[1, C // 2], c.y[2, 0] = float("inf"), float("-inf")
+        dy = torch.empty_like(c.y)
+        E.echo_block_norm_backward(c.x, dout=c.dout, dy=dy, **c.params)
+        want = np64(c.dout) * np64(c.gate)
+        assert_close(dy, want, np.abs(want) * U, c.Y, "dy")  # one product in fp32
+
+
 def test_block_norm_gradient_against_differences(E):
     """d loss along a direction, in fp32 with steps of 2^-7: the difference quotient is off by the
     third derivative (h^2 / 6, below 1e-4 of these sums) and by the forward pass's roundings / h."""
