@@ -1,15 +1,16 @@
 // The norm of many tensors together, and the tensors scaled by min(1, max_norm / (norm +
 // 1e-6)).  Two launches for up to 176 tensors (280 in place): the first adds squares, a
 // partial sum per workgroup; in the second every workgroup adds the partial sums, in the same
-// order, and scales its chunks.  Tensors come in the launch's arguments, so nothing is kept
-// between calls and a captured call needs no table in device memory.
+// order (one workgroup beforehand, where several launches left some), and scales its chunks.
+// Tensors come in the launch's arguments, so nothing is kept between calls and a captured call
+// needs no table in device memory.
 //
 // Squares are formed and added in 64 bits, so that neither a gradient of 1e30 nor one of
 // 1e-30 is lost; the memory hides it.
 //
 // Bound by the memory: 64 tensors of 16 Mi fp32 take 2.36 ms, the squares 0.69 (6.2 TB/s) and
 // the scaling 1.64 (5.2 TB/s); 24 tensors of 4096 take 9 to 11 us, 3.4 and 4.3 of them the
-// kernels; 331 mixed ones of 26 M elements 49 us in four launches.
+// kernels; 331 mixed ones of 26 M elements 47 us in five launches.
 #include "echo_row.h"
 
 namespace echo {
@@ -157,10 +158,14 @@ __global__ __launch_bounds__(kThreads) void echo_clip_sum_k(const ClipInPlace gi
   if (threadIdx.x == 0) part[blockIdx.x] = s;
 }
 
-__device__ __forceinline__ double norm_of(const double* part, int64_t n_part, double* lds) {
+__device__ __forceinline__ double sum_of(const double* part, int64_t n_part, double* lds) {
   double s = 0.0;
   for (int64_t i = threadIdx.x; i < n_part; i += kThreads) s = s + part[i];
-  return sqrt(block_sum64(s, lds));
+  return block_sum64(s, lds);
+}
+
+__device__ __forceinline__ double norm_of(const double* part, int64_t n_part, double* lds) {
+  return sqrt(sum_of(part, n_part, lds));
 }
 
 // STREAM: past the caches, so that what the first launch read and the cache still holds is not
@@ -234,6 +239,13 @@ __global__ __launch_bounds__(kThreads) void echo_clip_norm_k(const double* part,
   if (threadIdx.x == 0) *norm = static_cast<float>(total);
 }
 
+// One partial sum in place of all, the same that norm_of adds up.
+__global__ __launch_bounds__(kThreads) void echo_clip_join_k(double* part, int64_t n_part) {
+  __shared__ double lds[4];
+  const double total = sum_of(part, n_part, lds);
+  if (threadIdx.x == 0) part[0] = total;
+}
+
 template <typename Args>
 hipError_t launch_scale(const Args& a, const double* part, int64_t n_part, double max_norm, float* norm, bool stream, hipStream_t s) {
   const dim3 grid(clip_grid(a.first[a.tensors]));
@@ -259,6 +271,11 @@ hipError_t launch_clip_scale(const ClipInPlace& a, const double* part, int64_t n
 hipError_t launch_clip_scale(const ClipApart& a, const double* part, int64_t n_part, double max_norm, float* norm,
                              bool stream, hipStream_t s) {
   return launch_scale(a, part, n_part, max_norm, norm, stream, s);
+}
+
+hipError_t launch_clip_join(double* part, int64_t n_part, hipStream_t s) {
+  hipLaunchKernelGGL(echo_clip_join_k, dim3(1), dim3(kThreads), 0, s, part, n_part);
+  return hipGetLastError();
 }
 
 hipError_t launch_clip_norm(const double* part, int64_t n_part, float* norm, hipStream_t s) {

@@ -377,6 +377,10 @@ echo_status echo_clip_grads(const void* const* grads, void* const* out, const in
   int64_t n_part;
   if ((e = launch_sums(grads, numel, dtypes, n_tensors, part, &n_part, s)) != ECHO_OK) return e;
   if (n_part == 0) return status_of(echo::launch_clip_norm(part, 0, norm, s));
+  if (n_part > echo::kClipGroups) {
+    if ((e = status_of(echo::launch_clip_join(part, n_part, s))) != ECHO_OK) return e;
+    n_part = 1;
+  }
   bool in_place = true;
   for (int64_t i = 0; i < n_tensors && in_place; ++i) in_place = numel[i] == 0 || grads[i] == out[i];
   return in_place ? launch_scales<echo::ClipInPlace>(grads, out, numel, dtypes, n_tensors, part, n_part, max_norm, norm, s)

@@ -148,6 +148,10 @@ hipError_t launch_clip_scale(const ClipInPlace& a, const double* part, int64_t n
 hipError_t launch_clip_scale(const ClipApart& a, const double* part, int64_t n_part, double max_norm, float* norm,
                              bool stream, hipStream_t s);
 hipError_t launch_clip_norm(const double* part, int64_t n_part, float* norm, hipStream_t s);
+// part[0] = the sum of all: more partial sums than one launch leaves cost a launch of their own
+// less than every workgroup of every launch adding them up (331 tensors, 46.8 us and 47.6; 1200 of
+// 256 KB, 200 and 249; 6000, 1039 and 2484)
+hipError_t launch_clip_join(double* part, int64_t n_part, hipStream_t s);
 
 struct EmbedArgs {
   const void* table[kMaxRanks];

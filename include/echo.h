@@ -521,8 +521,8 @@ echo_status echo_grad_norm(const void* const* grads, const int64_t* numel, const
  * = 0 (and NaN where the element is infinite), a NaN makes every element NaN.
  * out_i may be g_i itself (it is not touched then where f is 1) and overlaps no
  * other tensor.  max_norm: finite, at least 0.  A launch for every 280 tensors,
- * and one for every 176 (280 where all are scaled in place).  Limits, workspace
- * and errors as above. */
+ * one for every 176 (280 where all are scaled in place), and one between them for
+ * many tensors.  Limits, workspace and errors as above. */
 echo_status echo_clip_grads(const void* const* grads, void* const* out, const int64_t* numel, const int32_t* dtypes,
                             int64_t n_tensors, double max_norm, float* norm, void* workspace, size_t workspace_bytes,
                             echo_stream_t stream);

@@ -42,7 +42,7 @@ struct Seen {
 };
 std::vector<Seen> g_summed, g_scaled;
 std::vector<const double*> g_parts;
-int64_t g_n_part = -1;
+int64_t g_n_part = -1, g_joined = 0;
 int g_norms = 0;
 
 template <typename Args>
@@ -89,6 +89,11 @@ hipError_t launch_clip_scale(const ClipInPlace& a, const double*, int64_t n, dou
 }
 hipError_t launch_clip_scale(const ClipApart& a, const double*, int64_t n, double, float* norm, bool, hipStream_t) {
   return scaled(a, n, norm);
+}
+hipError_t launch_clip_join(double* part, int64_t n, hipStream_t) {
+  CHECK(!g_parts.empty() && part == g_parts[0]);
+  g_joined = n;
+  return launched();
 }
 hipError_t launch_clip_norm(const double*, int64_t n, float*, hipStream_t) {
   g_n_part = n;
@@ -189,6 +194,7 @@ void check_block() {
 void check_clip() {
   std::mt19937 g(3);
   const auto pick = [&](int64_t lo, int64_t hi) { return std::uniform_int_distribution<int64_t>(lo, hi)(g); };
+  int joins = 0;
   for (int n : {0, 1, 5, 175, 176, 177, 279, 280, 281, 353, 1000}) {
     std::vector<const void*> src;
     std::vector<void*> dst;
@@ -215,9 +221,13 @@ void check_clip() {
     for (int in_place = 0; in_place < 2; ++in_place) {
       g_summed.clear(), g_scaled.clear(), g_parts.clear();
       g_norms = g_launches = 0;
+      g_joined = 0;
       CHECK(echo_clip_grads(src.data(), in_place ? const_cast<void* const*>(src.data()) : dst.data(), numel.data(), types.data(),
                             n, 1.0, static_cast<float*>(fake(900 * G)), fake(901 * G), bytes, nullptr) == ECHO_OK);
-      CHECK(g_norms == 1 && g_summed.size() == static_cast<size_t>(whole) && g_n_part == static_cast<int64_t>(g_parts.size()));
+      CHECK(g_norms == 1 && g_summed.size() == static_cast<size_t>(whole));
+      const int64_t parts = static_cast<int64_t>(g_parts.size());  // more than one launch leaves are joined first
+      CHECK(g_joined == (parts > echo::kClipGroups ? parts : 0) && g_n_part == (g_joined != 0 ? 1 : parts));
+      joins += g_joined != 0;
       CHECK(g_scaled.size() == g_summed.size());
       size_t k = 0;
       for (int i = 0; i < n; ++i) {
@@ -247,6 +257,7 @@ void check_clip() {
       g_fail_at = -1;
     }
   }
+  CHECK(joins > 0);
 }
 
 // Overlaps of clipping calls against a byte-by-byte count.

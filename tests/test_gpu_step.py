@@ -343,6 +343,14 @@ def test_clip_many_tensors_of_mixed_types_at_any_element(E):
             assert torch.equal(b[at[t]:], rest[t])
 
 
+def test_clip_more_sums_than_a_launch_leaves(E):
+    import torch
+    g = gen(7)
+    grads = [torch.randn(1 << 16, generator=g, device="cuda") for _ in range(301)]
+    check_clip(E, grads, 3.0)
+    check_clip(E, grads, 5.0, in_place=True)
+
+
 def test_clip_is_the_same_every_time_and_in_place(E):
     import torch
     g = gen(4)
@@ -568,6 +576,39 @@ def test_calls_on_another_stream(E):
         E.echo_block_norm_backward(c.x, dout=c.dout, da=c.da, dx=dx.zero_(), dw_pre=dw.zero_(), **c.params)
     torch.cuda.current_stream().wait_stream(s)
     assert torch.equal(dx, want["dx"].t) and torch.equal(dw, want["dw_pre"])
+
+
+def test_calls_on_two_streams_at_once(E):
+    """Each with its own workspace: what they give alone."""
+    import torch
+    T, V, C = 20000, 700, 512
+    g = gen(13)
+    tokens = [torch.randint(0, V, (T,), generator=g, device="cuda") for _ in range(2)]
+    d = [torch.randn(T, C, generator=g, device="cuda") for _ in range(2)]
+    x = torch.randn(T, C, generator=g, device="cuda")
+    w = torch.rand(C, generator=g, device="cuda")
+    u8 = lambda n: torch.empty(n, dtype=torch.uint8, device="cuda")
+    sizes = E.echo_block_norm_workspace(T, C), E.echo_embed_workspace(T, C), E.echo_clip_workspace(2)
+
+    def buffers():
+        return dict(dx=torch.empty(T, C, device="cuda"), dw=torch.empty(C, device="cuda"), dt=torch.empty(V, C, device="cuda"),
+                    norm=torch.empty(1, device="cuda"), ws=[u8(n) for n in sizes])
+
+    def run(i, b, stream):
+        E.echo_block_norm_backward(x, da=d[i], dx=b["dx"], w_pre=w, dw_pre=b["dw"], workspace=b["ws"][0], stream=stream)
+        E.echo_embed_backward(b["dx"], tokens[i], [b["dt"]], workspace=b["ws"][1], stream=stream)
+        E.echo_clip_grads([b["dt"], b["dw"]], 0.5, b["norm"], workspace=b["ws"][2], stream=stream)
+
+    want, got, streams = [buffers() for _ in range(2)], [buffers() for _ in range(2)], [torch.cuda.Stream() for _ in range(2)]
+    for i in range(2):
+        run(i, want[i], torch.cuda.current_stream())
+    torch.cuda.synchronize()
+    for _ in range(3):
+        for i in range(2):
+            run(i, got[i], streams[i])
+    torch.cuda.synchronize()
+    for a, b in zip(got, want):
+        assert all(torch.equal(a[k], b[k]) for k in ("dx", "dw", "dt", "norm"))
 
 
 @pytest.mark.parametrize("T", [200, 20000])
