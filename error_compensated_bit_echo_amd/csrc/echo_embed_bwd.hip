@@ -13,8 +13,8 @@
 // its end into the workspace; a last launch adds those up along the chunks.  So a token
 // that comes up ten thousand times costs as much as ten thousand different ones.
 //
-// Bound by the memory: 16384 tokens, 4 tables of 16384 x 4096 fp32, take 289 us, 4.6 TB/s: the
-// zeros 189 (5.2 TB/s, the sort of 31 us behind them), the sums 83, the join 7. 16384 tokens of
+// Bound by the memory: 16384 tokens, 4 tables of 16384 x 4096 fp32, take 245 us, 5.5 TB/s: the
+// zeros 165 (the sort of 31 us behind them), the sums 77, the join 7. 16384 tokens of
 // a table of 1000 x 512 take 48 us, where the sort shows.
 #include "echo_row.h"
 
@@ -29,7 +29,7 @@ constexpr int kSmallRounds = 16;
 constexpr int64_t kSmall = kSortThreads * kSmallRounds;  // tokens that one workgroup sorts: 128 KB of LDS
 constexpr int kTileRounds = 4;
 constexpr int kThreads = 256;  // of the join
-constexpr unsigned kClearGroups = 512;  // of kSortThreads: two to a CU
+constexpr unsigned kClearGroups = 256;  // of kSortThreads: one to a CU
 
 struct SortLds {
   uint32_t count[kWaves][kDigits];
@@ -104,8 +104,9 @@ template <int E>
 constexpr int kZeros = 16 / sizeof(typename ElemOf<E>::T);
 
 // STREAM: past the caches, which the sums' reads and writes would otherwise have to empty of
-// zeros first (4 tables of 16384 x 4096 fp32: 285 us, 299 without); tables that the last-level
-// cache holds stay there (50000 x 1024 fp32: 42 us, 52 past it).
+// zeros first (4 tables of 16384 x 4096 fp32, 16384 tokens: 252 us, 294 without; 8192 x 4096, whose
+// gradients do not fit: 112 and 131); tables that the last-level cache holds, beside gradients that
+// it holds, stay there (50000 x 1024 fp32, 4096 tokens: 46 us, 52 past it).
 template <int E, bool STREAM>
 __device__ __forceinline__ void clear_run(void* table, int64_t at, int64_t left) {
   typedef typename ElemOf<E>::T T;
@@ -119,12 +120,50 @@ __device__ __forceinline__ void clear_run(void* table, int64_t at, int64_t left)
   }
 }
 
-// Part `part` of `parts` of clearing the tables, by workgroup `id` of `of`.  Tables whose
-// rows follow each other without a gap are one row each.
+// A table whose rows follow each other without a gap is cleared page by page of 4 KB: workgroup b
+// takes every 8th only, those at addresses of one remainder of 32 KB, its wavefronts one after the
+// other.  The workgroups of an XCD, which are every 8th too, then write one remainder, and 255
+// of 16 wavefronts reach 6.5 TB/s of nothing but zeros, where stretches of 32 KB to a wavefront
+// reach 6.1 and pages as they come 5.4.  Rows that the sums will write are written here too: with
+// the tenth of them left out that 16384 tokens of 65536 rows take, the pattern breaks (4 tables of
+// 16384 x 4096 fp32: 271 us in all, 252 with them).
+constexpr int64_t kPage = 4096;
+
+// Pages lo .. hi - 1 of the ranks' tables, `per` to a table of `bytes`, by the workgroups from
+// `first` on, 8 at least.
+template <bool STREAM, typename Args>
+__device__ __forceinline__ void clear_pages_as(const Args* a, int64_t bytes, int64_t per, int64_t lo, int64_t hi, uint32_t first) {
+  typedef uint32_t u4 __attribute__((ext_vector_type(4), aligned(2)));
+  const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+  const uint32_t kind = blockIdx.x & 7, least = first + ((kind - first) & 7);
+  const uint32_t groups = (gridDim.x - least + 7) >> 3, slot = (blockIdx.x - least) >> 3;
+  for (int64_t r = lo / per; r < a->P && r * per < hi; ++r) {
+    char* table = static_cast<char*>(a->dtable[r]);
+    const int64_t from = lo - r * per, to = hi - r * per, end = to < per ? to : per;
+    int64_t page = from > 0 ? from : 0;
+    page += (kind - static_cast<uint32_t>(reinterpret_cast<uintptr_t>(table) >> 12) - static_cast<uint32_t>(page)) & 7;
+    for (page += int64_t{slot * kWaves + wave} * 8; page < end; page += int64_t{groups} * kWaves * 8) {
+      const int64_t at = page * kPage + lane * 16;
+      char* p = table + at;
+      if ((page + 1) * kPage <= bytes) {
+#pragma unroll
+        for (int i = 0; i < kPage / 1024; ++i) {
+          u4* q = reinterpret_cast<u4*>(p + i * 1024);
+          if constexpr (STREAM) __builtin_nontemporal_store(u4{0, 0, 0, 0}, q);
+          else *q = u4{0, 0, 0, 0};
+        }
+      } else {
+        for (int i = 0; i < kPage; i += 1024)
+          for (int b = 0; b < 16 && at + i + b < bytes; b += 2) *reinterpret_cast<uint16_t*>(p + i + b) = 0;
+      }
+    }
+  }
+}
+
+// Part `part` of `parts` of clearing tables with gaps between their rows, by workgroup `id` of `of`.
 template <int E, bool STREAM, typename Args>
-__device__ __forceinline__ void clear_tables_as(const Args* a, int part, int parts, uint32_t id, uint32_t of) {
-  const bool whole = a->ldt == a->C || a->V == 1;
-  const int64_t C = whole ? a->V * a->C : a->C, V = whole ? 1 : a->V;
+__device__ __forceinline__ void clear_rows_as(const Args* a, int part, int parts, uint32_t id, uint32_t of) {
+  const int64_t C = a->C, V = a->V;
   constexpr int kZ = kZeros<E>;
   int shift = 0;  // 2^shift threads to a row
   while ((1 << shift) < kSortThreads && (int64_t{kZ} << shift) < C) ++shift;
@@ -139,71 +178,24 @@ __device__ __forceinline__ void clear_tables_as(const Args* a, int part, int par
   }
 }
 
-// The two are apart as a whole: the compiler would make one of two stores that differ in
-// their cache policy alone.
+// Part `part` of `parts` of clearing the tables, by the launch's workgroups from `first` on.  The two
+// policies are apart as a whole: the compiler would make one of two stores that differ in it alone.
 template <int E, typename Args>
-__device__ __forceinline__ void clear_tables(const Args* a, int part, int parts, uint32_t id, uint32_t of) {
-  if (a->stream) clear_tables_as<E, true>(a, part, parts, id, of);
-  else clear_tables_as<E, false>(a, part, parts, id, of);
-}
-
-// Clears the rows that no token has, workgroup `id` of `of`: it takes every `of`-th block of
-// rows, 2^shift threads (64 at most) to a row, and marks those of its rows that a token has in
-// LDS, kMarked rows at a time.  A wavefront writes rows behind one another, up to 32 KB of them
-// (1 GiB filled so: 6.4 TB/s, with 16 KB 6.0, 4 KB 5.3; the workgroup's wavefronts all on one
-// row: 5.4).  Rows that the sums will write are not written twice: at 16384 tokens, 65536 rows
-// of 4096 fp32, a tenth of them.
-constexpr int kMarked = 32 * kSortThreads;
-
-template <int E, bool STREAM, typename Args>
-__device__ __forceinline__ void clear_untouched_as(const Args* a, uint32_t id, uint32_t of, uint32_t* marks) {
-  constexpr int kZ = kZeros<E>;
-  const int64_t C = a->C;
-  const uint32_t V = static_cast<uint32_t>(a->V), rows = static_cast<uint32_t>(a->P) * V;
-  const int shift = embed_shift(C);
-  static_assert(kSortThreads == 1 << 10, "rows of a block");
-  int deep = 0;  // 2^deep rows behind one another
-  while (deep < 5 && (C * static_cast<int64_t>(sizeof(typename ElemOf<E>::T)) << (deep + 1)) <= 32768 &&
-         (rows >> (11 - shift + deep)) >= of)
-    ++deep;
-  const int bits = 10 - shift + deep;  // 2^bits rows to a block
-  const uint32_t blocks = ((rows - 1) >> bits) + 1, window = kMarked >> bits;
-  for (uint64_t j0 = 0; id + j0 * of < blocks; j0 += window) {
-    marks[threadIdx.x] = 0;
-    __syncthreads();
-    for (int64_t t = threadIdx.x; t < a->T; t += kSortThreads) {
-      const uint32_t k = key_of(a, t), block = k >> bits;
-      if (k >= rows || block % of != id) continue;
-      const uint64_t j = block / of;
-      if (j < j0 || j >= j0 + window) continue;
-      const uint32_t m = static_cast<uint32_t>((j - j0) << bits) + (k & ((1u << bits) - 1));
-      atomicOr(&marks[m >> 5], 1u << (m & 31));
-    }
-    __syncthreads();
-    for (uint32_t j = 0; j < window; ++j) {
-      const uint64_t block = id + (j0 + j) * of;
-      if (block >= blocks) break;
-      for (uint32_t in = threadIdx.x >> shift << deep, end = in + (1u << deep); in < end; ++in) {
-        const uint32_t row = (static_cast<uint32_t>(block) << bits) + in, m = (j << bits) + in;
-        if (row >= rows || (marks[m >> 5] >> (m & 31) & 1)) continue;
-        const uint32_t r = row / V;
-        void* table = a->dtable[r];
-        const int64_t v = (row - r * V) * a->ldt;
-        for (int64_t at = (threadIdx.x & ((1 << shift) - 1)) * kZ; at < C; at += int64_t{kZ} << shift)
-          clear_run<E, STREAM>(table, v + at, C - at);
-      }
-    }
-    __syncthreads();
+__device__ __forceinline__ void clear_tables(const Args* a, int part, int parts, uint32_t first) {
+  const uint32_t id = blockIdx.x - first, of = gridDim.x - first;
+  if ((a->ldt == a->C || a->V == 1) && of >= 8) {
+    const int64_t bytes = a->V * a->C * static_cast<int64_t>(sizeof(typename ElemOf<E>::T));
+    const int64_t per = (bytes + kPage - 1) / kPage, pages = per * a->P, lo = pages * part / parts, hi = pages * (part + 1) / parts;
+    if (a->stream) clear_pages_as<true>(a, bytes, per, lo, hi, first);
+    else clear_pages_as<false>(a, bytes, per, lo, hi, first);
+  } else if (a->stream) {
+    clear_rows_as<E, true>(a, part, parts, id, of);
+  } else {
+    clear_rows_as<E, false>(a, part, parts, id, of);
   }
 }
 
-template <int E, typename Args>
-__device__ __forceinline__ void clear_untouched(const Args* a, uint32_t id, uint32_t of, uint32_t* marks) {
-  if (a->stream) clear_untouched_as<E, true>(a, id, of, marks);
-  else clear_untouched_as<E, false>(a, id, of, marks);
-}
-
-// Workgroup 0 sorts up to 1024 * ROUNDS tokens; the others clear the rows without one.
+// Workgroup 0 sorts up to 1024 * ROUNDS tokens; the others clear the tables.
 template <int E, int ROUNDS>
 __global__ __launch_bounds__(kSortThreads) void echo_embed_sort_k(const EmbedBwdArgs given, int digits, uint32_t* keys,
                                                                   uint32_t* order) {
@@ -212,7 +204,7 @@ __global__ __launch_bounds__(kSortThreads) void echo_embed_sort_k(const EmbedBwd
   __shared__ uint16_t so[kSortThreads * ROUNDS];
   const auto* a = kernel_args<EmbedBwdArgs>();
   if (blockIdx.x != 0) {
-    clear_untouched<E>(a, blockIdx.x - 1, gridDim.x - 1, sk);
+    clear_tables<E>(a, 0, 1, 1);
     return;
   }
   const int T = static_cast<int>(a->T);
@@ -251,7 +243,7 @@ __global__ __launch_bounds__(kSortThreads) void echo_embed_sort_k(const EmbedBwd
 
 template <int E>
 __global__ __launch_bounds__(kSortThreads) void echo_embed_clear_k(const EmbedBwdArgs given) {
-  clear_tables<E>(kernel_args<EmbedBwdArgs>(), 0, 1, blockIdx.x, gridDim.x);
+  clear_tables<E>(kernel_args<EmbedBwdArgs>(), 0, 1, 0);
 }
 
 // ---- more than kSmall tokens -------------------------------------------------------------
@@ -286,7 +278,7 @@ __global__ __launch_bounds__(kSortThreads) void echo_embed_count_k(const EmbedBw
   __shared__ uint32_t n[kDigits];
   const auto* a = kernel_args<EmbedBwdArgs>();
   if (blockIdx.x >= sh.work) {
-    clear_tables<E>(a, sh.part, sh.parts, blockIdx.x - sh.work, gridDim.x - sh.work);
+    clear_tables<E>(a, sh.part, sh.parts, sh.work);
     return;
   }
   if (threadIdx.x < kDigits) n[threadIdx.x] = 0;
@@ -306,7 +298,7 @@ __global__ __launch_bounds__(kSortThreads) void echo_embed_scan_k(const EmbedBwd
                                                                   int64_t n) {
   __shared__ uint32_t total[kWaves];
   if (blockIdx.x >= sh.work) {
-    clear_tables<E>(kernel_args<EmbedBwdArgs>(), sh.part, sh.parts, blockIdx.x - sh.work, gridDim.x - sh.work);
+    clear_tables<E>(kernel_args<EmbedBwdArgs>(), sh.part, sh.parts, sh.work);
     return;
   }
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -348,7 +340,7 @@ __global__ __launch_bounds__(kSortThreads) void echo_embed_place_k(const EmbedBw
   __shared__ uint32_t start[kDigits];  // the digit's first place in the tile
   const auto* a = kernel_args<EmbedBwdArgs>();
   if (blockIdx.x >= sh.work) {
-    clear_tables<E>(a, sh.part, sh.parts, blockIdx.x - sh.work, gridDim.x - sh.work);
+    clear_tables<E>(a, sh.part, sh.parts, sh.work);
     return;
   }
   uint32_t key[kTileRounds], at[kTileRounds], place[kTileRounds];
@@ -581,7 +573,7 @@ hipError_t launch_sort(const EmbedBwdArgs& a, int digits, uint32_t* const keys[2
 
 hipError_t launch_embed_bwd(const EmbedBwdArgs& given, Elem dout, Elem table, hipStream_t s) {
   EmbedBwdArgs a = given;
-  a.stream = a.P * a.V * a.C * (table == kElemF32 ? 4 : 2) >= int64_t{256} << 20;
+  a.stream = a.P * a.V * a.C * elem_size(table) >= int64_t{256} << 20 || a.T * a.C * elem_size(dout) >= int64_t{256} << 20;
   const int64_t T = a.T;
   const EmbedLayout w = embed_layout(T, a.C);
   char* base = static_cast<char*>(a.workspace);
@@ -603,7 +595,7 @@ hipError_t launch_embed_bwd(const EmbedBwdArgs& given, Elem dout, Elem table, hi
     else if (T <= 8 * kSortThreads)
       hipLaunchKernelGGL((echo_embed_sort_k<E(), 8>), dim3(1 + clear), dim3(kSortThreads), 0, s, a, digits, keys[0], order[0]);
     else if (T <= kSmall)
-      hipLaunchKernelGGL((echo_embed_sort_k<E(), kSmallRounds>), dim3(1 + (clear < 255 ? clear : 255)), dim3(kSortThreads), 0, s, a, digits, keys[0],
+      hipLaunchKernelGGL((echo_embed_sort_k<E(), kSmallRounds>), dim3(1 + clear), dim3(kSortThreads), 0, s, a, digits, keys[0],
                          order[0]);
     else
       e = launch_sort<E()>(a, digits, keys, order, reinterpret_cast<uint32_t*>(base + w.counts), &in, s);

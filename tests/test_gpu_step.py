@@ -491,6 +491,15 @@ def test_embed_backward_every_size(E, T, C):
     check_embed_backward(E, 3, 50, T, C, "f32", "bf16", scale=0.3, first=11, wide=False)
 
 
+@pytest.mark.parametrize("T", [3, 5000, 20000])
+@pytest.mark.parametrize("V,C", [(1000, 77), (257, 1024), (70001, 5), (1, 300001), (2100, 2048)])
+def test_embed_backward_clears_what_no_token_has(E, V, C, T):
+    """Tables without gaps, their ends inside a page and at any element; and with gaps."""
+    for at in (0, 1):
+        check_embed_backward(E, 3, V, min(T, 40000000 // C), C, "bf16", "bf16", at=at)
+    check_embed_backward(E, 2, V, min(T, 40000000 // C), C, "f32", "f32", at=3, pad=0 if C > 2000 else 9)
+
+
 @pytest.mark.parametrize("T", [1023, 1024, 1025, 16383, 16384, 16385, 20480, 20481, 70000])
 @pytest.mark.parametrize("n", [200, 255, 256, 65535, 65536, 70001])
 def test_embed_backward_sorts_any_number_of_tokens(E, T, n):
