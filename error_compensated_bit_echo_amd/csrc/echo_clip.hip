@@ -8,8 +8,8 @@
 // Squares are formed and added in 64 bits, so that neither a gradient of 1e30 nor one of
 // 1e-30 is lost; the memory hides it.
 //
-// Bound by the memory: 64 tensors of 16 Mi fp32 take 2.36 ms, the squares 0.69 (6.2 TB/s) and
-// the scaling 1.64 (5.2 TB/s); 24 tensors of 4096 take 9 to 11 us, 3.4 and 4.3 of them the
+// Bound by the memory: 64 tensors of 16 Mi fp32 take 2.22 ms, the squares 0.69 (6.2 TB/s) and
+// the scaling 1.52 (5.6 TB/s); 24 tensors of 4096 take 9 to 11 us, 3.4 and 4.3 of them the
 // kernels; 331 mixed ones of 26 M elements 47 us in five launches.
 #include "echo_row.h"
 
@@ -34,6 +34,13 @@ __device__ __forceinline__ double block_sum64(double v, double* lds) {
   __syncthreads();
   return (lds[0] + lds[1]) + (lds[2] + lds[3]);
 }
+
+// Chunks of 8 next to each other, where a tensor has them whole, share their 256 KB page by page: a
+// chunk is 8 pages of 4 KB, 32 KB apart.  The 8 lie with workgroups of the 8 XCDs, each of which so
+// keeps to one remainder of 32 KB in a large tensor (a copy of 1 GiB in chunks: 5.99 TB/s, with
+// chunks of 32 KB in a row 5.37).
+constexpr int kPage = kThreads * 16, kSpan = 8;
+static_assert(kPage * kSpan == kClipChunk, "a page to a round of the threads");
 
 // A launch's chunks: where each lies.  Every lane keeps a few of the tensors' first chunks, so
 // that finding a chunk's tensor is a count of those not behind it, with no chain of loads.
@@ -63,14 +70,18 @@ struct Chunk {
   int64_t at;      // its first byte in the tensor
   int tensor, elem;
   int bytes;       // of it
+  int step;        // bytes from a thread's unit to its next
 };
 
 template <typename Args, typename A>
 __device__ __forceinline__ Chunk chunk_of(const A* a, const Tensors<Args>& ts, uint32_t c) {
   const int t = ts.tensor_of(c);
-  const uint32_t tail = a->tail[t], first = a->first[t];
-  return Chunk{static_cast<int64_t>(c - first) * kClipChunk, t, static_cast<int>(tail >> 14),
-               c + 1 == a->first[t + 1] ? static_cast<int>(((tail & 0x3FFF) + 1) * 2) : static_cast<int>(kClipChunk)};
+  const uint32_t tail = a->tail[t], first = a->first[t], end = a->first[t + 1], in = c - first;
+  const int elem = static_cast<int>(tail >> 14), last = static_cast<int>(((tail & 0x3FFF) + 1) * 2);
+  if ((in | (kSpan - 1)) < end - first - (last < kClipChunk ? 1 : 0))
+    return Chunk{static_cast<int64_t>(in / kSpan) * (kSpan * kClipChunk) + in % kSpan * kPage, t, elem, static_cast<int>(kClipChunk),
+                 kSpan * kPage};
+  return Chunk{static_cast<int64_t>(in) * kClipChunk, t, elem, c + 1 == end ? last : static_cast<int>(kClipChunk), kPage};
 }
 
 // 16 bytes of a chunk.  One that would reach past the tensor's end starts 16 bytes before it
@@ -87,7 +98,7 @@ struct Spot {
 
 __device__ __forceinline__ Spot spot_of(const Chunk& c, int k) {
   const int at = (k * kThreads + static_cast<int>(threadIdx.x)) * 16, last = c.bytes - 16;
-  return at <= last ? Spot{c.at + at, 0} : Spot{c.at + last, at - last < 16 ? at - last : 16};
+  return at <= last ? Spot{c.at + k * c.step + static_cast<int>(threadIdx.x) * 16, 0} : Spot{c.at + last, at - last < 16 ? at - last : 16};
 }
 
 template <int N>

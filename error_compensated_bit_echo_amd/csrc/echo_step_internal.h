@@ -117,7 +117,9 @@ hipError_t launch_block_norm_bwd(const BlockNormBwdArgs& a, Elem x, Elem y, Elem
 // bits of its last chunk's length and its type; where the result goes elsewhere, a second
 // pointer.  4 KB of arguments hold 176 tensors, or 280 where there is one pointer each.
 constexpr int64_t kClipChunk = 32768;
-constexpr int kClipGroups = 2048;  // workgroups, and partial sums, of a launch at most
+// workgroups, and partial sums, of a launch at most: four to a CU (64 tensors of 16 Mi fp32 2215 us,
+// with 2048 2277, with 256 2300; 331 mixed ones 46.2, 48.5 and 50.6)
+constexpr int kClipGroups = 1024;
 template <int N, bool APART>
 struct ClipArgs {
   static constexpr int kTensors = N;
@@ -149,8 +151,8 @@ hipError_t launch_clip_scale(const ClipApart& a, const double* part, int64_t n_p
                              bool stream, hipStream_t s);
 hipError_t launch_clip_norm(const double* part, int64_t n_part, float* norm, hipStream_t s);
 // part[0] = the sum of all: more partial sums than one launch leaves cost a launch of their own
-// less than every workgroup of every launch adding them up (331 tensors, 46.8 us and 47.6; 1200 of
-// 256 KB, 200 and 249; 6000, 1039 and 2484)
+// less than every workgroup of every launch adding them up (with 2048 a launch: 331 tensors, 46.8 us
+// and 47.6; 1200 of 256 KB, 200 and 249; 6000, 1039 and 2484)
 hipError_t launch_clip_join(double* part, int64_t n_part, hipStream_t s);
 
 struct EmbedArgs {
