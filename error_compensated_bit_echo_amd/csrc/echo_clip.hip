@@ -9,7 +9,7 @@
 // 1e-30 is lost; the memory hides it.
 //
 // Bound by the memory: 64 tensors of 16 Mi fp32 take 2.22 ms, the squares 0.69 (6.2 TB/s) and
-// the scaling 1.52 (5.6 TB/s); 24 tensors of 4096 take 9 to 11 us, 3.4 and 4.3 of them the
+// the scaling 1.54 (5.6 TB/s); 24 tensors of 4096 take 9 to 11 us, 3.4 and 4.3 of them the
 // kernels; 331 mixed ones of 26 M elements 47 us in five launches.
 #include "echo_row.h"
 
