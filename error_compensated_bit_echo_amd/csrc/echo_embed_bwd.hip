@@ -13,7 +13,7 @@
 // its end into the workspace; a last launch adds those up along the chunks.  So a token
 // that comes up ten thousand times costs as much as ten thousand different ones.
 //
-// Bound by the memory: 16384 tokens, 4 tables of 16384 x 4096 fp32, take 245 to 261 us, 5.5 to 5.1 TB/s:
+// Bound by the memory: 16384 tokens, 4 tables of 16384 x 4096 fp32, take 238 to 259 us, 5.6 to 5.2 TB/s:
 // the zeros 164 (the sort of 31 us behind them), the sums 70 to 83, the join 7. 16384 tokens of
 // a table of 1000 x 512 take 48 us, where the sort shows.
 #include "echo_row.h"
@@ -364,10 +364,10 @@ __global__ __launch_bounds__(kSortThreads) void echo_embed_place_k(const EmbedBw
 
 // ---- sums over runs ----------------------------------------------------------------------
 
-// The columns that thread `lane` of 2^shift has in tile blockIdx.y; all 8 below `lo` where it
+// The columns that thread `lane` of 2^shift has in the tile; all 8 below `lo` where it
 // has none.
-__device__ __forceinline__ Run columns_of(uint32_t lane, int shift, int64_t C) {
-  const uint32_t at = ((blockIdx.y << shift) + lane) * 8;
+__device__ __forceinline__ Run columns_of(uint32_t tile, uint32_t lane, int shift, int64_t C) {
+  const uint32_t at = ((tile << shift) + lane) * 8;
   if (static_cast<int64_t>(at) + 8 <= C) return Run{at, 0};
   return Run{static_cast<uint32_t>(C) - 8, static_cast<int64_t>(at) < C ? static_cast<int>(at + 8 - static_cast<uint32_t>(C)) : 8};
 }
@@ -389,7 +389,9 @@ constexpr int kSumThreads = 512;
 // leaves the sums of its first and last run in LDS; a thread a column then adds those along
 // the chunks.  part: two rows of C to a workgroup, for the run that crosses its start and for
 // the one that crosses its end only.  WAVE: a chunk to a wavefront (shift 6), whose tokens
-// come through scalar loads.
+// come through scalar loads.  Workgroups next to each other take the tiles of the same tokens' rows,
+// so that an XCD stays with a tile (4 tables of 16384 x 4096 fp32, 16384 tokens: 238 us in all, with
+// the tokens first 244).
 template <int O, int E, bool WAVE>
 __global__ __launch_bounds__(kSumThreads) void echo_embed_sum_k(const EmbedBwdArgs given, int shift, int length,
                                                                 const uint32_t* __restrict__ keys,
@@ -404,8 +406,8 @@ __global__ __launch_bounds__(kSumThreads) void echo_embed_sum_k(const EmbedBwdAr
   uint32_t sub = threadIdx.x >> shift;
   if constexpr (WAVE) sub = __builtin_amdgcn_readfirstlane(sub);
   const uint32_t lane = threadIdx.x & ((1u << shift) - 1);
-  const Run run = columns_of(lane, shift, C);
-  const int64_t block = static_cast<int64_t>(blockIdx.x) * subs * length;  // the workgroup's first token
+  const Run run = columns_of(blockIdx.x, lane, shift, C);
+  const int64_t block = static_cast<int64_t>(blockIdx.y) * subs * length;  // the workgroup's first token
   const int64_t lo = block + static_cast<int64_t>(sub) * length, hi = lo + length < T ? lo + length : T;
   // the tokens around the workgroup's
   const int64_t end = block + static_cast<int64_t>(subs) * length;
@@ -451,14 +453,14 @@ __global__ __launch_bounds__(kSumThreads) void echo_embed_sum_k(const EmbedBwdAr
     if (lane == 0) last[sub] = cur;
   }
   __syncthreads();
-  const int64_t col = static_cast<int64_t>(blockIdx.y) * width + threadIdx.x;
+  const int64_t col = static_cast<int64_t>(blockIdx.x) * width + threadIdx.x;
   if (static_cast<int>(threadIdx.x) >= width || col >= C) return;
   const auto put = [&](uint32_t key, float sum, bool at_end) {
     if (key == none) return;  // tokens without a row
     if (key == before) {
-      part[2 * blockIdx.x * C + col] = sum;
+      part[2 * blockIdx.y * C + col] = sum;
     } else if (at_end && key == behind) {
-      part[(2 * blockIdx.x + 1) * C + col] = sum;
+      part[(2 * blockIdx.y + 1) * C + col] = sum;
     } else {
       const uint32_t V = static_cast<uint32_t>(a->V), r = key / V, v = key - r * V;
       store1<E>(a->dtable[r], v * a->ldt + col, sum * a->scale);
@@ -492,7 +494,7 @@ __global__ __launch_bounds__(kThreads) void echo_embed_join_k(const EmbedBwdArgs
   const auto* a = kernel_args<EmbedBwdArgs>();
   const int64_t C = a->C, T = a->T;
   const int64_t group = static_cast<int64_t>(blockIdx.x) * (kThreads >> shift) + (threadIdx.x >> shift);
-  const Run run = columns_of(threadIdx.x & ((1u << shift) - 1), shift, C);
+  const Run run = columns_of(blockIdx.y, threadIdx.x & ((1u << shift) - 1), shift, C);
   const int64_t lo = group * length, hi = lo + length;
   if (hi >= T || run.lo == 8) return;
   const uint32_t k = keys[hi - 1];
@@ -529,7 +531,7 @@ hipError_t launch_sums(const EmbedBwdArgs& a, int shift, const uint32_t* keys, c
   const int64_t runs = (a.C + 7) / 8, length = embed_chunk(a.T), group = length * (kSumThreads >> shift);
   const int64_t groups = (a.T + group - 1) / group;
   hipLaunchKernelGGL((echo_embed_sum_k<O, E, WAVE>),
-                     dim3(static_cast<unsigned>(groups), static_cast<unsigned>((runs + (1 << shift) - 1) >> shift)),
+                     dim3(static_cast<unsigned>((runs + (1 << shift) - 1) >> shift), static_cast<unsigned>(groups)),
                      dim3(kSumThreads), 0, s, a, shift, static_cast<int>(length), keys, order, part);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || groups == 1) return e;
