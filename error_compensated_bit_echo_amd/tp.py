@@ -629,10 +629,10 @@ class TPMLPStack:
 
 def train_step(model: TPMLPStack, group: EchoGroup, x0, target, weights8=None, max_norm=None):
     """One forward + backward; returns (loss, dL/dx0, [dL/dW...]).  ``x0``: the residual
-    stream, or tokens (dL/dx0 is None).  ``weights8``: the weights in 8 bits
-    (quantize_weights), for several steps before they change.  ``max_norm``: the gradients
-    of the parameters are clipped to that norm together, and the norm before is returned too,
-    as a fourth value."""
+    stream (the gradients of a vocabulary's tables are zeros), or tokens (dL/dx0 is None).
+    ``weights8``: the weights in 8 bits (quantize_weights), for several steps before they
+    change.  ``max_norm``: the gradients of the parameters are clipped to that norm together,
+    and the norm before is returned too, as a fourth value."""
     import torch
 
     group.reset()
@@ -646,6 +646,7 @@ def train_step(model: TPMLPStack, group: EchoGroup, x0, target, weights8=None, m
     loss.backward()
     if model.rng is not None and model.training:
         model.rng[1] += model.L  # the next step draws other masks
-    grads = [p.grad.detach() for p in model.parameters()]
+    # a parameter without a part in the pass: the tables beside a residual stream
+    grads = [torch.zeros_like(p) if p.grad is None else p.grad.detach() for p in model.parameters()]
     result = loss.detach(), None if x.grad is None else x.grad.detach(), grads
     return result if max_norm is None else result + (clip_grads(grads, max_norm),)

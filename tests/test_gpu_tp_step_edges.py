@@ -1,0 +1,39 @@
+"""The tensor-parallel stack's options around its blocks at the edges of what they take, on the GPU."""
+import pytest
+
+pytestmark = pytest.mark.gpu
+
+T, H, F, P, LAYERS, VOCAB = 96, 160, 256, 2, 2, 101
+
+
+@pytest.fixture(scope="module")
+def tp(cuda):
+    from error_compensated_bit_echo_amd import tp
+    return tp
+
+
+def normal(seed, *shapes):
+    import torch
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    return [torch.randn(s, generator=g, device="cuda") for s in shapes]
+
+
+@pytest.mark.parametrize("product", ["f32", "fp8"])
+@pytest.mark.parametrize("max_norm", [None, 0.01])
+def test_step_on_a_residual_stream_of_a_stack_with_a_vocabulary(cuda, tp, product, max_norm):
+    """The tables take no part: the step is that of the stack without them, their gradients zeros."""
+    import torch
+    x0, target = normal(1, (T, H), (T, H))
+    group = tp.EchoGroup(P, T * H, device=cuda)
+    kw = dict(seed=5, device=cuda, product=product, block_norms=True)
+    plain, vocab = tp.TPMLPStack(LAYERS, H, F, P, **kw), tp.TPMLPStack(LAYERS, H, F, P, vocab=VOCAB, **kw)
+    want = tp.train_step(plain, group, x0, target, max_norm=max_norm)
+    got = tp.train_step(vocab, group, x0, target, max_norm=max_norm)
+    assert torch.equal(want[0], got[0]) and torch.equal(want[1], got[1])
+    assert len(got[2]) == len(vocab.parameters()) == len(want[2]) + P
+    assert all(torch.equal(a, b) for a, b in zip(want[2], got[2]))
+    for g, table in zip(got[2][-P:], vocab.tables):
+        assert g.shape == table.shape and not g.any()
+    if max_norm is not None:  # zeros add nothing to the norm
+        assert torch.equal(want[3], got[3])
