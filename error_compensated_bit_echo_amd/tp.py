@@ -392,7 +392,7 @@ def _fns():
         def backward(ctx, grad):
             (tokens,) = ctx.saved_tensors
             d = [torch.empty(shape, dtype=dtype, device=grad.device) for shape, dtype in ctx.like]
-            B.echo_embed_backward(grad.contiguous().view(tokens.numel(), -1), tokens, d, scale=ctx.scale)
+            B.echo_embed_backward(grad.contiguous().view(tokens.numel(), grad.shape[-1]), tokens, d, scale=ctx.scale)
             return (None, None, None) + tuple(d)
 
     return (ReduceForward, ReduceBackward, RowParallelEcho, ColumnParallelEcho, RowParallelFp8, ColumnParallelFp8, DropoutAdd,

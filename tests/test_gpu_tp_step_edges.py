@@ -37,3 +37,14 @@ def test_step_on_a_residual_stream_of_a_stack_with_a_vocabulary(cuda, tp, produc
         assert g.shape == table.shape and not g.any()
     if max_norm is not None:  # zeros add nothing to the norm
         assert torch.equal(want[3], got[3])
+
+
+@pytest.mark.parametrize("shape", [(0,), (3, 0)])
+def test_embedding_of_no_tokens(cuda, tp, shape):
+    import torch
+    tables = [t.requires_grad_() for t in normal(2, *[(7, H)] * P)]
+    group = tp.EchoGroup(P, 0, mode="exact", device=cuda)
+    x = tp.vocab_embed(group, tables, torch.zeros(shape, dtype=torch.long, device=cuda), 2.0)
+    assert x.shape == shape + (H,)
+    x.sum().backward()
+    assert all(t.grad.shape == t.shape and not t.grad.any() for t in tables)

@@ -27,3 +27,24 @@ def test_step_on_a_residual_stream_of_a_stack_with_a_vocabulary(layers):
     assert all(torch.equal(a, b) for a, b in zip(grads, grads2))
     for g, table in zip(grads2[-P:], vocab.tables):
         assert g.shape == table.shape and g.dtype == table.dtype and not g.requires_grad and not g.any()
+
+
+@pytest.mark.parametrize("shape", [(0,), (3, 0)])
+def test_embedding_of_no_tokens(monkeypatch, shape):
+    """Both directions around the kernels, which stand-ins replace here."""
+    import torch
+    asked = []
+
+    def backward(dout, tokens, dtables, scale=1.0):
+        asked.append((tuple(dout.shape), tuple(tokens.shape)))
+        for d in dtables:
+            d.zero_()
+
+    monkeypatch.setattr(tp.B, "echo_embed", lambda tables, tokens, out, scale=1.0: out)
+    monkeypatch.setattr(tp.B, "echo_embed_backward", backward)
+    tables = [torch.randn(4, H, requires_grad=True) for _ in range(P)]
+    x = tp.vocab_embed(tp.EchoGroup(P, 0, mode="exact", device="cpu"), tables, torch.zeros(shape, dtype=torch.long), 2.0)
+    assert x.shape == shape + (H,)
+    x.sum().backward()
+    assert asked == [((0, H), shape)]
+    assert all(t.grad.shape == t.shape and not t.grad.any() for t in tables)
