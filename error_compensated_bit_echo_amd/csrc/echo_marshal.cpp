@@ -12,6 +12,7 @@
 #include <ATen/ops/empty.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <optional>
 #include <string>
 #include <vector>
 
@@ -402,6 +403,21 @@ void* workspace_of(PyObject* given, PyObject* stream, size_t need, const Device&
   return owned->data_ptr();
 }
 
+// Tells autograd that a call wrote into a tensor: a graph that saved it from before then
+// refuses its backward pass rather than differentiate with the new values.  Inference
+// tensors have no version to move.
+void wrote(const at::Tensor& t) {
+  if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
+}
+
+void wrote(PyObject* o) {
+  if (o != Py_None) wrote(THPVariable_Unpack(o));
+}
+
+void wrote(const Items& x) {
+  for (Py_ssize_t i = 0; i < x.size(); ++i) wrote(x[i]);
+}
+
 struct Block {
   echo_block c{};
   int64_t rows = 0, cols = 0;
@@ -439,9 +455,11 @@ PyObject* block_norm(PyObject*, PyObject* const* args, Py_ssize_t n) {
     b.c.y_dtype = args[3] != Py_None ? my.type : mx.type;
     b.c.a_dtype = args[2] != Py_None ? ma.type : mx.type;
     const OnDevice on(dev.index);
-    return answer(echo_block_norm(&b.c, mx.p, mx.ld, my.p, my.ld, mo.p, mo.ld, ma.p, ma.ld,
-                                  stream_of(args[11], args[12], dev.index)),
-                  "echo_block_norm");
+    const echo_status s = echo_block_norm(&b.c, mx.p, mx.ld, my.p, my.ld, mo.p, mo.ld, ma.p, ma.ld,
+                                          stream_of(args[11], args[12], dev.index));
+    if (s == ECHO_OK)
+      for (int i : {1, 2}) wrote(args[i]);
+    return answer(s, "echo_block_norm");
   });
 }
 
@@ -475,10 +493,12 @@ PyObject* block_norm_backward(PyObject*, PyObject* const* args, Py_ssize_t n) {
     size_t bytes = 0;
     const size_t need = echo_block_norm_workspace(b.rows, b.cols, b.c.gate != nullptr ? b.c.gate_rows : 0);
     void* ws = workspace_of(args[16], args[17], need, dev, &owned, &bytes);
-    return answer(echo_block_norm_backward(&b.c, mo.p, mo.ld, my.p, my.ld, mdo.p, mdo.ld, mda.p, mda.ld, mdx.p, mdx.ld,
-                                           mdy.p, mdy.ld, dgate, ldg, dw_post, dw_pre, ws, bytes,
-                                           stream_of(args[17], args[18], dev.index)),
-                  "echo_block_norm_backward");
+    const echo_status s = echo_block_norm_backward(&b.c, mo.p, mo.ld, my.p, my.ld, mdo.p, mdo.ld, mda.p, mda.ld, mdx.p, mdx.ld,
+                                                   mdy.p, mdy.ld, dgate, ldg, dw_post, dw_pre, ws, bytes,
+                                                   stream_of(args[17], args[18], dev.index));
+    if (s == ECHO_OK)
+      for (int i : {3, 5, 6, 7, 8}) wrote(args[i]);
+    return answer(s, "echo_block_norm_backward");
   });
 }
 
@@ -515,10 +535,11 @@ PyObject* clip(PyObject* const* args, bool scale) {
     dev.on(norm, "norm");
     if (norm.scalar_type() != at::kFloat || norm.numel() != 1) refuse(ECHO_ERR_ARG, "norm: one element of float32 expected");
     Tensors g, o;
+    std::optional<Items> to_items;
     tensor_list(&g, G, &dev, "grads");
     const int64_t count = static_cast<int64_t>(g.p.size());
     if (scale && args[3] != Py_None) {
-      const Items O(args[3], "out");
+      const Items& O = to_items.emplace(args[3], "out");
       if (O.size() != G.size()) refuse(ECHO_ERR_ARG, "out: as many tensors as gradients expected");
       tensor_list(&o, O, &dev, "out");
       for (Py_ssize_t i = 0; i < O.size(); ++i) {
@@ -533,11 +554,18 @@ PyObject* clip(PyObject* const* args, bool scale) {
     void* ws = workspace_of(args[2], stream, echo_clip_workspace(count), dev, &owned, &bytes);
     float* to = static_cast<float*>(norm.data_ptr());
     const echo_stream_t s = stream_of(stream, current, dev.index);
-    if (!scale)
-      return answer(echo_grad_norm(g.p.data(), g.n.data(), g.type.data(), count, to, ws, bytes, s), "echo_grad_norm");
-    return answer(echo_clip_grads(g.p.data(), (args[3] != Py_None ? o : g).p.data(), g.n.data(), g.type.data(), count,
-                                  number(args[4]), to, ws, bytes, s),
-                  "echo_clip_grads");
+    if (!scale) {
+      const echo_status e = echo_grad_norm(g.p.data(), g.n.data(), g.type.data(), count, to, ws, bytes, s);
+      if (e == ECHO_OK) wrote(norm);
+      return answer(e, "echo_grad_norm");
+    }
+    const echo_status e = echo_clip_grads(g.p.data(), (args[3] != Py_None ? o : g).p.data(), g.n.data(), g.type.data(), count,
+                                          number(args[4]), to, ws, bytes, s);
+    if (e == ECHO_OK) {
+      wrote(norm);
+      wrote(to_items ? *to_items : G);
+    }
+    return answer(e, "echo_clip_grads");
   });
 }
 
@@ -576,10 +604,11 @@ PyObject* embed(PyObject*, PyObject* const* args, Py_ssize_t n) {
     if (o.rows != tokens.numel() || o.cols != e.cols)
       refuse(ECHO_ERR_ARG, "out must be [" + std::to_string(tokens.numel()) + ", " + std::to_string(e.cols) + "]");
     const OnDevice on(dev.index);
-    return answer(echo_embed(e.ptr, tokens.data_ptr(), o.ptr, P, e.rows, e.cols, e.s0, o.rows, o.s0, elem_type(e.type, "tables"),
-                             elem_type(o.type, "out"), wide, whole(args[4]), number(args[3]),
-                             stream_of(args[5], args[6], dev.index)),
-                  "echo_embed");
+    const echo_status s = echo_embed(e.ptr, tokens.data_ptr(), o.ptr, P, e.rows, e.cols, e.s0, o.rows, o.s0,
+                                     elem_type(e.type, "tables"), elem_type(o.type, "out"), wide, whole(args[4]), number(args[3]),
+                                     stream_of(args[5], args[6], dev.index));
+    if (s == ECHO_OK) wrote(O);
+    return answer(s, "echo_embed");
   });
 }
 
@@ -602,10 +631,11 @@ PyObject* embed_backward(PyObject*, PyObject* const* args, Py_ssize_t n) {
     at::Tensor owned;
     size_t bytes = 0;
     void* ws = workspace_of(args[5], args[6], echo_embed_workspace(d.rows, d.cols), dev, &owned, &bytes);
-    return answer(echo_embed_backward(d.ptr[0], tokens.data_ptr(), e.ptr, P, e.rows, e.cols, e.s0, d.rows, d.s0,
-                                      elem_type(d.type, "dout"), elem_type(e.type, "dtables"), wide, whole(args[4]),
-                                      number(args[3]), ws, bytes, stream_of(args[6], args[7], dev.index)),
-                  "echo_embed_backward");
+    const echo_status s = echo_embed_backward(d.ptr[0], tokens.data_ptr(), e.ptr, P, e.rows, e.cols, e.s0, d.rows, d.s0,
+                                              elem_type(d.type, "dout"), elem_type(e.type, "dtables"), wide, whole(args[4]),
+                                              number(args[3]), ws, bytes, stream_of(args[6], args[7], dev.index));
+    if (s == ECHO_OK) wrote(E);
+    return answer(s, "echo_embed_backward");
   });
 }
 
