@@ -357,8 +357,9 @@ void* weight(const at::Tensor* t, int64_t cols, at::ScalarType* type, Device* de
   return t->data_ptr();
 }
 
-// A gate [cols] or [gate_rows, cols] with contiguous rows, or none.
-void* gate_of(const at::Tensor* t, int64_t cols, int64_t* rows, int64_t* ld, at::ScalarType* type, Device* dev,
+// A gate [cols] or [gate_rows, cols] with contiguous rows, or none.  One without rows goes
+// with no rows of the stream (`of`): a gate per token of no tokens.
+void* gate_of(const at::Tensor* t, int64_t of, int64_t cols, int64_t* rows, int64_t* ld, at::ScalarType* type, Device* dev,
               const char* what) {
   if (t == nullptr) return nullptr;
   dev->on(*t, what);
@@ -369,7 +370,9 @@ void* gate_of(const at::Tensor* t, int64_t cols, int64_t* rows, int64_t* ld, at:
   *type = t->scalar_type();
   *rows = t->dim() == 2 ? t->size(0) : 1;
   *ld = t->dim() == 2 ? t->stride(0) : cols;
-  return t->data_ptr();
+  if (*rows > 0) return address(*t);
+  if (of > 0) refuse(ECHO_ERR_SHAPE, std::string(what) + ": no rows");
+  return nullptr;
 }
 
 double number(PyObject* o) {
@@ -426,7 +429,7 @@ struct Block {
 
 // args: gate, w_post, w_pre, post_norm, residual_scale, weight_offset, eps
 void block_params(Block* b, PyObject* const* args, Device* dev) {
-  b->c.gate = gate_of(optional_tensor(args[0], "gate"), b->cols, &b->c.gate_rows, &b->c.ld_gate, &b->params, dev, "gate");
+  b->c.gate = gate_of(optional_tensor(args[0], "gate"), b->rows, b->cols, &b->c.gate_rows, &b->c.ld_gate, &b->params, dev, "gate");
   b->c.w_post = weight(optional_tensor(args[1], "w_post"), b->cols, &b->params, dev, "w_post");
   b->c.w_pre = weight(optional_tensor(args[2], "w_pre"), b->cols, &b->params, dev, "w_pre");
   b->c.post_norm = truth(args[3]);
@@ -481,7 +484,7 @@ PyObject* block_norm_backward(PyObject*, PyObject* const* args, Py_ssize_t n) {
       refuse(ECHO_ERR_DTYPE, "a gradient must be of the type of what it is the gradient of");
     block_params(&b, args + 9, &dev);
     int64_t gate_rows = b.c.gate_rows, ldg = 0;
-    void* dgate = gate_of(optional_tensor(args[6], "dgate"), b.cols, &gate_rows, &ldg, &b.params, &dev, "dgate");
+    void* dgate = gate_of(optional_tensor(args[6], "dgate"), b.rows, b.cols, &gate_rows, &ldg, &b.params, &dev, "dgate");
     if (dgate != nullptr && gate_rows != b.c.gate_rows) refuse(ECHO_ERR_ARG, "dgate: the gate's shape expected");
     void* dw_post = weight(optional_tensor(args[7], "dw_post"), b.cols, &b.params, &dev, "dw_post");
     void* dw_pre = weight(optional_tensor(args[8], "dw_pre"), b.cols, &b.params, &dev, "dw_pre");
