@@ -627,7 +627,8 @@ PyObject* embed_backward(PyObject*, PyObject* const* args, Py_ssize_t n) {
     const int32_t wide = token_bytes(tokens, &dev);
     Mats d;
     take(&d, 0, dout, &dev, "dout");
-    if (d.cols > 1 && d.s1 != 1) refuse(ECHO_ERR_ARG, "dout must have contiguous rows");
+    // the strides of no rows say nothing (those of an expanded gradient are 0)
+    if (d.rows > 0 && d.cols > 1 && d.s1 != 1) refuse(ECHO_ERR_ARG, "dout must have contiguous rows");
     if (d.rows != tokens.numel() || d.cols != e.cols)
       refuse(ECHO_ERR_ARG, "dout must be [" + std::to_string(tokens.numel()) + ", " + std::to_string(e.cols) + "]");
     const OnDevice on(dev.index);
