@@ -117,12 +117,6 @@ __device__ __forceinline__ void load_run(int elem, const void* base, int64_t at,
   else load_run<kElemF16>(base, at, n, v);
 }
 
-__device__ __forceinline__ void store_run(int elem, void* base, int64_t at, int n, const float v[8]) {
-  if (elem == kElemF32) store_run<kElemF32>(base, at, n, v);
-  else if (elem == kElemBf16) store_run<kElemBf16>(base, at, n, v);
-  else store_run<kElemF16>(base, at, n, v);
-}
-
 // v as it reads back from an element of the type.
 template <int E>
 __device__ __forceinline__ float stored(float v) {
