@@ -396,27 +396,30 @@ def tp_report(torch, dev) -> dict:
     per direction) with Echo, Echo without compensation and exact all-reduces
     (fp32 products), and with Echo and the row-parallel products in bfloat16 on
     libecho's kernel, written out or with stage 1 fused into them, or with every
-    product in 8-bit floating point; errors of the loss and the gradients against the exact fp32 step, and step times (median
-    of three steps after a warm-up step)."""
+    product in 8-bit floating point, and with learned block norms, an embedding of 65536
+    rows in front and clipped gradients around those; errors of the loss and the gradients
+    against the exact fp32 step, and step times (median of three steps after a warm-up
+    step)."""
     from error_compensated_bit_echo_amd import tp
 
-    T, H, F, P, L = 2048, 4096, 16384, 4, 8
+    T, H, F, P, L, V = 2048, 4096, 16384, 4, 8, 65536
     model = tp.TPMLPStack(L, H, F, P, seed=21, device=dev)
     g = torch.Generator(device=dev)
     g.manual_seed(22)
     x0 = torch.randn(T, H, generator=g, device=dev)
     target = torch.randn(T, H, generator=g, device=dev)
+    tokens = torch.randint(0, V, (T,), generator=g, device=dev)
     res, ms = {}, {}
 
-    def timed(m, group):
+    def timed(m, group, x0=x0, **kw):
         """One warm-up step, then the median of three timed steps."""
-        tp.train_step(m, group, x0, target)
+        tp.train_step(m, group, x0, target, **kw)
         torch.cuda.synchronize()
         times = []
         for _ in range(3):
             a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
             a.record()
-            out = tp.train_step(m, group, x0, target)
+            out = tp.train_step(m, group, x0, target, **kw)
             b.record()
             torch.cuda.synchronize()
             times.append(a.elapsed_time(b))
@@ -443,6 +446,14 @@ def tp_report(torch, dev) -> dict:
             res[name], ms[name] = timed(m2, tp.EchoGroup(P, T * H, mode="echo", device=dev, sender_feedback=True,
                                                          state_bf16=True))
         del m2
+    # what stands around the blocks, on 8-bit products
+    group = tp.EchoGroup(P, T * H, mode="echo", device=dev)
+    m2 = tp.TPMLPStack(L, H, F, P, seed=21, device=dev, product="fp8", block_norms=True)
+    ms["echo_fp8_block_norms"] = timed(m2, group)[1]
+    m2 = tp.TPMLPStack(L, H, F, P, seed=21, device=dev, product="fp8", block_norms=True, vocab=V)
+    ms["echo_fp8_block_norms_vocab"] = timed(m2, group, tokens)[1]
+    ms["echo_fp8_block_norms_vocab_clipped"] = timed(m2, group, tokens, max_norm=1.0)[1]
+    del m2
 
     def rel(x, y):
         return float((x - y).float().norm() / y.float().norm())
