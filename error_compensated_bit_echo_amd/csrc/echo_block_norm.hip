@@ -211,8 +211,9 @@ hipError_t launch_block_norm(const BlockNormArgs& a, Elem x, Elem y, Elem out_a,
   return with_types(x, y, out_a, [&](auto X, auto Y, auto A) {
     const int64_t per = 8 * kMaxThreads;
     // two runs to a thread where there are rows for several workgroups to a CU (16384 x 8192
-    // bfloat16: 207 us, one run 215; 65536 x 2048: 184 and 192), one where a row should be as
-    // short as it can (64 x 4096: 4.0 us, two runs 4.5), or is short (262144 x 512: 181 and 220)
+    // bfloat16: 195 us, one run 199, and 197 and 204 with results that stay in the caches; 65536 x
+    // 2048: 182 and 186), one where there are few (2048 x 4096: 12.8 us, two runs 13.1), or where a
+    // row is short (262144 x 512: 171 and 206)
     if (a.p.C >= 8 && a.p.C <= per) {
       if (a.p.C <= 1024 || a.p.R <= 2048) return launch_runs<X(), Y(), A(), 1, 1024, true>(a, s);
       const int64_t x = elem_size(X()), y = a.y != nullptr ? x + elem_size(Y()) : 0;

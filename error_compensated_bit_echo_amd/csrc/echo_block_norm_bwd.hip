@@ -5,13 +5,13 @@
 //   dw_pre = sum over rows of da s rs,  dw_post = sum of dn y ry,  dgate = sum over the gate's rows of t n.
 // sum s^2, sum u s and sum y^2 need nothing but the inputs, so they are one reduction and
 // no statistics of the forward pass are kept; sum v y needs t, which is the second.  A
-// workgroup takes consecutive rows and sums its columns in registers; the workgroups' sums
-// go to the workspace and are added in order by a second kernel, so the result does not
-// depend on timing.
+// workgroup takes every n-th row of a gate's (all rows without one), or the rows of whole
+// gates, and sums its columns in registers; the workgroups' sums go to the workspace and are
+// added in order by a second kernel, so the result does not depend on timing.
 //
 // As many workgroups as the CUs hold, each with its next row's inputs in flight while it works
 // on one; the parameters' factors wait in LDS, which leaves the registers (127 of 128) to the
-// sums and the inputs. 16384 x 8192 bfloat16 takes 297 us (5.4 TB/s of what it has to move), the
+// sums and the inputs. 16384 x 8192 bfloat16 takes 296 us (5.4 TB/s of what it has to move), the
 // kernel 286 and the join 6; the vector units issue in 56 % of its cycles, so that every
 // instruction a row counts: with the exact root and division it took 345, with a 64-bit
 // division a row 309. 2048 x 4096 fp32: 57 us, 10 of them the column sums' way through memory.

@@ -13,8 +13,9 @@
 // its end into the workspace; a last launch adds those up along the chunks.  So a token
 // that comes up ten thousand times costs as much as ten thousand different ones.
 //
-// Bound by the memory: 16384 tokens, 4 tables of 16384 x 4096 fp32, take 238 to 259 us, 5.6 to 5.2 TB/s:
-// the zeros 164 (the sort of 31 us behind them), the sums 70 to 83, the join 7. 16384 tokens of
+// Bound by the memory: 16384 tokens, 4 tables of 16384 x 4096 fp32, take 259 us on inputs that change from
+// call to call, 5.2 TB/s, and 238 on the same again: the zeros 165 (the sort of 31 us behind them),
+// the sums 67 (their gradients in the last-level cache) to 83, the join 7. 16384 tokens of
 // a table of 1000 x 512 take 48 us, where the sort shows.
 #include "echo_row.h"
 

@@ -470,7 +470,8 @@ def block_norm(x, y=None, gate=None, w_post=None, w_pre=None, *, post_norm: bool
 def vocab_embed(group: "EchoGroup", tables, tokens, scale: float = 1.0):
     """The embedding [.., H] of ``tokens`` from P tables [rows, H] that hold consecutive
     stretches of the vocabulary: their partials through Echo's forward state (fp32),
-    differentiable in the tables.  Tokens outside the vocabulary give zeros."""
+    differentiable in the tables, which are float32 or bfloat16 (the partials are bfloat16,
+    and float16 does not go with it).  Tokens outside the vocabulary give zeros."""
     global _FNS
     if _FNS is None:
         _FNS = _fns()

@@ -426,7 +426,8 @@ echo_status echo_dropout_add(const void* x, const void* residual, void* out, int
  * launch, no allocation on the device), but a call may launch several kernels
  * and some take a workspace, which the caller owns and which one call at a time
  * may use.  fp32 goes with either 16-bit type in one call; bfloat16 and fp16 do
- * not go together (ECHO_ERR_DTYPE), except in the list of a clipping call.
+ * not go together (ECHO_ERR_DTYPE), except in the list of a clipping call and
+ * between a block norm's parameters and its matrices.
  * Results do not depend on timing; non-finite values are specified. */
 
 /* The end of one block and the start of the next, for a residual stream x and
@@ -467,7 +468,8 @@ typedef struct {
  * out (where y has a post-norm) and of a NaN; an infinity gives NaN in its own
  * place and 0 in the others.
  * ld*: elements between rows, any alignment of the element type.  out may be x
- * itself (same pointer and pitch); outputs overlap nothing else.  One launch.
+ * itself (same pointer and pitch); outputs overlap nothing else.  One launch for
+ * every 2^32 threads, of which a row takes 64 to 1024.
  * Errors: ECHO_ERR_ARG (null or misaligned pointer, parameters without y, an
  * overlap), ECHO_ERR_SHAPE, ECHO_ERR_DTYPE, ECHO_ERR_HIP. */
 echo_status echo_block_norm(const echo_block* b, const void* x, int64_t ldx, const void* y, int64_t ldy, void* out,
@@ -490,7 +492,8 @@ size_t echo_block_norm_workspace(int64_t rows, int64_t cols, int64_t gate_rows);
  * Sums over rows are fp32, in an order that the sizes fix; every output is
  * rounded once.  dx may be dout itself.  With no rows, gradients of parameters
  * are zeros.  workspace: echo_block_norm_workspace bytes, 16-byte aligned.  One to
- * three launches.  Errors as above, and ECHO_ERR_WORKSPACE. */
+ * three launches, and one more for every further 2^32 threads over rows of more
+ * than 8192 columns.  Errors as above, and ECHO_ERR_WORKSPACE. */
 echo_status echo_block_norm_backward(const echo_block* b, const void* out, int64_t ldo, const void* y, int64_t ldy,
                                      const void* dout, int64_t lddo, const void* da, int64_t ldda, void* dx, int64_t lddx,
                                      void* dy, int64_t lddy, void* dgate, int64_t ld_dgate, void* dw_post, void* dw_pre,

@@ -48,3 +48,20 @@ def test_embedding_of_no_tokens(cuda, tp, shape):
     assert x.shape == shape + (H,)
     x.sum().backward()
     assert all(t.grad.shape == t.shape and not t.grad.any() for t in tables)
+
+
+def test_embedding_types(cuda, tp):
+    """float32 and bfloat16 tables go with the bfloat16 partials, float16 ones do not."""
+    import torch
+    tokens = torch.arange(T, device=cuda) % 14
+    group = tp.EchoGroup(P, T * H, mode="exact", device=cuda)
+    for dtype in (torch.float32, torch.bfloat16):
+        tables = [t.to(dtype).requires_grad_() for t in normal(3, *[(7, H)] * P)]
+        x = tp.vocab_embed(group, tables, tokens)
+        assert torch.equal(x, torch.cat(tables)[tokens].bfloat16().float())
+        x.backward(torch.ones_like(x))
+        # every token comes up 6 or 7 times
+        assert torch.equal(torch.cat([t.grad for t in tables]),
+                           torch.bincount(tokens, minlength=14)[:, None].expand(14, H).to(dtype))
+    with pytest.raises(tp.B.EchoError):
+        tp.vocab_embed(group, [t.half() for t in normal(3, *[(7, H)] * P)], tokens)
